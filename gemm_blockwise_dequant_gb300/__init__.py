@@ -27,6 +27,9 @@ __all__ = [
     "qmoe_ragged_mm_workspace_bytes", "qg_gather_block_quantized", "QG_WF_U2", "QG_WF_U4", "QG_WF_U8", "QG_WF_E4M3",
     "qgemm_nbits_packed_zp", "qgemm_nbits_packed_zp_workspace_bytes", "qg_test_bounded_wait",
     "qg_test_gemv_plan", "qmoe_ragged_mm_device_offsets", "qmoe_ragged_mm_device_offsets_workspace_bytes",
+    "qg_lora_apply", "qg_lora_apply_workspace_bytes", "qg_lora_grad", "qg_lora_grad_workspace_bytes",
+    "qgemm_nbits_dgrad", "qgemm_nbits_uniform_zp_dgrad", "qgemm_codebook4_dgrad", "qgemm_dgrad_workspace_bytes",
+    "QGGradList", "qg_clip_grad_norm", "qg_clip_grad_norm_workspace_bytes",
 ]
 
 QG_OK, QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_CUDA, QG_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3, 4
@@ -55,7 +58,7 @@ def _status_name(s):
             4: "QG_ERR_WORKSPACE_TOO_SMALL"}.get(s, "status %d" % s)
 
 
-_P, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_P, _I, _SZ, _F, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64
 _SIGS = {
     "qgemm_nbits": ([_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P], _I),
     "qgemm_nbits_uniform_zp": ([_P, _I, _P, _P, _F, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P], _I),
@@ -81,6 +84,19 @@ _SIGS = {
     "qmoe_ragged_mm_workspace_bytes": ([_I, _P, _I, _I, _I, _I, _I], _SZ),
     "qmoe_ragged_mm_device_offsets": ([_P, _I, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _SZ, _P, _P], _I),
     "qmoe_ragged_mm_device_offsets_workspace_bytes": ([_I], _SZ),
+    "qg_lora_apply_workspace_bytes": ([_I, _I, _I], _SZ),
+    "qg_lora_apply": ([_P, _I, _L, _P, _P, _I, _P, _P, _I, _P, _I, _I, _P, _I, _L, _P, _I, _L, _P, _I, _I, _I, _P, _P,
+                       _SZ, _P], _I),
+    "qg_lora_grad_workspace_bytes": ([_I, _I, _I, _I, _I, _I], _SZ),
+    "qg_lora_grad": ([_P, _I, _L, _P, _L, _P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _P, _P, _L, _P, _P, _I, _I, _I, _I,
+                      _I, _P, _P, _SZ, _P], _I),
+    "qgemm_dgrad_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
+    "qgemm_nbits_dgrad": ([_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P], _I),
+    "qgemm_nbits_uniform_zp_dgrad": ([_P, _I, _P, _P, _F, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P], _I),
+    "qgemm_codebook4_dgrad": ([_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _SZ, _P], _I),
+    "qg_grad_list_init": ([_P, _I, _P], _I),
+    "qg_clip_grad_norm_workspace_bytes": ([_L], _SZ),
+    "qg_clip_grad_norm": ([_P, _I, _L, _F, _F, _P, _P, _SZ, _P], _I),
     "qg_read_device_fault": ([_P], _I),
     "qg_test_bounded_wait": ([_I, ctypes.c_uint, _P, _P], _I),
     "qg_test_gemv_plan": ([_I, _I, _I, _I, _I, _P], _I),
@@ -372,6 +388,206 @@ def qg_gather_block_quantized(indices, W, scales, zero_points, Y, *, w_format, b
                                         W.shape[0], D, block_size, _ptr(Y), _dtype_code(Y), _ptr(status),
                                         _stream(stream))
     return s if raw else _check(s, "qg_gather_block_quantized")
+
+
+# ---------------------------------------------------------------- adapters and fine-tuning
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_and_workspace(need, workspace, t, stream):
+    """(raw stream, workspace address, its bytes, the workspace): on `stream`, or on the device's current one.
+    A workspace made here is not given away again before the work on `stream` that uses it is done."""
+    torch = _torch()
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace, nbytes = torch.empty(need, dtype=torch.uint8, device=t.device), need
+        if stream is not None:
+            workspace.record_stream(stream)
+    else:
+        nbytes = 0
+    raw = torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+    return raw, _addr(workspace), nbytes, workspace
+
+
+def _rows2d(t, cols, what):
+    """The distance between the rows of a 2-D tensor whose rows are contiguous (the C calls take no other)."""
+    if t.dim() != 2 or t.shape[1] != cols or (t.stride(1) != 1 and cols > 1):
+        raise ValueError("%s: a 2-D tensor with rows of %d contiguous values is wanted" % (what, cols))
+    ld = t.stride(0)
+    return ld if ld >= cols or t.shape[0] > 1 else cols  # the stride of a single row says nothing
+
+
+def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter):
+    torch = _torch()
+    na, r, K = A.shape
+    N = B.shape[1]
+    if B.shape[0] != na or B.shape[2] != r or A.dtype != B.dtype or not A.is_contiguous() or not B.is_contiguous():
+        raise ValueError("A [adapters, rank, K] and B [adapters, N, rank] of one type, contiguous, are wanted")
+    if scaling is not None and (scaling.dtype != torch.float32 or scaling.shape != (na,) or not scaling.is_contiguous()):
+        raise ValueError("scaling: [adapters] float32 is wanted")
+    S = seg_adapter.numel()
+    if seg_offsets.numel() != S + 1 or seg_offsets.dtype != torch.int64 or seg_adapter.dtype != torch.int32 \
+            or not seg_offsets.is_contiguous() or not seg_adapter.is_contiguous():
+        raise ValueError("seg_offsets [requests + 1] int64 and seg_adapter [requests] int32 are wanted")
+    return na, r, K, N, S
+
+
+def qg_lora_apply_workspace_bytes(rows: int, num_segments: int, rank: int) -> int:
+    return lib().qg_lora_apply_workspace_bytes(rows, num_segments, rank)
+
+
+def qg_lora_apply(X, seg_offsets, seg_adapter, A, B, scaling, Y_in, Y, *, V=None, status=None, workspace=None,
+                  stream=None, raw=False):
+    """Y[t] = Y_in[t] + scaling[a] (X[t] A[a]^T) B[a]^T for the rows t of each request, a the request's adapter.
+
+    X: [T, K]; seg_offsets: [S + 1] int64 and seg_adapter: [S] int32, both on the device (request i owns rows
+    seg_offsets[i] .. seg_offsets[i+1]-1; a negative adapter means none); A: [adapters, rank, K]; B: [adapters, N,
+    rank]; scaling: [adapters] float32 or None (1); Y_in: [T, N] in float32 or Y's type, None (zeros) or Y itself;
+    Y: [T, N]; V: [T, rank] float32 that receives X A^T for qg_lora_grad, or None; status: a device int32 or None.
+    X, Y_in and Y may be column slices (rows apart, values contiguous).
+    """
+    na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter)
+    T = X.shape[0]
+    if Y.shape[0] != T or (Y_in is not None and Y_in.shape[0] != T):
+        raise ValueError("X, Y_in and Y: one number of rows is wanted")
+    if V is not None and (V.shape != (T, r) or V.dtype != _torch().float32 or not V.is_contiguous()):
+        raise ValueError("V: [rows, rank] float32 is wanted")
+    L = lib()
+    st, wp, wb, _ = _stream_and_workspace(L.qg_lora_apply_workspace_bytes(T, S, r), workspace, X, stream)
+    s = L.qg_lora_apply(_addr(X), _dtype_code(X), _rows2d(X, K, "X"), _addr(seg_offsets), _addr(seg_adapter), S,
+                        _addr(A), _addr(B), _dtype_code(A), _addr(scaling), na, r, _addr(Y_in),
+                        0 if Y_in is None else _dtype_code(Y_in), 0 if Y_in is None else _rows2d(Y_in, N, "Y_in"),
+                        _addr(Y), _dtype_code(Y), _rows2d(Y, N, "Y"), _addr(V), T, N, K, _addr(status), wp, wb, st)
+    return s if raw else _check(s, "qg_lora_apply")
+
+
+def qg_lora_grad_workspace_bytes(rows: int, num_segments: int, num_adapters: int, rank: int, N: int, K: int) -> int:
+    return lib().qg_lora_grad_workspace_bytes(rows, num_segments, num_adapters, rank, N, K)
+
+
+def qg_lora_grad(dY, X, V, seg_offsets, seg_adapter, A, B, scaling, dX_in, dX, dA, dB, *, accumulate=False, status=None,
+                 workspace=None, stream=None, raw=False):
+    """The backward pass of qg_lora_apply: dX = dX_in + G A with G = scaling dY B, dA = G^T X, dB = scaling dY^T V.
+
+    dY: [T, N] and X: [T, K] of one type; V: [T, rank] float32 from qg_lora_apply; dX_in and dX: [T, K] in X's type
+    (dX_in None for zeros or dX itself; dX None when no gradient of X is wanted); dA and dB: shapes of A and B, in
+    their type or float32, zero for adapters without rows (accumulate: added to what they hold).
+    """
+    na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter)
+    T = X.shape[0]
+    if dY.shape[0] != T or dY.dtype != X.dtype or V.shape != (T, r) or V.dtype != _torch().float32 or not V.is_contiguous():
+        raise ValueError("dY and X of one type and number of rows and V [rows, rank] float32 are wanted")
+    if dA.shape != A.shape or dB.shape != B.shape or dA.dtype != dB.dtype or not dA.is_contiguous() or not dB.is_contiguous():
+        raise ValueError("dA and dB: the shapes of A and B, contiguous and of one type, are wanted")
+    lddx = 0
+    if dX is not None:
+        lddx = _rows2d(dX, K, "dX")
+        for t in (dX, dX if dX_in is None else dX_in):
+            if t.shape[0] != T or t.dtype != X.dtype or _rows2d(t, K, "dX_in") != lddx:
+                raise ValueError("dX_in and dX: X's type and rows, and one distance between rows, are wanted")
+    L = lib()
+    st, wp, wb, _ = _stream_and_workspace(L.qg_lora_grad_workspace_bytes(T, S, na, r, N, K), workspace, X, stream)
+    s = L.qg_lora_grad(_addr(dY), _dtype_code(X), _rows2d(dY, N, "dY"), _addr(X), _rows2d(X, K, "X"), _addr(V),
+                       _addr(seg_offsets), _addr(seg_adapter), S, _addr(A), _addr(B), _dtype_code(A), _addr(scaling), na, r,
+                       _addr(dX_in), _addr(dX), lddx, _addr(dA), _addr(dB), _dtype_code(dA), 1 if accumulate else 0,
+                       T, N, K, _addr(status), wp, wb, st)
+    return s if raw else _check(s, "qg_lora_grad")
+
+
+def qgemm_dgrad_workspace_bytes(dy_dtype: int, M: int, N: int, K: int, bits: int) -> int:
+    return lib().qgemm_dgrad_workspace_bytes(dy_dtype, M, N, K, bits)
+
+
+def _dgrad_sizes(dY, W, params, dX, bits, block_size):
+    M, N = dY.shape
+    K = dX.shape[1]
+    if not dY.is_contiguous() or not dX.is_contiguous() or dX.shape[0] != M or W.shape != (N, K * bits // 8) \
+            or params.shape[0] != N or (block_size > 0 and params.shape[1] != K // block_size):
+        raise ValueError("dY [M, N], W [N, K*bits/8], parameters [N, K/block_size] and dX [M, K], contiguous, are wanted")
+    return M, N, K
+
+
+def qgemm_nbits_dgrad(dY, W, scales, zero_points, dX, *, bits, block_size, workspace=None, stream=None, raw=False):
+    """dX[M,K] = dY[M,N] . dequant(W)[N,K]: the gradient of the activations through the frozen weight of qgemm_nbits."""
+    M, N, K = _dgrad_sizes(dY, W, scales, dX, bits, block_size)
+    L = lib()
+    st, wp, wb, _ = _stream_and_workspace(L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits), workspace, dY, stream)
+    s = L.qgemm_nbits_dgrad(_addr(dY), _dtype_code(dY), _addr(W), _addr(scales), _addr(zero_points), _addr(dX),
+                            _dtype_code(dX), M, N, K, bits, block_size, wp, wb, st)
+    return s if raw else _check(s, "qgemm_nbits_dgrad")
+
+
+def qgemm_nbits_uniform_zp_dgrad(dY, W, scales, uniform_zp, dX, *, bits, block_size, workspace=None, stream=None, raw=False):
+    """As qgemm_nbits_dgrad with every zero point equal to the scalar uniform_zp."""
+    M, N, K = _dgrad_sizes(dY, W, scales, dX, bits, block_size)
+    L = lib()
+    st, wp, wb, _ = _stream_and_workspace(L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits), workspace, dY, stream)
+    s = L.qgemm_nbits_uniform_zp_dgrad(_addr(dY), _dtype_code(dY), _addr(W), _addr(scales), float(uniform_zp), _addr(dX),
+                                       _dtype_code(dX), M, N, K, bits, block_size, wp, wb, st)
+    return s if raw else _check(s, "qgemm_nbits_uniform_zp_dgrad")
+
+
+def qgemm_codebook4_dgrad(dY, W, codebook, absmax, dX, *, block_size, workspace=None, stream=None, raw=False):
+    """dX = dY . (codebook[q] * absmax): the gradient of the activations through the frozen weight of qgemm_codebook4."""
+    M, N, K = _dgrad_sizes(dY, W, absmax, dX, 4, block_size)
+    L = lib()
+    st, wp, wb, _ = _stream_and_workspace(L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, 4), workspace, dY, stream)
+    s = L.qgemm_codebook4_dgrad(_addr(dY), _dtype_code(dY), _addr(W), _addr(codebook), _addr(absmax), _addr(dX),
+                                _dtype_code(dX), M, N, K, block_size, wp, wb, st)
+    return s if raw else _check(s, "qgemm_codebook4_dgrad")
+
+
+class _GradTensor(ctypes.Structure):
+    _fields_ = [("grad", _P), ("out", _P), ("numel", _L), ("first_chunk", _L), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class QGGradList:
+    """The gradient tensors of a step, for qg_clip_grad_norm: made once, used every step.
+
+    It holds the tensors and their addresses on the device, so it is for buffers that stay where they are from
+    step to step.  outs: where the clipped gradients go, each of its gradient's size and type (default: in place).
+    """
+
+    def __init__(self, grads, outs=None):
+        torch = _torch()
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError("outs: one for each gradient is wanted")
+        host = (_GradTensor * max(1, len(grads)))()
+        for h, g, o in zip(host, grads, outs):
+            if not g.is_contiguous() or not o.is_contiguous() or g.numel() != o.numel() or g.dtype != o.dtype:
+                raise ValueError("gradients and outs: contiguous tensors of one size and type are wanted")
+            h.grad, h.out, h.numel, h.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g)
+        chunks = ctypes.c_int64(0)
+        _check(lib().qg_grad_list_init(host, len(grads), ctypes.byref(chunks)), "qg_grad_list_init")
+        self.grads, self.outs, self.count, self.chunks = grads, outs, len(grads), chunks.value
+        device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+        self.table = torch.frombuffer(bytearray(host), dtype=torch.uint8).to(device)
+        self.workspace_bytes = lib().qg_clip_grad_norm_workspace_bytes(self.chunks)
+
+
+def qg_clip_grad_norm_workspace_bytes(chunks: int) -> int:
+    return lib().qg_clip_grad_norm_workspace_bytes(chunks)
+
+
+def qg_clip_grad_norm(grads, max_norm, norm, *, eps=1e-6, workspace=None, stream=None, raw=False):
+    """norm = the 2-norm over all gradients; each out = its gradient * min(1, max_norm / (norm + eps)).
+
+    grads: a QGGradList, or a sequence of tensors (clipped in place; the list is then laid out in every call);
+    norm: a float32 device tensor of one value.
+    """
+    if not isinstance(grads, QGGradList):
+        grads = QGGradList(grads)
+    st, wp, wb, _ = _stream_and_workspace(grads.workspace_bytes, workspace, grads.table, stream)
+    if stream is not None:
+        grads.table.record_stream(stream)
+    s = lib().qg_clip_grad_norm(_addr(grads.table), grads.count, grads.chunks, float(max_norm), float(eps), _addr(norm), wp,
+                                wb, st)
+    return s if raw else _check(s, "qg_clip_grad_norm")
 
 
 def qg_read_device_fault() -> int:

@@ -148,6 +148,58 @@ struct GatherProblem {
 };
 cudaError_t launch_gather(const GatherProblem &g, cudaStream_t s);
 
+// Low-rank adapters (validated requests; qg_lora.cu).
+struct LoraProblem {
+    const int64_t *offs;   // [S + 1] device
+    const int32_t *ids;    // [S] device
+    int S;
+    const void *A, *B;     // [na][r][K], [na][N][r]
+    int w_dtype;
+    const float *scaling;  // [na] or null
+    int na, r;
+    int T, N, K;
+    int *status;
+};
+struct LoraApply {
+    LoraProblem p;
+    const void *X;
+    int x_dtype;
+    int64_t ldx;
+    const void *Yin;       // or null
+    int yin_dtype;
+    int64_t ldyin;
+    void *Y;
+    int y_dtype;
+    int64_t ldy;
+    float *V;              // or null
+};
+struct LoraGrad {
+    LoraProblem p;
+    const void *dY, *X;
+    int x_dtype;
+    int64_t lddy, ldx;
+    const float *V;
+    const void *dXin;      // or null
+    void *dX;              // or null
+    int64_t lddx;
+    void *dA, *dB;
+    int g_dtype, accumulate;
+};
+size_t lora_apply_workspace_bytes(int T, int S, int r);
+cudaError_t lora_apply(const LoraApply &q, void *ws, cudaStream_t s);
+size_t lora_grad_workspace_bytes(int T, int S, int na, int r, int N, int K);
+cudaError_t lora_grad(const LoraGrad &q, void *ws, cudaStream_t s);
+
+// dX = dY . dequant(W) (validated; A is dY [M][N], Y is dX [M][K]; qg_dgrad.cu).
+size_t dgrad_workspace_bytes(int dy_dtype, int M, int N, int K, int bits);
+cudaError_t dgrad(const GemmProblem &p, void *ws, cudaStream_t s);
+
+// Gradient norm and clipping (qg_clip.cu); the list is include/qgemm.h's qg_grad_tensor.
+int64_t clip_chunks(int64_t numel);
+size_t clip_workspace_bytes(int64_t chunks);
+cudaError_t clip_grad_norm(const void *list, int count, int64_t chunks, float max_norm, float eps, float *norm, void *ws,
+                           cudaStream_t s);
+
 // Utility kernels.
 cudaError_t launch_dequant(const GemmProblem &p, float *out, cudaStream_t s);
 cudaError_t launch_uniform_check(const uint16_t *t, size_t n, unsigned *ws, cudaStream_t s);

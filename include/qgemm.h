@@ -426,6 +426,130 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
                               int block_size, void *Y, int y_dtype, int *status_dev, qg_stream_t stream);
 
 /*
+ * Low-rank adapters beside a shared projection, served and trained.  The
+ * source pages have no counterpart: these are additions of this library (the
+ * quantized weight W [N][K] of the entry points above stays frozen; a request
+ * brings an adapter of rank r, A [r][K] and B [N][r], of its own).
+ *
+ * Requests.  The T rows of X are grouped by request: request i owns rows
+ * seg_offsets[i] .. seg_offsets[i+1]-1 and uses adapter seg_adapter[i]
+ * (negative: none).  Both arrays are DEVICE memory, read after the preceding
+ * work on the stream: offs[0] = 0, never decreasing (a request may own no
+ * row), offs[num_segments] <= rows.  Offsets breaking that rule make the call
+ * compute nothing and set *status_dev to 1; an adapter id at or past
+ * num_adapters counts as none and sets it too.  status_dev may be NULL and is
+ * never cleared.  Rows at or past offs[num_segments] are left untouched.
+ *
+ * qg_lora_apply -- for every row t of a request with adapter a
+ *   V[t][j] = sum_k X[t][k] * A[a][j][k]                        (fp32)
+ *   Y[t][n] = round( Y_in[t][n] + scaling[a] * sum_j V[t][j] * B[a][n][j] )
+ * and Y = round(Y_in) for rows of requests without one.
+ *
+ *   X            [rows] rows of K values, ldx values apart; x_dtype
+ *   A, B         [num_adapters][rank][K] and [num_adapters][N][rank]; w_dtype:
+ *                x_dtype, or any type beside fp32 activations
+ *   scaling      [num_adapters] fp32, or NULL (all 1)
+ *   Y_in         [rows] rows of N values, ldy_in apart, y_in_dtype (QG_F32 or
+ *                y_dtype), or NULL (zeros); may be Y itself
+ *   Y            [rows] rows of N values, ldy apart, y_dtype
+ *   V_out        [rows][rank] fp32 or NULL: V, for the backward pass (0 for
+ *                rows without an adapter)
+ *   rank         8 .. 128, a multiple of 8 (pad smaller or mixed ranks with
+ *                zeros); others QG_ERR_UNSUPPORTED
+ *   K            a multiple of 8; X, A and B 16-byte aligned, ldx * the
+ *                element size a multiple of 16.  N and the strides of Y are free.
+ * Sums are fp32 (16-bit operands multiply exactly; with fp32 operands each
+ * value is split in two TF32 terms, dropping less than 2^-21 of a product).
+ * Deterministic.  workspace: at least qg_lora_apply_workspace_bytes(rows,
+ * num_segments, rank) bytes, 16-byte aligned (NULL when that is 0).
+ *
+ * qg_lora_grad -- the backward pass, given dY, X and the V of the forward pass:
+ *   G[t][j]  = scaling[a] * sum_n dY[t][n] * B[a][n][j]         (fp32)
+ *   dX[t][k] = round( dX_in[t][k] + sum_j G[t][j] * A[a][j][k] )
+ *   dA[a][j][k] = sum over the rows t of adapter a of G[t][j] * X[t][k]
+ *   dB[a][n][j] = scaling[a] * sum over those rows of dY[t][n] * V[t][j]
+ *
+ *   dY           [rows] rows of N values, lddy apart, x_dtype (any alignment)
+ *   X, A, B      as above;  V  [rows][rank] fp32
+ *   dX_in, dX    [rows] rows of K values, lddx apart (both), x_dtype; dX may be
+ *                NULL (no gradient of the activations is wanted: A is then not
+ *                read), dX_in may be NULL (zeros) or dX itself
+ *   dA, dB       shapes of A and B; g_dtype: w_dtype or QG_F32; zero for an
+ *                adapter without rows.  accumulate = 1 adds to their contents.
+ *   workspace    at least qg_lora_grad_workspace_bytes(...) bytes, 16-byte aligned
+ */
+size_t qg_lora_apply_workspace_bytes(int rows, int num_segments, int rank);
+int qg_lora_apply(const void *X, int x_dtype, int64_t ldx, const int64_t *seg_offsets, const int32_t *seg_adapter,
+                  int num_segments, const void *A, const void *B, int w_dtype, const float *scaling, int num_adapters,
+                  int rank, const void *Y_in, int y_in_dtype, int64_t ldy_in, void *Y, int y_dtype, int64_t ldy,
+                  float *V_out, int rows, int N, int K, int *status_dev, void *workspace, size_t workspace_bytes,
+                  qg_stream_t stream);
+size_t qg_lora_grad_workspace_bytes(int rows, int num_segments, int num_adapters, int rank, int N, int K);
+int qg_lora_grad(const void *dY, int x_dtype, int64_t lddy, const void *X, int64_t ldx, const float *V,
+                 const int64_t *seg_offsets, const int32_t *seg_adapter, int num_segments, const void *A,
+                 const void *B, int w_dtype, const float *scaling, int num_adapters, int rank, const void *dX_in,
+                 void *dX, int64_t lddx, void *dA, void *dB, int g_dtype, int accumulate, int rows, int N, int K,
+                 int *status_dev, void *workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/*
+ * qgemm_*_dgrad -- the gradient of the activations through a frozen quantized
+ * weight: dX[M][K] = dY[M][N] . dequant(W)[N][K], with W, its parameters, bits
+ * and block_size as in qgemm_nbits / qgemm_nbits_uniform_zp / qgemm_codebook4
+ * (an addition of this library, like the adapters above).
+ *   dY   [M][N] contiguous, dy_dtype;  dX  [M][K] contiguous, dx_dtype; both
+ *        16-byte aligned
+ *   16-bit dY: the weight is rounded to dY's type before the product, as in
+ *   the forward pass; fp32 accumulation, one rounding to dx_dtype.
+ *   workspace: at least qgemm_dgrad_workspace_bytes(dy_dtype, M, N, K, bits)
+ *   bytes, 16-byte aligned (NULL when that is 0).
+ * M == 0 or K == 0 is a no-op; N == 0 writes zeros.
+ */
+size_t qgemm_dgrad_workspace_bytes(int dy_dtype, int M, int N, int K, int bits);
+int qgemm_nbits_dgrad(const void *dY, int dy_dtype, const uint8_t *W, const uint16_t *scales_f16,
+                      const uint16_t *zero_points_f16, void *dX, int dx_dtype, int M, int N, int K, int bits,
+                      int block_size, void *workspace, size_t workspace_bytes, qg_stream_t stream);
+int qgemm_nbits_uniform_zp_dgrad(const void *dY, int dy_dtype, const uint8_t *W, const uint16_t *scales_f16,
+                                 float uniform_zp, void *dX, int dx_dtype, int M, int N, int K, int bits,
+                                 int block_size, void *workspace, size_t workspace_bytes, qg_stream_t stream);
+int qgemm_codebook4_dgrad(const void *dY, int dy_dtype, const uint8_t *W, const float *codebook16,
+                          const float *absmax, void *dX, int dx_dtype, int M, int N, int K, int block_size,
+                          void *workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/*
+ * qg_clip_grad_norm -- the 2-norm over all the values of a list of gradient
+ * tensors, and their scaling to at most max_norm:
+ *   norm = sqrt( sum over every tensor and value of grad^2 )
+ *   out  = round( grad * min(1, max_norm / (norm + eps)) )
+ * A norm that is infinite or NaN is written as such and scales by what the
+ * formula gives (0 or NaN), so every out shows it.
+ *
+ *   tensors     the list in DEVICE memory, laid out by qg_grad_list_init from
+ *               a host array (copy it to the device once; it holds addresses)
+ *   count       tensors in the list;  chunks  what qg_grad_list_init returned
+ *   out         may be grad itself; same dtype and element alignment as grad
+ *   norm_dev    fp32, device
+ *   workspace   at least qg_clip_grad_norm_workspace_bytes(chunks) bytes, 16-byte aligned
+ * Squares are added in fp32 within a chunk (in fp64 where they overflow or
+ * underflow there) and in fp64 across chunks.  Deterministic.
+ *
+ * qg_grad_list_init -- checks a host array's grad, out, numel and dtype (a
+ * NULL out means grad; numel may be 0) and fills in first_chunk; *chunks
+ * receives the number of chunks.  Host only: enqueues nothing.
+ */
+typedef struct {
+    const void *grad;
+    void *out;
+    int64_t numel;
+    int64_t first_chunk; /* filled in by qg_grad_list_init */
+    int32_t dtype;       /* QG_F32, QG_F16 or QG_BF16 */
+    int32_t reserved;    /* filled in by qg_grad_list_init */
+} qg_grad_tensor;
+int qg_grad_list_init(qg_grad_tensor *tensors_host, int count, int64_t *chunks);
+size_t qg_clip_grad_norm_workspace_bytes(int64_t chunks);
+int qg_clip_grad_norm(const qg_grad_tensor *tensors_dev, int count, int64_t chunks, float max_norm, float eps,
+                      float *norm_dev, void *workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/*
  * qg_read_device_fault -- every wait inside the library's kernels is
  * bounded; a wait that gives up records a bit in a device-side fault word
  * instead of hanging.  This call synchronises the current device, returns
