@@ -3,16 +3,437 @@
 //
 // The contraction runs over the weight's rows n, so a block's scale and zero
 // point change along the sum and the weight has to be formed before the
-// product (in the forward pass they could be applied to a block's partial
-// sum).
+// product.  Tensor cores (tcgen05):
+//
+//  * Operand A is dY (n contiguous: K-major), loaded by TMA with the 128-byte
+//    swizzle.  Operand B is the dequantized weight, 64 rows n by 128 columns k
+//    a CTA and step.  Its k are contiguous in memory, so it is written MN-major
+//    -- [64-column block][8-row group][row][swizzled 16-byte chunk] -- and
+//    nothing is transposed: a thread turns 32 codes of one row (which share
+//    their block parameters, as blocks are at least 32 wide) into four 16-byte
+//    chunks.
+//  * PAIR = 2: two CTAs of a cluster share one tile (cta_group::2).  Each holds
+//    128 rows of every 256-row half and 128 of the 256 columns, so a weight is
+//    dequantized once for 512 rows and the tensor core reads each operand byte
+//    from shared memory half as often as with one CTA a tile.  The step's
+//    shared-memory traffic (operands read, weights written, dY written) is what
+//    a one-CTA tile of the same size is bound by.
+//  * The codes and parameters go from global memory straight into registers,
+//    one step ahead; only dY needs the TMA.
+//  * Tiles that do not fill a wave are split along n; their fp32 pieces are
+//    added in a fixed order by a second kernel.
 #include <algorithm>
+#include <atomic>
 
-#include "qg_device.cuh"
 #include "qg_internal.h"
+#include "qg_tc_common.cuh"
 
 namespace qg {
 namespace {
 
+// ------------------------------------------------------------------ tensor cores
+constexpr int kBK = 64;         // rows n of a step
+constexpr int kRows = 128;      // dY rows a CTA holds of each half
+constexpr int kCols = 128;      // weight columns a CTA dequantizes
+constexpr int kTask = 32;       // weights of one thread's task: one row, one block
+constexpr int kGroups = 2;      // the dequantizing warps take the steps in turn
+constexpr int kGroupThreads = kBK * kCols / kTask;  // 256
+constexpr int kDequantWarps = kGroups * kGroupThreads / 32;
+constexpr int kThreads = 64 + 32 * kDequantWarps;  // warp 0 TMA, warp 1 MMA, then dequant + epilogue
+constexpr int kABytes = kRows * kBK * 2;
+constexpr int kWBytes = kBK * kCols * 2;
+constexpr int kBlockBytes = kBK * 128;             // one 64-column block of the B operand
+constexpr int kSmemFixed = 1024 + 512 + 2048;      // alignment, barriers, codebook table
+constexpr int kSmemBudget = 227 * 1024;
+
+struct DgradArgs {
+    const uint8_t *W;
+    const void *par;         // fp16 scales or fp32 absmax, [N][nb]
+    const uint16_t *zp;
+    int zp_mode;
+    float zpv;
+    const float *codebook;
+    void *dX;
+    int x_dtype;
+    float *partial;
+    int M, N, K, nb, lbs, steps, mt;
+    int full_tiles, splits, split_steps;  // as TcArgs: whole tiles first, then the others split along n
+    unsigned *fault;
+};
+
+// B operand, MN-major, 128-byte swizzle: 64-column blocks kBlockBytes apart
+// (leading offset), 8-row groups 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kBlockBytes >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+template <int PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (PAIR == 1)
+        umma_f16(d, a, b, idesc, acc);
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+
+// Arrive on `bar` (of both CTAs of a pair) once every MMA issued so far has finished.
+template <int PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (PAIR == 1)
+        umma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+
+template <int PAIR>
+__device__ __forceinline__ void alloc_tmem(uint32_t *slot, uint32_t cols) {
+    if constexpr (PAIR == 1) {
+        tmem_alloc(slot, cols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int PAIR>
+__device__ __forceinline__ void free_tmem(uint32_t addr, uint32_t cols) {
+    if constexpr (PAIR == 1)
+        tmem_dealloc(addr, cols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One arrival on the same barrier of CTA 0 of the cluster.
+__device__ __forceinline__ void arrive_leader(uint64_t *bar) {
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+
+// As mbar_wait, acquiring what other CTAs of the cluster released.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned *fault, unsigned code) {
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 63u) == 63u) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+                if (fault) atomicOr(fault, code);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+constexpr int w_bufs() { return 4; }
+__host__ __device__ constexpr int a_slots(int h) {
+    const int n = (kSmemBudget - kSmemFixed - w_bufs() * kWBytes) / (h * kABytes);
+    return n > 8 ? 8 : n;
+}
+constexpr int smem_bytes(int h) { return kSmemFixed + w_bufs() * kWBytes + a_slots(h) * h * kABytes; }
+
+// The codes and parameters of one task.
+template <int BITS>
+struct Task {
+    uint32_t c[BITS];  // 32 weights of BITS bits
+    uint32_t par, zp;
+};
+
+template <int WK, int BITS, bool BF16, int PAIR, int H>
+__global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constant__ CUtensorMap dy_map, const DgradArgs p) {
+    constexpr int NA = a_slots(H), NW = w_bufs();
+    constexpr int BN = PAIR * kCols;
+    constexpr uint32_t TMEM_COLS = H * BN;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char *a_s = smem, *w_s = a_s + NA * H * kABytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(w_s + NW * kWBytes);  // dY of a step landed
+    uint64_t *aempty = full + NA;    // its MMAs are done
+    uint64_t *wfull = aempty + NA;   // weights of a step written (one arrival a warp)
+    uint64_t *wempty = wfull + NW;   // their MMAs are done
+    uint64_t *pfull = wempty + NW;   // (leader) the other CTA's dY and weights of a step are there
+    uint64_t *accf = pfull + NW;     // every MMA of the tile is done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *lut = reinterpret_cast<float *>(w_s + NW * kWBytes + 512);  // 16 x 32 (codebook)
+    static_assert((2 * NA + 3 * NW + 1) * 8 + 8 <= 512, "barriers fit");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
+    int tile = blockIdx.x / PAIR, s0 = 0, ns = p.steps, piece = -1;
+    if (tile >= p.full_tiles) {
+        const int q = tile - p.full_tiles;
+        tile = p.full_tiles + q / p.splits;
+        s0 = (q % p.splits) * p.split_steps;
+        ns = max(0, min(p.steps, s0 + p.split_steps) - s0);
+        if (p.splits > 1) piece = q;
+    }
+    const int m0 = (tile % p.mt) * (H * PAIR * kRows), k0 = (tile / p.mt) * BN;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&aempty[i], 1);
+        }
+        for (int i = 0; i < NW; ++i) {
+            mbar_init(&wfull[i], kGroupThreads / 32);
+            mbar_init(&wempty[i], 1);
+            mbar_init(&pfull[i], 1);
+        }
+        mbar_init(accf, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) alloc_tmem<PAIR>(tmem_slot, TMEM_COLS);
+    pdl_launch_dependents();
+    pdl_wait();  // nothing of the call is read or written before the preceding kernel is done
+    if constexpr (WK == WK_CODEBOOK)
+        for (int i = threadIdx.x; i < 16 * 32; i += kThreads) lut[i] = __ldg(p.codebook + (i >> 5));
+    tc_fence_before();
+    if constexpr (PAIR == 2) cluster_sync();  // the peer's barriers are ready
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0)
+            for (int i = 0; i < ns; ++i) {
+                const int s = i % NA;
+                if (!mbar_wait(&aempty[s], ((i / NA) & 1) ^ 1, abort_flag, p.fault, FAULT_WAIT_TC)) break;
+                mbar_arrive_expect_tx(&full[s], H * kABytes);
+#pragma unroll
+                for (int h = 0; h < H; ++h)  // rows past M and columns past N come as zeros
+                    tma_load_2d(a_s + (s * H + h) * kABytes, &dy_map, (s0 + i) * kBK, m0 + (h * PAIR + rank) * kRows, &full[s]);
+            }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f16(PAIR * kRows, BN, BF16) | (1u << 16);  // B MN-major
+            const bool two = H == 2 && m0 + PAIR * kRows < p.M;  // the second half holds rows
+            bool ok = true;
+            for (int i = 0; i < ns && ok; ++i) {
+                const int s = i % NA, b = i % NW;
+                ok = mbar_wait(&full[s], (i / NA) & 1, abort_flag, p.fault, FAULT_WAIT_TC) &&
+                     mbar_wait(&wfull[b], (i / NW) & 1, abort_flag, p.fault, FAULT_WAIT_TC);
+                if (!ok) break;
+                if (PAIR == 2 && rank == 1) {  // the other CTA's part: tell the leader
+                    arrive_leader(&pfull[b]);
+                    continue;
+                }
+                if (PAIR == 2) ok = mbar_wait_cluster(&pfull[b], (i / NW) & 1, abort_flag, p.fault, FAULT_WAIT_TC);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ad = sdesc_k128(smem_u32(a_s + s * H * kABytes));
+                const uint64_t ad1 = sdesc_k128(smem_u32(a_s + (s * H + H - 1) * kABytes));
+                const uint64_t bd = sdesc_mn128(smem_u32(w_s + b * kWBytes));
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k) {  // 16 n: 32 bytes along A's rows, two 8-row groups of B
+                    mma<PAIR>(tmem, ad + 2 * k, bd + 128 * k, idesc, (i | k) != 0);
+                    if (two) mma<PAIR>(tmem + BN, ad1 + 2 * k, bd + 128 * k, idesc, (i | k) != 0);
+                }
+                commit<PAIR>(&aempty[s]);
+                commit<PAIR>(&wempty[b]);
+            }
+            if (rank == 0) commit<PAIR>(accf);
+        }
+    } else {
+        // ---------------------------------------------------------------- dequant
+        const int t = threadIdx.x - 64, group = t / kGroupThreads, u = t % kGroupThreads;
+        const int r = u >> 2, j = u & 3;                       // row of the step, 32-column quarter
+        const int col = k0 + rank * kCols + j * kTask;
+        const bool col_in = col < p.K;
+        const size_t row_bytes = static_cast<size_t>(p.K) * BITS / 8;
+        const uint8_t *wp = p.W + static_cast<size_t>(col) * BITS / 8;
+        const int pb = col >> p.lbs;
+        const bool zt = WK == WK_NBITS && p.zp_mode == ZP_TENSOR;
+        // The two quarters of a 64-column block's pair of quarters share banks:
+        // quarters 2 and 3 write their chunks in the order 2 3 0 1.
+        const bool swap = j >= 2;
+        uint32_t off[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            off[i] = (j >> 1) * kBlockBytes + (r >> 3) * 1024 + (r & 7) * 128 + ((((j & 1) * 4 + (i ^ (swap ? 2 : 0))) ^ (r & 7)) << 4);
+        auto load = [&](int i, Task<BITS> &k) {
+            const int n = (s0 + i) * kBK + r;
+            const bool in = i < ns && n < p.N && col_in;  // outside: codes with scale 0, weights 0
+            k.par = k.zp = 0;
+#pragma unroll
+            for (int q = 0; q < BITS; ++q) k.c[q] = 0;
+            if (!in) return;
+            const uint8_t *src = wp + n * row_bytes;
+            if constexpr (BITS == 2) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+                k.c[0] = v.x, k.c[1] = v.y;
+            } else {
+#pragma unroll
+                for (int q = 0; q < BITS / 4; ++q) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + q);
+                    k.c[4 * q] = v.x, k.c[4 * q + 1] = v.y, k.c[4 * q + 2] = v.z, k.c[4 * q + 3] = v.w;
+                }
+            }
+            const size_t pi = static_cast<size_t>(n) * p.nb + pb;
+            if constexpr (WK == WK_NBITS) {
+                k.par = __ldg(static_cast<const unsigned short *>(p.par) + pi);
+                if (zt) k.zp = __ldg(reinterpret_cast<const unsigned short *>(p.zp) + pi);
+            } else {
+                k.par = __ldg(static_cast<const unsigned int *>(p.par) + pi);
+            }
+        };
+        const float *lut_lane = lut + lane;
+        const uint32_t zpu = __half_as_ushort(__float2half_rn(p.zpv)) * 0x10001u;
+        Task<BITS> next;
+        load(group, next);
+        for (int i = group; i < ns; i += kGroups) {
+            Task<BITS> k = next;
+            load(i + kGroups, next);
+            const int b = i % NW;
+            if (!mbar_wait(&wempty[b], ((i / NW) & 1) ^ 1, abort_flag, p.fault, FAULT_WAIT_TC)) break;
+            if (swap) {
+#pragma unroll
+                for (int q = 0; q < BITS / 2; ++q) {
+                    const uint32_t x = k.c[q];
+                    k.c[q] = k.c[q + BITS / 2];
+                    k.c[q + BITS / 2] = x;
+                }
+            }
+            unsigned char *ws = w_s + b * kWBytes;
+            UnitPar up;
+            up.lo = false;
+            if constexpr (WK == WK_NBITS) {
+                if constexpr (BF16) {
+                    up.zpf = zt ? h2f(static_cast<uint16_t>(k.zp)) : p.zpv;
+                    up.sf = h2f(static_cast<uint16_t>(k.par));
+                } else {
+                    up.zp2 = u32_as_h2(zt ? k.zp * 0x10001u : zpu);
+                    up.s2 = u32_as_h2(k.par * 0x10001u);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint4 w;
+                if constexpr (WK == WK_CODEBOOK)
+                    w = dequant8_codebook<BF16>(k.c[q], __uint_as_float(k.par), lut_lane);
+                else if constexpr (BITS == 2)
+                    w = dequant8_nbits<2, BF16>((k.c[q >> 1] >> (16 * (q & 1))) & 0xFFFFu, 0u, up);
+                else if constexpr (BITS == 4)
+                    w = dequant8_nbits<4, BF16>(k.c[q], 0u, up);
+                else
+                    w = dequant8_nbits<8, BF16>(k.c[2 * q], k.c[2 * q + 1], up);
+                *reinterpret_cast<uint4 *>(ws + off[q]) = w;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wfull[b]);
+        }
+        // ---------------------------------------------------------------- epilogue
+        const bool ok = mbar_wait(accf, 0, abort_flag, p.fault, FAULT_WAIT_TC);
+        tc_fence_after();
+        const int sub = warp & 3, cq = (warp - 2) >> 2;  // tensor-memory sub-partition; share of the columns
+        constexpr int CW = H * BN / (kDequantWarps / 4);
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+#pragma unroll 1
+        for (int cc = cq * CW; cc < (cq + 1) * CW; cc += 32) {
+            uint32_t v[32];
+            tmem_ld32(lane_addr + cc, v);
+            const int h = cc / BN, c0 = cc - h * BN;
+            const int row = h * PAIR * kRows + rank * kRows + sub * 32 + lane, m = m0 + row, kc = k0 + c0;
+            if (!ok || ns == 0 || m >= p.M || kc >= p.K) continue;  // K is a multiple of 32: a column group is in or out
+            if (piece >= 0) {
+                float4 *dst = reinterpret_cast<float4 *>(p.partial + (static_cast<size_t>(piece) * (H * PAIR * kRows) + row) * BN + c0);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
+                                         __uint_as_float(v[4 * q + 3]));
+            } else if (p.x_dtype == 0) {
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.dX) + static_cast<size_t>(m) * p.K + kc);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
+                                         __uint_as_float(v[4 * q + 3]));
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dX) + static_cast<size_t>(m) * p.K + kc);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float lo = __uint_as_float(v[8 * q + 2 * e]), hi = __uint_as_float(v[8 * q + 2 * e + 1]);
+                        o[e] = p.x_dtype == 1 ? (static_cast<uint32_t>(f2h(hi)) << 16) | f2h(lo)
+                                              : (static_cast<uint32_t>(f2bf(hi)) << 16) | f2bf(lo);
+                    }
+                    dst[q] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if constexpr (PAIR == 2) cluster_sync();  // the peer's MMAs and arrivals are done with this CTA's memory
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        free_tmem<PAIR>(tmem, TMEM_COLS);
+    }
+}
+
+// dX of the split tiles: their pieces in order, four columns a thread.
+__global__ void __launch_bounds__(256) dgrad_reduce_kernel(const float *__restrict__ partial, int tiles, int splits, int rows, int bn,
+                                                           int first, int mt, int M, int K, void *dX, int x_dtype) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int per = rows * (bn / 4);
+    const int64_t total = static_cast<int64_t>(tiles) * per;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const int q = static_cast<int>(i / per), e = static_cast<int>(i - static_cast<int64_t>(q) * per);
+        const int row = e / (bn / 4), c = (e - row * (bn / 4)) * 4, tile = first + q;
+        const int m = (tile % mt) * rows + row, k = (tile / mt) * bn + c;
+        if (m >= M || k >= K) continue;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int z = 0; z < splits; ++z) {
+            const float4 v = *reinterpret_cast<const float4 *>(partial + ((static_cast<size_t>(q) * splits + z) * rows + row) * bn + c);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        const size_t at = static_cast<size_t>(m) * K + k;
+        if (x_dtype == 0) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(dX) + at) = s;
+        } else {
+            const uint16_t a = x_dtype == 1 ? f2h(s.x) : f2bf(s.x), b = x_dtype == 1 ? f2h(s.y) : f2bf(s.y);
+            const uint16_t cc = x_dtype == 1 ? f2h(s.z) : f2bf(s.z), d = x_dtype == 1 ? f2h(s.w) : f2bf(s.w);
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dX) + at) =
+                make_uint2(a | static_cast<uint32_t>(b) << 16, cc | static_cast<uint32_t>(d) << 16);
+        }
+    }
+}
+
+// dY with its rows at 16-byte boundaries (the TMA's rule), for N that is no multiple of 8.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *__restrict__ src, int N, int ld, uint16_t *__restrict__ dst) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const size_t row = blockIdx.x;
+    for (int n = threadIdx.x; n < ld; n += 256) dst[row * ld + n] = n < N ? src[row * N + n] : 0;
+}
+
+// ------------------------------------------------------------------ plain fp32 tiles
 // One weight in fp32, exactly as the forward kernels define it.
 __device__ float weight_at(const GemmProblem &p, int n, int k) {
     const int nb = p.K / p.bs, b = k / p.bs;
@@ -59,13 +480,149 @@ __global__ void __launch_bounds__(256) dgrad_simple_kernel(const GemmProblem p) 
                 store_y_elem(p.Y, p.y_dtype, static_cast<size_t>(m0 + tm + i) * p.K + k0 + tk + j, acc[i][j]);
 }
 
+// ------------------------------------------------------------------ host side
+struct Plan {
+    int pair, h, rows, bn, mt, kt, steps;
+    int full_tiles, tail_tiles, splits, split_steps;
+    size_t partial_bytes, pad_bytes;
+    int ld;
+};
+
+// Rows decide the tile: up to 128 rows one CTA a tile (128 x 128), up to 256 a
+// pair (256 x 256), above that two halves a pair (512 x 256).  Whole tiles fill
+// complete waves, the others are split along n over the SMs, at least four
+// steps a piece.
+Plan make_plan(int M, int N, int K) {
+    Plan c{};
+    c.pair = M <= kRows ? 1 : 2;
+    c.h = M <= 2 * kRows ? 1 : 2;
+    c.rows = c.pair * c.h * kRows;
+    c.bn = c.pair * kCols;
+    c.mt = (M + c.rows - 1) / c.rows;
+    c.kt = (K + c.bn - 1) / c.bn;
+    c.steps = (N + kBK - 1) / kBK;
+    const int units = device_info().sm_count / c.pair;
+    const int64_t tiles = static_cast<int64_t>(c.mt) * c.kt;
+    c.full_tiles = static_cast<int>(tiles / units * units);
+    c.tail_tiles = static_cast<int>(tiles - c.full_tiles);
+    c.splits = 1;
+    c.split_steps = c.steps;
+    if (c.tail_tiles) {
+        const int sp = std::max(1, std::min(units / c.tail_tiles, c.steps / 4));
+        c.split_steps = (c.steps + sp - 1) / sp;
+        c.splits = (c.steps + c.split_steps - 1) / c.split_steps;
+    }
+    if (c.splits > 1) c.partial_bytes = sizeof(float) * c.tail_tiles * c.splits * static_cast<size_t>(c.rows) * c.bn;
+    c.ld = (N + 7) / 8 * 8;
+    if (c.ld != N) c.pad_bytes = (static_cast<size_t>(M) * c.ld * 2 + 255) / 256 * 256;
+    return c;
+}
+
+// 3-bit codes and fp32 dY take the plain kernel.
+bool tensor_cores(int dy_dtype, int bits) { return dy_dtype != 0 && bits != 3 && encode_fn() != nullptr; }
+
+template <int WK, int BITS, bool BF16, int PAIR, int H>
+cudaError_t launch(const CUtensorMap &map, const DgradArgs &a, int tiles, cudaStream_t s) {
+    auto kern = dgrad_kernel<WK, BITS, BF16, PAIR, H>;
+    static std::atomic<unsigned long long> configured{0};
+    const int slot = device_slot();
+    const unsigned long long bit = slot < 0 ? 0 : 1ull << slot;
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(H));
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(tiles * PAIR);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes(H);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = PAIR;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, map, a);
+}
+
+template <int WK, int BITS, bool BF16>
+cudaError_t launch_shape(const Plan &c, const CUtensorMap &map, const DgradArgs &a, cudaStream_t s) {
+    const int tiles = c.full_tiles + c.tail_tiles * c.splits;
+    if (c.pair == 1) return launch<WK, BITS, BF16, 1, 1>(map, a, tiles, s);
+    return c.h == 1 ? launch<WK, BITS, BF16, 2, 1>(map, a, tiles, s) : launch<WK, BITS, BF16, 2, 2>(map, a, tiles, s);
+}
+
+template <bool BF16>
+cudaError_t launch_kind(const GemmProblem &p, const Plan &c, const CUtensorMap &map, const DgradArgs &a, cudaStream_t s) {
+    if (p.kind == WK_CODEBOOK) return launch_shape<WK_CODEBOOK, 4, BF16>(c, map, a, s);
+    if (p.bits == 2) return launch_shape<WK_NBITS, 2, BF16>(c, map, a, s);
+    if (p.bits == 4) return launch_shape<WK_NBITS, 4, BF16>(c, map, a, s);
+    return launch_shape<WK_NBITS, 8, BF16>(c, map, a, s);
+}
+
 }  // namespace
 
-size_t dgrad_workspace_bytes(int, int, int, int, int) { return 0; }
+size_t dgrad_workspace_bytes(int dy_dtype, int M, int N, int K, int bits) {
+    if (!tensor_cores(dy_dtype, bits)) return 0;
+    const Plan c = make_plan(M, N, K);
+    return c.pad_bytes + c.partial_bytes;
+}
 
-cudaError_t dgrad(const GemmProblem &p, void *, cudaStream_t s) {
-    const cudaError_t e = launch_pdl(dgrad_simple_kernel, dim3((p.K + 63) / 64, (p.M + 63) / 64), dim3(256), 0, s, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+cudaError_t dgrad(const GemmProblem &p, void *ws, cudaStream_t s) {
+    if (!tensor_cores(p.a_dtype, p.bits)) {
+        const cudaError_t e = launch_pdl(dgrad_simple_kernel, dim3((p.K + 63) / 64, (p.M + 63) / 64), dim3(256), 0, s, p);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    const Plan c = make_plan(p.M, p.N, p.K);
+    const void *dy = p.A;
+    cudaError_t e = cudaSuccess;
+    if (c.pad_bytes) {
+        e = launch_pdl(pad_rows_kernel, dim3(p.M), dim3(256), 0, s, static_cast<const uint16_t *>(p.A), p.N, c.ld, static_cast<uint16_t *>(ws));
+        if (e != cudaSuccess) return e;
+        dy = ws;
+    }
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.ld), static_cast<cuuint64_t>(p.M)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.ld) * 2};
+    const cuuint32_t box[2] = {kBK, kRows}, es[2] = {1, 1};
+    if (encode_fn()(&map, p.a_dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(dy),
+                    dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    DgradArgs a{};
+    a.W = p.W;
+    a.par = p.kind == WK_CODEBOOK ? static_cast<const void *>(p.absmax) : static_cast<const void *>(p.scales);
+    a.zp = p.zp;
+    a.zp_mode = p.zp_mode;
+    a.zpv = p.uniform_zp;
+    a.codebook = p.codebook;
+    a.dX = p.Y;
+    a.x_dtype = p.y_dtype;
+    a.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + c.pad_bytes);
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.nb = p.K / p.bs;
+    a.lbs = 31 - __builtin_clz(static_cast<unsigned>(p.bs));
+    a.steps = c.steps;
+    a.mt = c.mt;
+    a.full_tiles = c.full_tiles;
+    a.splits = c.splits;
+    a.split_steps = c.split_steps;
+    a.fault = fault_word();
+    e = p.a_dtype == 2 ? launch_kind<true>(p, c, map, a, s) : launch_kind<false>(p, c, map, a, s);
+    if (e != cudaSuccess) return e;
+    if (c.splits > 1) {
+        const int64_t work = static_cast<int64_t>(c.tail_tiles) * c.rows * (c.bn / 4);
+        e = launch_pdl(dgrad_reduce_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, device_info().sm_count * 16))),
+                       dim3(256), 0, s, static_cast<const float *>(a.partial), c.tail_tiles, c.splits, c.rows, c.bn, c.full_tiles, c.mt, p.M, p.K,
+                       p.Y, p.y_dtype);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaGetLastError();
 }
 
 }  // namespace qg
