@@ -532,20 +532,7 @@ cudaError_t launch(const CUtensorMap &map, const DgradArgs &a, int tiles, cudaSt
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(tiles * PAIR);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(H);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = PAIR;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR == 2 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, map, a);
+    return launch_cluster(kern, dim3(tiles * PAIR), dim3(kThreads), smem_bytes(H), s, PAIR, map, a);
 }
 
 template <int WK, int BITS, bool BF16>

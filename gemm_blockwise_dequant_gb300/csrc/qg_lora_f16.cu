@@ -1,0 +1,8 @@
+// qg_lora_f16.cu -- the row kernels of the adapters for fp16 activations and fp16 adapters.
+#include "qg_lora_rows.cuh"
+
+namespace qg {
+
+QG_DEFINE_LAUNCH_ROWS(kF16, kF16)
+
+}  // namespace qg

@@ -1,0 +1,8 @@
+// qg_lora_f32_bf16.cu -- the row kernels of the adapters for fp32 activations and bf16 adapters.
+#include "qg_lora_rows.cuh"
+
+namespace qg {
+
+QG_DEFINE_LAUNCH_ROWS(kF32, kBF16)
+
+}  // namespace qg

@@ -1,0 +1,540 @@
+// qg_lora_rows.cuh -- the two thin products over rows, in one kernel:
+//
+//   forward   V = X A^T,          Y  = Y_in  + scaling V B^T
+//   backward  G = scaling dY B,   dX = dX_in + G A
+//
+// Both read a wide row (contraction over `c1` values) into `rank` sums and
+// spread them over `c2` outputs.  A cluster of CTAs owns a tile of rows of one
+// request: each CTA contracts its share of the row, the partial sums meet
+// through distributed shared memory (added in rank order), and each CTA then
+// writes its share of the outputs.  One launch, no workspace between the
+// products, and the row's own width supplies the parallelism when there are
+// few rows; with many rows the cluster is one CTA and several of them on an SM
+// overlap each other's phases.  Bound by memory: the wide rows in and out.
+//
+// The adapter's tensor is read by every tile of its rows, from L2.  In the
+// forward pass its contiguous axis is the contraction (fragments load as they
+// are); in the backward pass it is the other one, and a byte permute pairs two
+// rows' values (NATIVE) where TF32 fragments take single values.
+#pragma once
+
+#include "qg_lora_common.cuh"
+
+namespace qg {
+
+struct RowsArgs {
+    LoraProblem p;
+    const void *in;      // X or dY
+    int64_t ld_in;
+    int c1, c2;          // contraction and output widths (forward K, N; backward N, K)
+    const void *w1, *w2; // forward A, B; backward B, A
+    const void *base;    // Y_in / dX_in or null
+    int base_dtype;
+    int64_t ld_base;
+    void *out;           // Y / dX or null (no second product)
+    int out_dtype;
+    int64_t ld_out;
+    float *sums;         // V_out / G or null, [T][rank]
+    int cs;              // CTAs of a cluster
+    int in_vec, out_vec; // rows at 16-byte boundaries: vector accesses
+};
+
+template <int XT, int WT, bool BWD, int MT, int RG, int NT>
+struct RowsKernel {
+    static constexpr bool NATIVE = XT != kF32;
+    static constexpr int KG = 8 / RG;              // warps sharing the rows of a group
+    static constexpr int R = 16 * MT * RG;         // rows of a tile
+    static constexpr int EL = NATIVE ? 8 : 4;      // contraction values of a lane's 16 bytes
+    static constexpr int CH = 4 * EL;              // of a warp's chunk
+    static constexpr int BLK = 2 * CH;             // two chunks: 128 bytes of a row
+    static constexpr int UW = NATIVE ? 16 : 8;     // rank values of one MMA of the second product
+    static constexpr int EU = UW / 4;
+    static constexpr int RC = 8 * NT;              // rank values of one pass of the first product
+    static constexpr int PS = RC + 4;              // row stride of the partial sums (bank spread)
+
+    // 16 bytes of a row (EL values from k on), zero past the end
+    static __device__ __forceinline__ uint4 load_in(const RowsArgs &q, const char *row, int k, bool row_in) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (!row_in) return v;
+        if (q.in_vec && k + EL <= q.c1) return __ldg(reinterpret_cast<const uint4 *>(row + static_cast<size_t>(k) * (NATIVE ? 2 : 4)));
+        uint32_t w[4] = {0, 0, 0, 0};
+        if constexpr (NATIVE) {
+            const unsigned short *x = reinterpret_cast<const unsigned short *>(row);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < q.c1) w[e >> 1] |= static_cast<uint32_t>(__ldg(x + k + e)) << (16 * (e & 1));
+        } else {
+            const unsigned int *x = reinterpret_cast<const unsigned int *>(row);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (k + e < q.c1) w[e] = __ldg(x + k + e);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+
+    // The adapter's values of a lane's chunk for rank columns: w[i][...] of tile i.
+    // NATIVE: 4 words, word x = values 2x, 2x+1 of the contraction.  TF32: 4
+    // values as fp32 bits.
+    static __device__ __forceinline__ void load_w1(const RowsArgs &q, int a, int j0, int ntr, int k, int g, uint32_t (&w)[NT][4]) {
+        const int r = q.p.r;
+        if constexpr (!BWD) {  // A[a][j][k ..]: j = j0 + 8 i + g
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+                if (i >= ntr || k >= q.c1) continue;
+                const size_t at = (static_cast<size_t>(a) * r + j0 + 8 * i + g) * q.c1 + k;
+                if constexpr (WT == kF32 || NATIVE) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(q.w1) + at * (NATIVE ? 2 : 4)));
+                    w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+                } else {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(q.w1) + at));
+                    widen(v.x, w[i][0], w[i][1]);
+                    widen(v.y, w[i][2], w[i][3]);
+                }
+            }
+        } else {  // B[a][k + e][j]: j = j0 + g ntr + i, ntr contiguous values
+            const size_t at = (static_cast<size_t>(a) * q.c1 + k) * r + j0 + g * ntr;
+            uint32_t raw[EL][NT];  // 16-bit values, or fp32 bits
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+                const bool in = k + e < q.c1;
+                const size_t o = at + static_cast<size_t>(e) * r;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) raw[e][i] = 0;
+                if (!in) continue;
+                if constexpr (WT == kF32) {
+                    const unsigned int *s = static_cast<const unsigned int *>(q.w1) + o;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        if (i < ntr) raw[e][i] = __ldg(s + i);
+                } else {
+                    const unsigned short *s = static_cast<const unsigned short *>(q.w1) + o;
+                    if (ntr == NT && NT == 2) {
+                        const uint32_t v = __ldg(reinterpret_cast<const unsigned int *>(s));
+                        raw[e][0] = v & 0xFFFFu, raw[e][1 % NT] = v >> 16;
+                    } else if (ntr == NT && NT == 4) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(s));
+                        raw[e][0] = v.x & 0xFFFFu, raw[e][1 % NT] = v.x >> 16, raw[e][2 % NT] = v.y & 0xFFFFu, raw[e][3 % NT] = v.y >> 16;
+                    } else if (ntr == NT && NT == 8) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(s));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) raw[e][i] = (i & 1) ? u[(i >> 1) & 3] >> 16 : u[(i >> 1) & 3] & 0xFFFFu;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            if (i < ntr) raw[e][i] = __ldg(s + i);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (NATIVE) w[i][x] = pack2(raw[2 * x][i], raw[2 * x + 1][i]);
+                    else if constexpr (WT == kF32) w[i][x] = raw[x][i];
+                    else w[i][x] = __float_as_uint(to_float<WT>(static_cast<uint16_t>(raw[x][i])));
+                }
+        }
+    }
+
+    static __device__ __forceinline__ void widen(uint32_t v, uint32_t &a, uint32_t &b) {  // two 16-bit values to fp32 bits
+        a = __float_as_uint(to_float<WT>(static_cast<uint16_t>(v & 0xFFFFu)));
+        b = __float_as_uint(to_float<WT>(static_cast<uint16_t>(v >> 16)));
+    }
+
+    // TF32 product of x (fp32, two terms) and w (fp32 bits; two terms when the adapter is fp32)
+    static __device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&x)[4], uint32_t w0, uint32_t w1) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_tf32(x[i], h[i], l[i]);
+        mma_tf32_split(d, h, l, w0, w1);
+    }
+    static __device__ __forceinline__ void mma_tf32_split(float (&d)[4], const uint32_t (&h)[4], const uint32_t (&l)[4], uint32_t w0, uint32_t w1) {
+        if constexpr (WT == kF32) {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(__uint_as_float(w0), h0, l0);
+            split_tf32(__uint_as_float(w1), h1, l1);
+            mma8(d, l[0], l[1], l[2], l[3], h0, h1);
+            mma8(d, h[0], h[1], h[2], h[3], l0, l1);
+            mma8(d, h[0], h[1], h[2], h[3], h0, h1);
+        } else {
+            mma8(d, l[0], l[1], l[2], l[3], w0, w1);
+            mma8(d, h[0], h[1], h[2], h[3], w0, w1);
+        }
+    }
+
+    // The adapter's values of the second product for unit u and the 4 tiles of a
+    // 32-column group: b[i][0..1].  Column (tile i, lane column q) is
+    // n0 + 8 (q / 2) + 2 i + q % 2, so that a lane ends with 8 contiguous outputs.
+    static __device__ __forceinline__ void load_w2(const RowsArgs &q, int a, int u, int n0, int g, int c, uint32_t (&b)[4][2]) {
+        const int r = q.p.r, j = u * UW + c * EU;
+        const bool jin = j < r;
+        if constexpr (!BWD) {  // B[a][n][j ..]
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = n0 + (g >> 1) * 8 + 2 * i + (g & 1);
+                b[i][0] = b[i][1] = 0;
+                if (!jin || n >= q.c2) continue;
+                const size_t at = (static_cast<size_t>(a) * q.c2 + n) * r + j;
+                if constexpr (NATIVE || WT == kF32) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(static_cast<const char *>(q.w2) + at * (NATIVE ? 2 : 4)));
+                    b[i][0] = v.x, b[i][1] = v.y;
+                } else {
+                    widen(__ldg(reinterpret_cast<const unsigned int *>(static_cast<const uint16_t *>(q.w2) + at)), b[i][0], b[i][1]);
+                }
+            }
+        } else {  // A[a][j + e][k ..]: 8 contiguous columns of each row, of which this lane's are every other one
+            const int k = n0 + (g >> 1) * 8;
+            const bool in = jin && k < q.c2;
+            const size_t at = (static_cast<size_t>(a) * r + j) * q.c2 + k;
+            if constexpr (NATIVE) {
+                uint4 row[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    row[e] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q.w2) + at + static_cast<size_t>(e) * q.c2))
+                                : make_uint4(0, 0, 0, 0);
+                const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    b[i][0] = __byte_perm(word(row[0], i), word(row[1], i), sel);
+                    b[i][1] = __byte_perm(word(row[2], i), word(row[3], i), sel);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const size_t o = at + static_cast<size_t>(e) * q.c2;
+                    if constexpr (WT == kF32) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint2 v = in ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const float *>(q.w2) + o + 2 * i)) : make_uint2(0, 0);
+                            b[i][e] = (g & 1) ? v.y : v.x;
+                        }
+                    } else {
+                        const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q.w2) + o)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t x = word(v, i);
+                            b[i][e] = __float_as_uint(to_float<WT>(static_cast<uint16_t>((g & 1) ? x >> 16 : x & 0xFFFFu)));
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    static __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+    // Shared memory: the warps' partial sums (later the operand fragments of the
+    // second product), the CTA's sums (read by the cluster), the rows' whole sums
+    // and their scales.
+    static __host__ __device__ int rank_pad(int r) { return (r + UW - 1) / UW * UW; }
+    static __host__ __device__ int part_bytes(int r) {
+        const int part = KG * R * PS * 4, frag = (R / 16) * (rank_pad(r) / UW) * 2 * 512;
+        return part > frag ? part : frag;
+    }
+    static __host__ __device__ int smem_bytes(int r) { return part_bytes(r) + 2 * R * rank_pad(r) * 4 + R * 4; }
+
+    static __device__ void run(const RowsArgs &q) {
+        extern __shared__ __align__(16) unsigned char sm[];
+        const LoraProblem &p = q.p;
+        const int r = p.r, rp = rank_pad(r);
+        float *part = reinterpret_cast<float *>(sm);
+        uint4 *frag = reinterpret_cast<uint4 *>(sm);
+        float *mine = reinterpret_cast<float *>(sm + part_bytes(r));
+        float *whole = mine + R * rp;
+        float *rscale = whole + R * rp;
+        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+        const int rg = warp / KG, kg = warp % KG;
+        const int rank = blockIdx.x % q.cs, tile = blockIdx.x / q.cs;
+        pdl_launch_dependents();
+        pdl_wait();
+        RowTile t;
+        if (!find_tile(p, tile, R, blockIdx.x == 0, t) || t.rows == 0) return;  // the same for the whole cluster
+        const float scale = t.adapter >= 0 && p.scaling ? __ldg(p.scaling + t.adapter) : 1.f;
+
+        if (t.adapter >= 0) {
+            // ---------------------------------------------------------- first product
+            const int nblk = (q.c1 + BLK - 1) / BLK;
+            const int b0 = static_cast<int>(static_cast<int64_t>(nblk) * rank / q.cs), b1 = static_cast<int>(static_cast<int64_t>(nblk) * (rank + 1) / q.cs);
+            const int row0 = rg * 16 * MT;
+            const char *rowp[MT][2];
+            bool rin[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = row0 + m * 16 + h * 8 + g;
+                    rin[m][h] = row < t.rows;
+                    rowp[m][h] = static_cast<const char *>(q.in) + static_cast<size_t>(t.t0 + (rin[m][h] ? row : 0)) * q.ld_in * (NATIVE ? 2 : 4);
+                }
+            for (int j0 = 0; j0 < r; j0 += RC) {
+                const int ntr = min(NT, (r - j0) / 8);
+                float acc[MT][NT][4] = {};
+                for (int b = b0 + kg; b < b1; b += KG) {
+                    uint4 x[2][MT][2];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) x[s][m][h] = load_in(q, rowp[m][h], b * BLK + s * CH + c * EL, rin[m][h]);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        uint32_t w[NT][4];
+                        load_w1(q, t.adapter, j0, ntr, b * BLK + s * CH + c * EL, g, w);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const uint4 x0 = x[s][m][0], x1 = x[s][m][1];
+                            if constexpr (NATIVE) {
+#pragma unroll
+                                for (int i = 0; i < NT; ++i) {
+                                    mma16<XT>(acc[m][i], x0.x, x1.x, x0.y, x1.y, w[i][0], w[i][1]);
+                                    mma16<XT>(acc[m][i], x0.z, x1.z, x0.w, x1.w, w[i][2], w[i][3]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    uint32_t hi[4], lo[4];
+                                    split_tf32(__uint_as_float(half ? x0.z : x0.x), hi[0], lo[0]);
+                                    split_tf32(__uint_as_float(half ? x1.z : x1.x), hi[1], lo[1]);
+                                    split_tf32(__uint_as_float(half ? x0.w : x0.y), hi[2], lo[2]);
+                                    split_tf32(__uint_as_float(half ? x1.w : x1.y), hi[3], lo[3]);
+#pragma unroll
+                                    for (int i = 0; i < NT; ++i) mma_tf32_split(acc[m][i], hi, lo, w[i][2 * half], w[i][2 * half + 1]);
+                                }
+                            }
+                        }
+                    }
+                }
+                if (j0) __syncthreads();  // the previous pass has read its partial sums
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int col = 2 * c + (e & 1), row = row0 + m * 16 + (e >> 1) * 8 + g;
+                            const int j = BWD ? col * ntr + i : i * 8 + col;
+                            if (i < ntr) part[(kg * R + row) * PS + j] = acc[m][i][e];
+                        }
+                __syncthreads();
+                for (int e = tid; e < R * 8 * ntr; e += 256) {
+                    const int row = e / (8 * ntr), j = e - row * 8 * ntr;
+                    float s = 0.f;
+#pragma unroll
+                    for (int w = 0; w < KG; ++w) s += part[(w * R + row) * PS + j];
+                    mine[row * rp + j0 + j] = s;
+                }
+            }
+            // ---------------------------------------------------------- the cluster's sums
+            if (q.cs > 1) {
+                __syncwarp();
+                cluster_arrive();
+                cluster_wait();
+            } else {
+                __syncthreads();
+            }
+            for (int e = tid; e < R * rp; e += 256) {
+                const int row = e / rp, j = e - row * rp;
+                float s = 0.f;
+                if (j < r) {
+                    if (q.cs > 1)
+                        for (int w = 0; w < q.cs; ++w) s += peer_float(mine + e, w);
+                    else
+                        s = mine[e];
+                    if (BWD) s *= scale;
+                    if (q.sums && rank == 0 && row < t.rows) q.sums[static_cast<size_t>(t.t0 + row) * r + j] = s;
+                }
+                whole[e] = s;
+            }
+            __syncthreads();
+            if (q.cs > 1) cluster_arrive();  // done with the peers' memory; awaited before leaving
+            // ---------------------------------------------------------- operand fragments of the sums
+            if (q.out) {
+                if constexpr (NATIVE) {
+                    for (int row = tid; row < R; row += 256) {
+                        float mx = 0.f;
+                        for (int j = 0; j < r; ++j) mx = fmaxf(mx, fabsf(whole[row * rp + j]));
+                        const int ef = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu);
+                        rscale[row] = exp2i(ef == 255 || mx == 0.f ? 0 : min(max(ef - 127, -126), 126));
+                    }
+                    __syncthreads();
+                }
+                const int units = rp / UW;
+                for (int f = tid; f < (R / 16) * units * 32; f += 256) {
+                    const int l = f & 31, u = (f >> 5) % units, m = (f >> 5) / units;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {  // fragment word x: row g (+8 for odd x), the first or second part of the lane's values
+                        const int row = m * 16 + (l >> 2) + (x & 1) * 8;
+                        const float *v = whole + row * rp + u * UW + (l & 3) * EU + (x >> 1) * (EU / 2);
+                        if constexpr (NATIVE) {
+                            const float inv = 1.f / rscale[row];
+                            uint16_t h0, l0, h1, l1;
+                            split16<XT>(v[0] * inv, h0, l0);
+                            split16<XT>(v[1] * inv, h1, l1);
+                            hi[x] = pack2(h0, h1), lo[x] = pack2(l0, l1);
+                        } else {
+                            split_tf32(v[0], hi[x], lo[x]);
+                        }
+                    }
+                    frag[((m * units + u) * 2) * 32 + l] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    frag[((m * units + u) * 2 + 1) * 32 + l] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                __syncthreads();
+            }
+        } else if (!BWD && q.sums && rank == 0) {
+            for (int e = tid; e < t.rows * r; e += 256) q.sums[static_cast<size_t>(t.t0) * r + e] = 0.f;
+        }
+
+        // -------------------------------------------------------------- second product
+        if (q.out) {
+            const int ngrp = (q.c2 + 31) / 32, units = rp / UW;
+            const int n_lo = static_cast<int>(static_cast<int64_t>(ngrp) * rank / q.cs), n_hi = static_cast<int>(static_cast<int64_t>(ngrp) * (rank + 1) / q.cs);
+            const int row0 = rg * 16 * MT;
+            float mul[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mul[m][h] = BWD ? 1.f : scale;
+                    if (NATIVE && t.adapter >= 0) mul[m][h] *= rscale[row0 + m * 16 + h * 8 + g];
+                }
+            for (int b = n_lo + kg; b < n_hi; b += KG) {
+                const int n0 = b * 32, n = n0 + c * 8;
+                const bool vec = q.out_vec && n + 8 <= q.c2;
+                float base[MT][2][8];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) load_base(q, t.t0 + row0 + m * 16 + h * 8 + g, row0 + m * 16 + h * 8 + g < t.rows, n, vec, base[m][h]);
+                float acc[MT][4][4] = {};
+                if (t.adapter >= 0)
+                    for (int u = 0; u < units; ++u) {
+                        uint32_t w[4][2];
+                        load_w2(q, t.adapter, u, n0, g, c, w);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const int mt = rg * MT + m;
+                            const uint4 h = frag[((mt * units + u) * 2) * 32 + lane], l = frag[((mt * units + u) * 2 + 1) * 32 + lane];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (NATIVE) {
+                                    mma16<XT>(acc[m][i], l.x, l.y, l.z, l.w, w[i][0], w[i][1]);
+                                    mma16<XT>(acc[m][i], h.x, h.y, h.z, h.w, w[i][0], w[i][1]);
+                                } else {
+                                    const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
+                                    mma_tf32_split(acc[m][i], hh, ll, w[i][0], w[i][1]);
+                                }
+                            }
+                        }
+                    }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = row0 + m * 16 + h * 8 + g;
+                        if (row >= t.rows) continue;
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = t.adapter >= 0 ? fmaf(acc[m][e >> 1][h * 2 + (e & 1)], mul[m][h], base[m][h][e]) : base[m][h][e];
+                        store_out(q, t.t0 + row, n, vec, y);
+                    }
+            }
+        }
+        if (q.cs > 1 && t.adapter >= 0) {
+            __syncwarp();
+            cluster_wait();
+        }
+    }
+
+    static __device__ __forceinline__ void load_base(const RowsArgs &q, int t, bool in, int n, bool vec, float (&v)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        if (!in || !q.base) return;
+        const size_t at = static_cast<size_t>(t) * q.ld_base + n;
+        if (vec) {
+            if (q.base_dtype == kF32) {
+                const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(q.base) + at);
+                const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(q.base) + at + 4);
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
+                const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q.base) + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = word(a, i);
+                    const uint16_t x0 = static_cast<uint16_t>(x & 0xFFFFu), x1 = static_cast<uint16_t>(x >> 16);
+                    v[2 * i] = q.base_dtype == kF16 ? h2f(x0) : bf2f(x0);
+                    v[2 * i + 1] = q.base_dtype == kF16 ? h2f(x1) : bf2f(x1);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < q.c2) v[e] = load_elem(q.base, q.base_dtype, at + e);
+        }
+    }
+
+    static __device__ __forceinline__ void store_out(const RowsArgs &q, int t, int n, bool vec, const float (&y)[8]) {
+        const size_t at = static_cast<size_t>(t) * q.ld_out + n;
+        if (vec) {
+            if (q.out_dtype == kF32) {
+                float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(q.out) + at);
+                d[0] = make_float4(y[0], y[1], y[2], y[3]);
+                d[1] = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = q.out_dtype == kF16 ? pack2(f2h(y[2 * i]), f2h(y[2 * i + 1])) : pack2(f2bf(y[2 * i]), f2bf(y[2 * i + 1]));
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(q.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < q.c2) store_y_elem(q.out, q.out_dtype, at + e, y[e]);
+        }
+    }
+};
+
+// Tiles of 16 rows (all eight warps share them) or 64 rows (two groups of 32).
+struct RowsPlan {
+    int rows, cs, tiles;
+};
+
+template <int XT, int WT, bool BWD, int MT, int RG, int NT>
+__global__ void __launch_bounds__(256, 2) lora_rows_kernel(const RowsArgs q) {
+    RowsKernel<XT, WT, BWD, MT, RG, NT>::run(q);
+}
+
+template <int XT, int WT, bool BWD, int MT, int RG, int NT>
+cudaError_t launch_rows_one(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
+    auto kern = lora_rows_kernel<XT, WT, BWD, MT, RG, NT>;
+    const int smem = RowsKernel<XT, WT, BWD, MT, RG, NT>::smem_bytes(q.p.r);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && q.cs > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return launch_cluster(kern, dim3(static_cast<unsigned>(plan.tiles) * q.cs), dim3(256), smem, s, q.cs, q);
+}
+
+template <int XT, int WT, bool BWD>
+cudaError_t launch_rows_shape(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
+    const int r = q.p.r;
+    if (plan.rows == 16)
+        return r <= 16 ? launch_rows_one<XT, WT, BWD, 1, 1, 2>(q, plan, s)
+                       : r <= 32 ? launch_rows_one<XT, WT, BWD, 1, 1, 4>(q, plan, s) : launch_rows_one<XT, WT, BWD, 1, 1, 8>(q, plan, s);
+    return r <= 16 ? launch_rows_one<XT, WT, BWD, 2, 2, 2>(q, plan, s)
+                   : r <= 32 ? launch_rows_one<XT, WT, BWD, 2, 2, 4>(q, plan, s) : launch_rows_one<XT, WT, BWD, 2, 2, 8>(q, plan, s);
+}
+
+// Defined once for each pair of types (qg_lora_bf16.cu and its siblings).
+template <int XT, int WT>
+cudaError_t launch_rows(const RowsArgs &q, bool bwd, const RowsPlan &plan, cudaStream_t s);
+#define QG_DEFINE_LAUNCH_ROWS(XT, WT)                                                                                  \
+    template <>                                                                                                        \
+    cudaError_t launch_rows<XT, WT>(const RowsArgs &q, bool bwd, const RowsPlan &plan, cudaStream_t s) {               \
+        return bwd ? launch_rows_shape<XT, WT, true>(q, plan, s) : launch_rows_shape<XT, WT, false>(q, plan, s);       \
+    }
+
+}  // namespace qg
