@@ -547,8 +547,8 @@ class _GradTensor(ctypes.Structure):
 class QGGradList:
     """The gradient tensors of a step, for qg_clip_grad_norm: made once, used every step.
 
-    It holds the tensors and their addresses on the device, so it is for buffers that stay where they are from
-    step to step.  outs: where the clipped gradients go, each of its gradient's size and type (default: in place).
+    It holds the tensors, their addresses on the device and a workspace, so it is for buffers that stay where they
+    are from step to step, and for one step at a time.  outs: where the clipped gradients go, each of its gradient's size and type (default: in place).
     """
 
     def __init__(self, grads, outs=None):
@@ -567,7 +567,7 @@ class QGGradList:
         self.grads, self.outs, self.count, self.chunks = grads, outs, len(grads), chunks.value
         device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
         self.table = torch.frombuffer(bytearray(host), dtype=torch.uint8).to(device)
-        self.workspace_bytes = lib().qg_clip_grad_norm_workspace_bytes(self.chunks)
+        self.workspace = torch.empty(lib().qg_clip_grad_norm_workspace_bytes(self.chunks), dtype=torch.uint8, device=device)
 
 
 def qg_clip_grad_norm_workspace_bytes(chunks: int) -> int:
@@ -582,9 +582,10 @@ def qg_clip_grad_norm(grads, max_norm, norm, *, eps=1e-6, workspace=None, stream
     """
     if not isinstance(grads, QGGradList):
         grads = QGGradList(grads)
-    st, wp, wb, _ = _stream_and_workspace(grads.workspace_bytes, workspace, grads.table, stream)
+    st, wp, wb, _ = _stream_and_workspace(0, grads.workspace if workspace is None else workspace, grads.table, stream)
     if stream is not None:
         grads.table.record_stream(stream)
+        grads.workspace.record_stream(stream)
     s = lib().qg_clip_grad_norm(_addr(grads.table), grads.count, grads.chunks, float(max_norm), float(eps), _addr(norm), wp,
                                 wb, st)
     return s if raw else _check(s, "qg_clip_grad_norm")

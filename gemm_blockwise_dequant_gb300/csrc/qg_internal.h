@@ -214,7 +214,7 @@ size_t dgrad_workspace_bytes(int dy_dtype, int M, int N, int K, int bits);
 cudaError_t dgrad(const GemmProblem &p, void *ws, cudaStream_t s);
 
 // Gradient norm and clipping (qg_clip.cu); the list is include/qgemm.h's qg_grad_tensor.
-int64_t clip_chunks(int64_t numel);
+int64_t clip_chunks(const void *grad, int64_t numel, int elem_size);
 size_t clip_workspace_bytes(int64_t chunks);
 cudaError_t clip_grad_norm(const void *list, int count, int64_t chunks, float max_norm, float eps, float *norm, void *ws,
                            cudaStream_t s);

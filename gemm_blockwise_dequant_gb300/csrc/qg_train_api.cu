@@ -222,7 +222,7 @@ int qg_grad_list_init(qg_grad_tensor *tensors_host, int count, int64_t *chunks) 
         if (!aligned(t.grad, esize(t.dtype)) || !aligned(t.out, esize(t.dtype))) return QG_ERR_INVALID_ARG;
         t.first_chunk = at;
         t.reserved = 0;
-        at += qg::clip_chunks(t.numel);
+        at += qg::clip_chunks(t.grad, t.numel, static_cast<int>(esize(t.dtype)));
         if (at > INT_MAX) return QG_ERR_UNSUPPORTED;
     }
     *chunks = at;
