@@ -20,6 +20,11 @@
 //    a one-CTA tile of the same size is bound by.
 //  * The codes and parameters go from global memory straight into registers,
 //    one step ahead; only dY needs the TMA.
+//  * fp32 dY: dY and the weight are each split in two fp16 terms and three of
+//    their four products are added in the same accumulator (TERMS = 2; the
+//    product of the second terms, 2^-22, is left out).  A row of dY is first
+//    scaled by a power of two, and all weights by one that their largest
+//    parameters give, so that neither term leaves fp16's range.
 //  * Tiles that do not fill a wave are split along n; their fp32 pieces are
 //    added in a fixed order by a second kernel.
 #include <algorithm>
@@ -58,6 +63,8 @@ struct DgradArgs {
     float *partial;
     int M, N, K, nb, lbs, steps, mt;
     int full_tiles, splits, split_steps;  // as TcArgs: whole tiles first, then the others split along n
+    const float *row_scale;  // TERMS = 2: what a row's sums are multiplied by, and the parameters' maxima
+    const float *maxima;
     unsigned *fault;
 };
 
@@ -146,12 +153,99 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
-constexpr int w_bufs() { return 4; }
-__host__ __device__ constexpr int a_slots(int h) {
-    const int n = (kSmemBudget - kSmemFixed - w_bufs() * kWBytes) / (h * kABytes);
+// Weight buffers: a multiple of kGroups, as a group must meet every phase of its buffers' barriers.
+__host__ __device__ constexpr int w_bufs(int terms) { return 4 / terms; }
+__host__ __device__ constexpr int a_slots(int h, int terms) {
+    const int n = (kSmemBudget - kSmemFixed - w_bufs(terms) * terms * kWBytes) / (h * terms * kABytes);
     return n > 8 ? 8 : n;
 }
-constexpr int smem_bytes(int h) { return kSmemFixed + w_bufs() * kWBytes + a_slots(h) * h * kABytes; }
+constexpr int smem_bytes(int h, int terms) {
+    return kSmemFixed + w_bufs(terms) * terms * kWBytes + a_slots(h, terms) * h * terms * kABytes;
+}
+
+// ------------------------------------------------------------------ fp32 dY: scales and terms
+constexpr int kMaxBlocks = 64;  // CTAs that look for the parameters' maxima
+
+// 2^e that brings `largest` to [2^14, 2^15); 1 for 0, infinity and NaN.
+__device__ __forceinline__ int scale_exponent(float largest) {
+    const int ef = static_cast<int>((__float_as_uint(largest) >> 23) & 0xFFu);
+    return ef == 0 || ef == 255 ? 0 : min(max(14 - (ef - 127), -100), 100);
+}
+
+// CTAs 0 .. M-1 split a row of dY; the others find the largest |scale| (absmax) and |zero point|.
+__global__ void __launch_bounds__(256) split_dy_kernel(const GemmProblem p, int ld, __half *__restrict__ hi, __half *__restrict__ lo,
+                                                       float *__restrict__ row_scale, float *__restrict__ maxima) {
+    __shared__ float red[2][8];
+    pdl_launch_dependents();
+    pdl_wait();
+    float mx = 0.f, mz = 0.f;
+    const int tid = threadIdx.x;
+    const float *dy = static_cast<const float *>(p.A) + static_cast<size_t>(blockIdx.x) * p.N;
+    const bool row = static_cast<int>(blockIdx.x) < p.M;
+    if (row) {
+        for (int n = tid; n < p.N; n += 256) mx = fmaxf(mx, fabsf(dy[n]));
+    } else {
+        const size_t total = static_cast<size_t>(p.N) * (p.K / p.bs);
+        const size_t first = static_cast<size_t>(blockIdx.x - p.M) * 256 + tid, stride = kMaxBlocks * 256;
+        if (p.kind == WK_CODEBOOK) {
+            for (size_t i = first; i < total; i += stride) mx = fmaxf(mx, fabsf(__ldg(p.absmax + i)));
+            if (tid < 16) mz = fabsf(__ldg(p.codebook + tid));
+        } else {
+            for (size_t i = first; i < total; i += stride) mx = fmaxf(mx, fabsf(h2f(__ldg(reinterpret_cast<const unsigned short *>(p.scales) + i))));
+            if (p.zp_mode == ZP_TENSOR)
+                for (size_t i = first; i < total; i += stride) mz = fmaxf(mz, fabsf(h2f(__ldg(reinterpret_cast<const unsigned short *>(p.zp) + i))));
+        }
+    }
+    for (int o = 16; o >= 1; o >>= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, o));
+    }
+    if ((tid & 31) == 0) red[0][tid >> 5] = mx, red[1][tid >> 5] = mz;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) mx = fmaxf(mx, red[0][w]), mz = fmaxf(mz, red[1][w]);
+    if (!row) {
+        if (tid == 0) maxima[blockIdx.x - p.M] = mx, maxima[kMaxBlocks + blockIdx.x - p.M] = mz;
+        return;
+    }
+    const int e = scale_exponent(mx);
+    if (tid == 0) row_scale[blockIdx.x] = exp2i(-e);
+    const float up = exp2i(e);
+    const size_t at = static_cast<size_t>(blockIdx.x) * ld;
+    for (int n = tid; n < ld; n += 256) {
+        const float x = n < p.N ? dy[n] * up : 0.f;
+        const __half h = __float2half_rn(x);
+        hi[at + n] = h;
+        lo[at + n] = __float2half_rn(x - __half2float(h));
+    }
+}
+
+// The exponent of all weights' scale, from the maxima (every thread of a warp calls it).
+__device__ __forceinline__ int weight_exponent(const float *maxima, bool codebook, int bits, bool zt, float zpv) {
+    const int lane = threadIdx.x & 31;
+    float mx = fmaxf(maxima[lane], maxima[lane + 32]), mz = fmaxf(maxima[kMaxBlocks + lane], maxima[kMaxBlocks + lane + 32]);
+    for (int o = 16; o >= 1; o >>= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, o));
+    }
+    return scale_exponent(codebook ? mx * mz : mx * (static_cast<float>((1 << bits) - 1) + (zt ? mz : fabsf(zpv))));
+}
+
+// Eight weights of a task (chunk q) in fp32, as the definition forms them, with the parameter already scaled.
+template <int WK, int BITS>
+__device__ __forceinline__ void weights8(const uint32_t (&c)[BITS], int q, float zp, float par, const float *lut_lane, float (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int bit = (q * 8 + i) * BITS;
+        const uint32_t code = (c[bit >> 5] >> (bit & 31)) & ((1u << BITS) - 1u);
+        w[i] = WK == WK_CODEBOOK ? __fmul_rn(lut_lane[code * 32], par) : __fmul_rn(__fsub_rn(static_cast<float>(code), zp), par);
+    }
+}
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b, float &ra, float &rb) {  // two fp16 values and what they leave
+    const __half2 h = __floats2half2_rn(a, b);
+    ra = a - __low2float(h), rb = b - __high2float(h);
+    return h2_as_u32(h);
+}
 
 // The codes and parameters of one task.
 template <int BITS>
@@ -160,15 +254,17 @@ struct Task {
     uint32_t par, zp;
 };
 
-template <int WK, int BITS, bool BF16, int PAIR, int H>
-__global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constant__ CUtensorMap dy_map, const DgradArgs p) {
-    constexpr int NA = a_slots(H), NW = w_bufs();
+template <int WK, int BITS, bool BF16, int PAIR, int H, int TERMS>
+__global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap dy_lo_map, const DgradArgs p) {
+    static_assert(TERMS == 1 || (!BF16 && H == 1), "the second term of dY takes the second half's place");
+    constexpr int NA = a_slots(H, TERMS), NW = w_bufs(TERMS);
+    constexpr int AT = H * TERMS * kABytes, WT = TERMS * kWBytes;  // of a step
     constexpr int BN = PAIR * kCols;
     constexpr uint32_t TMEM_COLS = H * BN;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    unsigned char *a_s = smem, *w_s = a_s + NA * H * kABytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(w_s + NW * kWBytes);  // dY of a step landed
+    unsigned char *a_s = smem, *w_s = a_s + NA * AT;
+    uint64_t *full = reinterpret_cast<uint64_t *>(w_s + NW * WT);  // dY of a step landed
     uint64_t *aempty = full + NA;    // its MMAs are done
     uint64_t *wfull = aempty + NA;   // weights of a step written (one arrival a warp)
     uint64_t *wempty = wfull + NW;   // their MMAs are done
@@ -176,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
     uint64_t *accf = pfull + NW;     // every MMA of the tile is done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float *lut = reinterpret_cast<float *>(w_s + NW * kWBytes + 512);  // 16 x 32 (codebook)
+    float *lut = reinterpret_cast<float *>(w_s + NW * WT + 512);  // 16 x 32 (codebook)
     static_assert((2 * NA + 3 * NW + 1) * 8 + 8 <= 512, "barriers fit");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -221,10 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
             for (int i = 0; i < ns; ++i) {
                 const int s = i % NA;
                 if (!mbar_wait(&aempty[s], ((i / NA) & 1) ^ 1, abort_flag, p.fault, FAULT_WAIT_TC)) break;
-                mbar_arrive_expect_tx(&full[s], H * kABytes);
+                mbar_arrive_expect_tx(&full[s], AT);
 #pragma unroll
                 for (int h = 0; h < H; ++h)  // rows past M and columns past N come as zeros
-                    tma_load_2d(a_s + (s * H + h) * kABytes, &dy_map, (s0 + i) * kBK, m0 + (h * PAIR + rank) * kRows, &full[s]);
+                    tma_load_2d(a_s + s * AT + h * kABytes, &dy_map, (s0 + i) * kBK, m0 + (h * PAIR + rank) * kRows, &full[s]);
+                if constexpr (TERMS == 2) tma_load_2d(a_s + s * AT + kABytes, &dy_lo_map, (s0 + i) * kBK, m0 + rank * kRows, &full[s]);
             }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -243,13 +340,18 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
                 if (PAIR == 2) ok = mbar_wait_cluster(&pfull[b], (i / NW) & 1, abort_flag, p.fault, FAULT_WAIT_TC);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t ad = sdesc_k128(smem_u32(a_s + s * H * kABytes));
-                const uint64_t ad1 = sdesc_k128(smem_u32(a_s + (s * H + H - 1) * kABytes));
-                const uint64_t bd = sdesc_mn128(smem_u32(w_s + b * kWBytes));
+                const uint64_t ad = sdesc_k128(smem_u32(a_s + s * AT));
+                const uint64_t ad1 = sdesc_k128(smem_u32(a_s + s * AT + AT - kABytes));
+                const uint64_t bd = sdesc_mn128(smem_u32(w_s + b * WT));
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k) {  // 16 n: 32 bytes along A's rows, two 8-row groups of B
                     mma<PAIR>(tmem, ad + 2 * k, bd + 128 * k, idesc, (i | k) != 0);
-                    if (two) mma<PAIR>(tmem + BN, ad1 + 2 * k, bd + 128 * k, idesc, (i | k) != 0);
+                    if constexpr (TERMS == 2) {
+                        mma<PAIR>(tmem, ad + 2 * k, bd + (kWBytes >> 4) + 128 * k, idesc, 1);
+                        mma<PAIR>(tmem, ad1 + 2 * k, bd + 128 * k, idesc, 1);
+                    } else if (two) {
+                        mma<PAIR>(tmem + BN, ad1 + 2 * k, bd + 128 * k, idesc, (i | k) != 0);
+                    }
                 }
                 commit<PAIR>(&aempty[s]);
                 commit<PAIR>(&wempty[b]);
@@ -301,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
         };
         const float *lut_lane = lut + lane;
         const uint32_t zpu = __half_as_ushort(__float2half_rn(p.zpv)) * 0x10001u;
+        float wscale = 1.f;
+        if constexpr (TERMS == 2) wscale = exp2i(weight_exponent(p.maxima, WK == WK_CODEBOOK, BITS, zt, p.zpv));
         Task<BITS> next;
         load(group, next);
         for (int i = group; i < ns; i += kGroups) {
@@ -316,7 +420,27 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
                     k.c[q + BITS / 2] = x;
                 }
             }
-            unsigned char *ws = w_s + b * kWBytes;
+            unsigned char *ws = w_s + b * WT;
+            if constexpr (TERMS == 2) {
+                const float par = (WK == WK_CODEBOOK ? __uint_as_float(k.par) : h2f(static_cast<uint16_t>(k.par))) * wscale;
+                const float zp = zt ? h2f(static_cast<uint16_t>(k.zp)) : p.zpv;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float w[8], l[8];
+                    uint32_t h[4];
+                    weights8<WK, BITS>(k.c, q, zp, par, lut_lane, w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = half_pair(w[2 * e], w[2 * e + 1], l[2 * e], l[2 * e + 1]);
+                    *reinterpret_cast<uint4 *>(ws + off[q]) = make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = h2_as_u32(__floats2half2_rn(l[2 * e], l[2 * e + 1]));
+                    *reinterpret_cast<uint4 *>(ws + kWBytes + off[q]) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wfull[b]);
+                continue;
+            }
             UnitPar up;
             up.lo = false;
             if constexpr (WK == WK_NBITS) {
@@ -358,6 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
             const int h = cc / BN, c0 = cc - h * BN;
             const int row = h * PAIR * kRows + rank * kRows + sub * 32 + lane, m = m0 + row, kc = k0 + c0;
             if (!ok || ns == 0 || m >= p.M || kc >= p.K) continue;  // K is a multiple of 32: a column group is in or out
+            if constexpr (TERMS == 2) {
+                const float rs = p.row_scale[m];
+#pragma unroll
+                for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * rs / wscale);
+            }
             if (piece >= 0) {
                 float4 *dst = reinterpret_cast<float4 *>(p.partial + (static_cast<size_t>(piece) * (H * PAIR * kRows) + row) * BN + c0);
 #pragma unroll
@@ -482,20 +611,21 @@ __global__ void __launch_bounds__(256) dgrad_simple_kernel(const GemmProblem p) 
 
 // ------------------------------------------------------------------ host side
 struct Plan {
-    int pair, h, rows, bn, mt, kt, steps;
+    int pair, h, terms, rows, bn, mt, kt, steps;
     int full_tiles, tail_tiles, splits, split_steps;
-    size_t partial_bytes, pad_bytes;
+    size_t partial_bytes, copy_bytes, front_bytes;  // pieces; one 16-bit copy of dY; everything before the pieces
     int ld;
 };
 
 // Rows decide the tile: up to 128 rows one CTA a tile (128 x 128), up to 256 a
-// pair (256 x 256), above that two halves a pair (512 x 256).  Whole tiles fill
-// complete waves, the others are split along n over the SMs, at least four
-// steps a piece.
-Plan make_plan(int M, int N, int K) {
+// pair (256 x 256), above that two halves a pair (512 x 256; fp32 dY needs the
+// second half's room for its second term).  Whole tiles fill complete waves, the
+// others are split along n over the SMs, at least four steps a piece.
+Plan make_plan(int dy_dtype, int M, int N, int K) {
     Plan c{};
+    c.terms = dy_dtype == 0 ? 2 : 1;
     c.pair = M <= kRows ? 1 : 2;
-    c.h = M <= 2 * kRows ? 1 : 2;
+    c.h = M <= 2 * kRows || c.terms == 2 ? 1 : 2;
     c.rows = c.pair * c.h * kRows;
     c.bn = c.pair * kCols;
     c.mt = (M + c.rows - 1) / c.rows;
@@ -514,71 +644,85 @@ Plan make_plan(int M, int N, int K) {
     }
     if (c.splits > 1) c.partial_bytes = sizeof(float) * c.tail_tiles * c.splits * static_cast<size_t>(c.rows) * c.bn;
     c.ld = (N + 7) / 8 * 8;
-    if (c.ld != N) c.pad_bytes = (static_cast<size_t>(M) * c.ld * 2 + 255) / 256 * 256;
+    if (c.ld != N || c.terms == 2) c.copy_bytes = (static_cast<size_t>(M) * c.ld * 2 + 255) / 256 * 256;
+    c.front_bytes = c.terms * c.copy_bytes;
+    if (c.terms == 2) c.front_bytes += (static_cast<size_t>(M) * 4 + 255) / 256 * 256 + 2 * kMaxBlocks * 4;
     return c;
 }
 
-// 3-bit codes and fp32 dY take the plain kernel.
-bool tensor_cores(int dy_dtype, int bits) { return dy_dtype != 0 && bits != 3 && encode_fn() != nullptr; }
+// 3-bit codes take the plain kernel.
+bool tensor_cores(int bits) { return bits != 3 && encode_fn() != nullptr; }
 
-template <int WK, int BITS, bool BF16, int PAIR, int H>
-cudaError_t launch(const CUtensorMap &map, const DgradArgs &a, int tiles, cudaStream_t s) {
-    auto kern = dgrad_kernel<WK, BITS, BF16, PAIR, H>;
+template <int WK, int BITS, bool BF16, int PAIR, int H, int TERMS = 1>
+cudaError_t launch(const CUtensorMap *maps, const DgradArgs &a, int tiles, cudaStream_t s) {
+    auto kern = dgrad_kernel<WK, BITS, BF16, PAIR, H, TERMS>;
     static std::atomic<unsigned long long> configured{0};
     const int slot = device_slot();
     const unsigned long long bit = slot < 0 ? 0 : 1ull << slot;
     if (!(configured.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(H));
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(H, TERMS));
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_cluster(kern, dim3(tiles * PAIR), dim3(kThreads), smem_bytes(H), s, PAIR, map, a);
+    return launch_cluster(kern, dim3(tiles * PAIR), dim3(kThreads), smem_bytes(H, TERMS), s, PAIR, maps[0], maps[1], a);
 }
 
 template <int WK, int BITS, bool BF16>
-cudaError_t launch_shape(const Plan &c, const CUtensorMap &map, const DgradArgs &a, cudaStream_t s) {
+cudaError_t launch_shape(const Plan &c, const CUtensorMap *maps, const DgradArgs &a, cudaStream_t s) {
     const int tiles = c.full_tiles + c.tail_tiles * c.splits;
-    if (c.pair == 1) return launch<WK, BITS, BF16, 1, 1>(map, a, tiles, s);
-    return c.h == 1 ? launch<WK, BITS, BF16, 2, 1>(map, a, tiles, s) : launch<WK, BITS, BF16, 2, 2>(map, a, tiles, s);
+    if constexpr (!BF16)
+        if (c.terms == 2) return c.pair == 1 ? launch<WK, BITS, false, 1, 1, 2>(maps, a, tiles, s) : launch<WK, BITS, false, 2, 1, 2>(maps, a, tiles, s);
+    if (c.pair == 1) return launch<WK, BITS, BF16, 1, 1>(maps, a, tiles, s);
+    return c.h == 1 ? launch<WK, BITS, BF16, 2, 1>(maps, a, tiles, s) : launch<WK, BITS, BF16, 2, 2>(maps, a, tiles, s);
 }
 
 template <bool BF16>
-cudaError_t launch_kind(const GemmProblem &p, const Plan &c, const CUtensorMap &map, const DgradArgs &a, cudaStream_t s) {
-    if (p.kind == WK_CODEBOOK) return launch_shape<WK_CODEBOOK, 4, BF16>(c, map, a, s);
-    if (p.bits == 2) return launch_shape<WK_NBITS, 2, BF16>(c, map, a, s);
-    if (p.bits == 4) return launch_shape<WK_NBITS, 4, BF16>(c, map, a, s);
-    return launch_shape<WK_NBITS, 8, BF16>(c, map, a, s);
+cudaError_t launch_kind(const GemmProblem &p, const Plan &c, const CUtensorMap *maps, const DgradArgs &a, cudaStream_t s) {
+    if (p.kind == WK_CODEBOOK) return launch_shape<WK_CODEBOOK, 4, BF16>(c, maps, a, s);
+    if (p.bits == 2) return launch_shape<WK_NBITS, 2, BF16>(c, maps, a, s);
+    if (p.bits == 4) return launch_shape<WK_NBITS, 4, BF16>(c, maps, a, s);
+    return launch_shape<WK_NBITS, 8, BF16>(c, maps, a, s);
 }
 
 }  // namespace
 
 size_t dgrad_workspace_bytes(int dy_dtype, int M, int N, int K, int bits) {
-    if (!tensor_cores(dy_dtype, bits)) return 0;
-    const Plan c = make_plan(M, N, K);
-    return c.pad_bytes + c.partial_bytes;
+    if (!tensor_cores(bits)) return 0;
+    const Plan c = make_plan(dy_dtype, M, N, K);
+    return c.front_bytes + c.partial_bytes;
 }
 
 cudaError_t dgrad(const GemmProblem &p, void *ws, cudaStream_t s) {
-    if (!tensor_cores(p.a_dtype, p.bits)) {
+    if (!tensor_cores(p.bits)) {
         const cudaError_t e = launch_pdl(dgrad_simple_kernel, dim3((p.K + 63) / 64, (p.M + 63) / 64), dim3(256), 0, s, p);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
-    const Plan c = make_plan(p.M, p.N, p.K);
-    const void *dy = p.A;
+    const Plan c = make_plan(p.a_dtype, p.M, p.N, p.K);
+    char *w = static_cast<char *>(ws);
+    const void *dy[2] = {p.A, p.A};  // the terms that the tensor maps read
+    float *row_scale = nullptr, *maxima = nullptr;
     cudaError_t e = cudaSuccess;
-    if (c.pad_bytes) {
+    if (c.terms == 2) {
+        dy[0] = w;
+        dy[1] = w + c.copy_bytes;
+        maxima = reinterpret_cast<float *>(w + 2 * c.copy_bytes);
+        row_scale = maxima + 2 * kMaxBlocks;
+        e = launch_pdl(split_dy_kernel, dim3(p.M + kMaxBlocks), dim3(256), 0, s, p, c.ld, reinterpret_cast<__half *>(w),
+                       reinterpret_cast<__half *>(w + c.copy_bytes), row_scale, maxima);
+    } else if (c.copy_bytes) {
+        dy[0] = dy[1] = w;
         e = launch_pdl(pad_rows_kernel, dim3(p.M), dim3(256), 0, s, static_cast<const uint16_t *>(p.A), p.N, c.ld, static_cast<uint16_t *>(ws));
-        if (e != cudaSuccess) return e;
-        dy = ws;
     }
-    CUtensorMap map;
+    if (e != cudaSuccess) return e;
+    CUtensorMap maps[2];
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.ld), static_cast<cuuint64_t>(p.M)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.ld) * 2};
     const cuuint32_t box[2] = {kBK, kRows}, es[2] = {1, 1};
-    if (encode_fn()(&map, p.a_dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(dy),
-                    dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    for (int i = 0; i < 2; ++i)
+        if (encode_fn()(&maps[i], p.a_dtype == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                        const_cast<void *>(dy[i]), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
     DgradArgs a{};
     a.W = p.W;
     a.par = p.kind == WK_CODEBOOK ? static_cast<const void *>(p.absmax) : static_cast<const void *>(p.scales);
@@ -588,7 +732,9 @@ cudaError_t dgrad(const GemmProblem &p, void *ws, cudaStream_t s) {
     a.codebook = p.codebook;
     a.dX = p.Y;
     a.x_dtype = p.y_dtype;
-    a.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + c.pad_bytes);
+    a.partial = reinterpret_cast<float *>(w + c.front_bytes);
+    a.row_scale = row_scale;
+    a.maxima = maxima;
     a.M = p.M;
     a.N = p.N;
     a.K = p.K;
@@ -600,7 +746,7 @@ cudaError_t dgrad(const GemmProblem &p, void *ws, cudaStream_t s) {
     a.splits = c.splits;
     a.split_steps = c.split_steps;
     a.fault = fault_word();
-    e = p.a_dtype == 2 ? launch_kind<true>(p, c, map, a, s) : launch_kind<false>(p, c, map, a, s);
+    e = p.a_dtype == 2 ? launch_kind<true>(p, c, maps, a, s) : launch_kind<false>(p, c, maps, a, s);
     if (e != cudaSuccess) return e;
     if (c.splits > 1) {
         const int64_t work = static_cast<int64_t>(c.tail_tiles) * c.rows * (c.bn / 4);
