@@ -119,6 +119,25 @@ __device__ __forceinline__ bool find_tile(const LoraProblem &p, int tile, int si
     return !bad;
 }
 
+// A lane's queue in shared memory.  A lane copies ahead exactly the bytes that it
+// will read itself, so nothing but its own cp.async groups has to be waited for,
+// and the loads in flight do not occupy registers.  What lies outside is written as zeros.
+template <int BYTES>
+__device__ __forceinline__ void queue_copy(void *dst, const void *src, bool in) {
+    const uint32_t n = in ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void queue_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void queue_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 

@@ -52,90 +52,93 @@ struct RowsKernel {
     static constexpr int RC = 8 * NT;              // rank values of one pass of the first product
     static constexpr int PS = RC + 4;              // row stride of the partial sums (bank spread)
 
-    // 16 bytes of a row (EL values from k on), zero past the end
-    static __device__ __forceinline__ uint4 load_in(const RowsArgs &q, const char *row, int k, bool row_in) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (!row_in) return v;
-        if (q.in_vec && k + EL <= q.c1) return __ldg(reinterpret_cast<const uint4 *>(row + static_cast<size_t>(k) * (NATIVE ? 2 : 4)));
-        uint32_t w[4] = {0, 0, 0, 0};
-        if constexpr (NATIVE) {
-            const unsigned short *x = reinterpret_cast<const unsigned short *>(row);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (k + e < q.c1) w[e >> 1] |= static_cast<uint32_t>(__ldg(x + k + e)) << (16 * (e & 1));
-        } else {
-            const unsigned int *x = reinterpret_cast<const unsigned int *>(row);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (k + e < q.c1) w[e] = __ldg(x + k + e);
+    static constexpr int PIECES = 4 * MT;          // 16-byte pieces of a lane and block: chunk, row group, row half
+    static constexpr int STAGES = 3;
+
+    // Puts 16 bytes of a row (EL values from k on) into the lane's queue, zeros past the end.
+    static __device__ __forceinline__ void queue_in(const RowsArgs &q, uint4 *dst, const char *row, int k, bool row_in) {
+        if (q.in_vec) {  // the last piece of a row that ends inside it is left to the loads below
+            if (!row_in || k >= q.c1 || k + EL <= q.c1) {
+                const bool in = row_in && k < q.c1;
+                queue_copy<16>(dst, row + (in ? static_cast<size_t>(k) * (NATIVE ? 2 : 4) : 0), in);
+                return;
+            }
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (row_in) {
+            if constexpr (NATIVE) {
+                const unsigned short *x = reinterpret_cast<const unsigned short *>(row);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (k + e < q.c1) w[e >> 1] |= static_cast<uint32_t>(__ldg(x + k + e)) << (16 * (e & 1));
+            } else {
+                const unsigned int *x = reinterpret_cast<const unsigned int *>(row);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (k + e < q.c1) w[e] = __ldg(x + k + e);
+            }
+        }
+        *dst = make_uint4(w[0], w[1], w[2], w[3]);
     }
 
-    // The adapter's values of a lane's chunk for rank columns: w[i][...] of tile i.
-    // NATIVE: 4 words, word x = values 2x, 2x+1 of the contraction.  TF32: 4
-    // values as fp32 bits.
-    static __device__ __forceinline__ void load_w1(const RowsArgs &q, int a, int j0, int ntr, int k, int g, uint32_t (&w)[NT][4]) {
+    // The adapter's values of a lane's chunk.  Forward: A[a][j][k ..], the lane
+    // column g of tile i is j = j0 + 8 i + g; w.v[i] is what tile i's MMAs take.
+    // Backward: B[a][k + e][j], j = j0 + g NT + i, NT contiguous values of EL rows.
+    struct W1 {
+        uint32_t v[BWD ? EL : NT][BWD ? (WT == kF32 ? NT : NT / 2) : 4];
+    };
+
+    static __device__ __forceinline__ void load_w1(const RowsArgs &q, int a, int j0, int k, int g, W1 &w) {
         const int r = q.p.r;
-        if constexpr (!BWD) {  // A[a][j][k ..]: j = j0 + 8 i + g
+        if constexpr (!BWD) {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
-                if (i >= ntr || k >= q.c1) continue;
+                w.v[i][0] = w.v[i][1] = w.v[i][2] = w.v[i][3] = 0;
+                if (j0 + 8 * i >= r || k >= q.c1) continue;  // the rank is a multiple of 8
                 const size_t at = (static_cast<size_t>(a) * r + j0 + 8 * i + g) * q.c1 + k;
                 if constexpr (WT == kF32 || NATIVE) {
                     const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(q.w1) + at * (NATIVE ? 2 : 4)));
-                    w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+                    w.v[i][0] = v.x, w.v[i][1] = v.y, w.v[i][2] = v.z, w.v[i][3] = v.w;
                 } else {
                     const uint2 v = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(q.w1) + at));
-                    widen(v.x, w[i][0], w[i][1]);
-                    widen(v.y, w[i][2], w[i][3]);
+                    widen(v.x, w.v[i][0], w.v[i][1]);
+                    widen(v.y, w.v[i][2], w.v[i][3]);
                 }
             }
-        } else {  // B[a][k + e][j]: j = j0 + g ntr + i, ntr contiguous values
-            const size_t at = (static_cast<size_t>(a) * q.c1 + k) * r + j0 + g * ntr;
-            uint32_t raw[EL][NT];  // 16-bit values, or fp32 bits
+        } else {
+            constexpr int WORDS = WT == kF32 ? NT : NT / 2;
+            const bool jin = j0 + g * NT < r;  // a multiple of 8: the NT values are in or out
+            const char *src = static_cast<const char *>(q.w1) + ((static_cast<size_t>(a) * q.c1 + k) * r + j0 + g * NT) * (WT == kF32 ? 4 : 2);
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
-                const bool in = k + e < q.c1;
-                const size_t o = at + static_cast<size_t>(e) * r;
+                const bool in = jin && k + e < q.c1;
+                const char *x = src + static_cast<size_t>(e) * r * (WT == kF32 ? 4 : 2);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) raw[e][i] = 0;
+                for (int o = 0; o < WORDS; ++o) w.v[e][o] = 0;
                 if (!in) continue;
-                if constexpr (WT == kF32) {
-                    const unsigned int *s = static_cast<const unsigned int *>(q.w1) + o;
+                if constexpr (WORDS % 4 == 0) {
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        if (i < ntr) raw[e][i] = __ldg(s + i);
-                } else {
-                    const unsigned short *s = static_cast<const unsigned short *>(q.w1) + o;
-                    if (ntr == NT && NT == 2) {
-                        const uint32_t v = __ldg(reinterpret_cast<const unsigned int *>(s));
-                        raw[e][0] = v & 0xFFFFu, raw[e][1 % NT] = v >> 16;
-                    } else if (ntr == NT && NT == 4) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(s));
-                        raw[e][0] = v.x & 0xFFFFu, raw[e][1 % NT] = v.x >> 16, raw[e][2 % NT] = v.y & 0xFFFFu, raw[e][3 % NT] = v.y >> 16;
-                    } else if (ntr == NT && NT == 8) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(s));
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) raw[e][i] = (i & 1) ? u[(i >> 1) & 3] >> 16 : u[(i >> 1) & 3] & 0xFFFFu;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-                            if (i < ntr) raw[e][i] = __ldg(s + i);
+                    for (int o = 0; o < WORDS; o += 4) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x) + o / 4);
+                        w.v[e][o] = v.x, w.v[e][o + 1] = v.y, w.v[e][o + 2] = v.z, w.v[e][o + 3] = v.w;
                     }
+                } else if constexpr (WORDS == 2) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(x));
+                    w.v[e][0] = v.x, w.v[e][1] = v.y;
+                } else {
+                    w.v[e][0] = __ldg(reinterpret_cast<const unsigned int *>(x));
                 }
             }
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if constexpr (NATIVE) w[i][x] = pack2(raw[2 * x][i], raw[2 * x + 1][i]);
-                    else if constexpr (WT == kF32) w[i][x] = raw[x][i];
-                    else w[i][x] = __float_as_uint(to_float<WT>(static_cast<uint16_t>(raw[x][i])));
-                }
         }
+    }
+
+    // What tile i's MMAs take: NATIVE word x = values 2x, 2x + 1 of the
+    // contraction; TF32 value x.
+    static __device__ __forceinline__ uint32_t w1_word(const W1 &w, int i, int x) {
+        if constexpr (!BWD) return w.v[i][x];
+        else if constexpr (NATIVE) return __byte_perm(w.v[2 * x][i / 2], w.v[2 * x + 1][i / 2], (i & 1) ? 0x7632u : 0x5410u);
+        else if constexpr (WT == kF32) return w.v[x][i];
+        else return __float_as_uint(to_float<WT>(static_cast<uint16_t>((i & 1) ? w.v[x][i / 2] >> 16 : w.v[x][i / 2] & 0xFFFFu)));
     }
 
     static __device__ __forceinline__ void widen(uint32_t v, uint32_t &a, uint32_t &b) {  // two 16-bit values to fp32 bits
@@ -225,25 +228,33 @@ struct RowsKernel {
 
     static __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-    // Shared memory: the warps' partial sums (later the operand fragments of the
-    // second product), the CTA's sums (read by the cluster), the rows' whole sums
-    // and their scales.
+    // Shared memory.  First product: the lanes' queues.  Then: the CTA's sums
+    // (read by the cluster), the rows' whole sums and their scales, and behind
+    // them the warps' partial sums, later the operand fragments of the second
+    // product and the queues of its base rows.
     static __host__ __device__ int rank_pad(int r) { return (r + UW - 1) / UW * UW; }
-    static __host__ __device__ int part_bytes(int r) {
-        const int part = KG * R * PS * 4, frag = (R / 16) * (rank_pad(r) / UW) * 2 * 512;
-        return part > frag ? part : frag;
+    static __host__ __device__ int sums_bytes(int r) { return 2 * R * rank_pad(r) * 4 + R * 4; }
+    static __host__ __device__ int frag_bytes(int r) { return (R / 16) * (rank_pad(r) / UW) * 2 * 512; }
+    static constexpr int PART_BYTES = KG * R * PS * 4;
+    static constexpr int IN_BYTES = 8 * STAGES * PIECES * 512;
+    static constexpr int BW = NATIVE ? 1 : 2;       // 16-byte pieces of 8 base values in the activations' type
+    static constexpr int BASE_PIECES = 2 * MT * BW;  // of a lane and group
+    static constexpr int BASE_BYTES = 8 * STAGES * BASE_PIECES * 512;
+    static __host__ __device__ int queue_offset(int r) { return r > RC ? sums_bytes(r) : 0; }  // several passes: their sums stay
+    static __host__ __device__ int smem_bytes(int r) {
+        const int later = PART_BYTES > frag_bytes(r) + BASE_BYTES ? PART_BYTES : frag_bytes(r) + BASE_BYTES;
+        return sums_bytes(r) + later > queue_offset(r) + IN_BYTES ? sums_bytes(r) + later : queue_offset(r) + IN_BYTES;
     }
-    static __host__ __device__ int smem_bytes(int r) { return part_bytes(r) + 2 * R * rank_pad(r) * 4 + R * 4; }
 
     static __device__ void run(const RowsArgs &q) {
         extern __shared__ __align__(16) unsigned char sm[];
         const LoraProblem &p = q.p;
         const int r = p.r, rp = rank_pad(r);
-        float *part = reinterpret_cast<float *>(sm);
-        uint4 *frag = reinterpret_cast<uint4 *>(sm);
-        float *mine = reinterpret_cast<float *>(sm + part_bytes(r));
+        float *mine = reinterpret_cast<float *>(sm);
         float *whole = mine + R * rp;
         float *rscale = whole + R * rp;
+        float *part = rscale + R;
+        uint4 *frag = reinterpret_cast<uint4 *>(part);
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
         const int rg = warp / KG, kg = warp % KG;
         const int rank = blockIdx.x % q.cs, tile = blockIdx.x / q.cs;
@@ -253,8 +264,12 @@ struct RowsKernel {
         if (!find_tile(p, tile, R, blockIdx.x == 0, t) || t.rows == 0) return;  // the same for the whole cluster
         const float scale = t.adapter >= 0 && p.scaling ? __ldg(p.scaling + t.adapter) : 1.f;
 
+        const int ngrp = (q.c2 + 31) / 32;  // 32-column groups of the second product, and this CTA's
+        const int n_lo = static_cast<int>(static_cast<int64_t>(ngrp) * rank / q.cs), n_hi = static_cast<int>(static_cast<int64_t>(ngrp) * (rank + 1) / q.cs);
+
         if (t.adapter >= 0) {
             // ---------------------------------------------------------- first product
+            if (R == 16 && q.out) prefetch_w2(q, t.adapter, n_lo * 32, min(n_hi * 32, q.c2));
             const int nblk = (q.c1 + BLK - 1) / BLK;
             const int b0 = static_cast<int>(static_cast<int64_t>(nblk) * rank / q.cs), b1 = static_cast<int>(static_cast<int64_t>(nblk) * (rank + 1) / q.cs);
             const int row0 = rg * 16 * MT;
@@ -269,28 +284,40 @@ struct RowsKernel {
                     rowp[m][h] = static_cast<const char *>(q.in) + static_cast<size_t>(t.t0 + (rin[m][h] ? row : 0)) * q.ld_in * (NATIVE ? 2 : 4);
                 }
             for (int j0 = 0; j0 < r; j0 += RC) {
-                const int ntr = min(NT, (r - j0) / 8);
                 float acc[MT][NT][4] = {};
+                uint4 *queue = reinterpret_cast<uint4 *>(sm + queue_offset(r)) + warp * (STAGES * PIECES * 32) + lane;
+                auto ahead = [&](int b, int slot) {
+                    if (b < b1) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    queue_in(q, queue + (slot * PIECES + (s * MT + m) * 2 + h) * 32, rowp[m][h], b * BLK + s * CH + c * EL, rin[m][h]);
+                    }
+                    queue_commit();
+                };
+                if (j0) __syncthreads();  // the queues lie over the partial sums of the previous pass
+#pragma unroll
+                for (int i = 0; i < STAGES - 1; ++i) ahead(b0 + kg + i * KG, i);
+                int slot = 0;
                 for (int b = b0 + kg; b < b1; b += KG) {
-                    uint4 x[2][MT][2];
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) x[s][m][h] = load_in(q, rowp[m][h], b * BLK + s * CH + c * EL, rin[m][h]);
+                    ahead(b + (STAGES - 1) * KG, slot == 0 ? STAGES - 1 : slot - 1);
+                    queue_wait<STAGES - 1>();
+                    const uint4 *x = queue + slot * PIECES * 32;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        uint32_t w[NT][4];
-                        load_w1(q, t.adapter, j0, ntr, b * BLK + s * CH + c * EL, g, w);
+                        W1 w;
+                        load_w1(q, t.adapter, j0, b * BLK + s * CH + c * EL, g, w);
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            const uint4 x0 = x[s][m][0], x1 = x[s][m][1];
+                            const uint4 x0 = x[((s * MT + m) * 2) * 32], x1 = x[((s * MT + m) * 2 + 1) * 32];
                             if constexpr (NATIVE) {
 #pragma unroll
                                 for (int i = 0; i < NT; ++i) {
-                                    mma16<XT>(acc[m][i], x0.x, x1.x, x0.y, x1.y, w[i][0], w[i][1]);
-                                    mma16<XT>(acc[m][i], x0.z, x1.z, x0.w, x1.w, w[i][2], w[i][3]);
+                                    mma16<XT>(acc[m][i], x0.x, x1.x, x0.y, x1.y, w1_word(w, i, 0), w1_word(w, i, 1));
+                                    mma16<XT>(acc[m][i], x0.z, x1.z, x0.w, x1.w, w1_word(w, i, 2), w1_word(w, i, 3));
                                 }
                             } else {
 #pragma unroll
@@ -301,13 +328,16 @@ struct RowsKernel {
                                     split_tf32(__uint_as_float(half ? x0.w : x0.y), hi[2], lo[2]);
                                     split_tf32(__uint_as_float(half ? x1.w : x1.y), hi[3], lo[3]);
 #pragma unroll
-                                    for (int i = 0; i < NT; ++i) mma_tf32_split(acc[m][i], hi, lo, w[i][2 * half], w[i][2 * half + 1]);
+                                    for (int i = 0; i < NT; ++i) mma_tf32_split(acc[m][i], hi, lo, w1_word(w, i, 2 * half), w1_word(w, i, 2 * half + 1));
                                 }
                             }
                         }
                     }
+                    slot = slot == STAGES - 1 ? 0 : slot + 1;
                 }
-                if (j0) __syncthreads();  // the previous pass has read its partial sums
+                queue_wait<0>();
+                __syncthreads();  // every lane is done with its queue
+                const int jn = min(RC, r - j0);
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -315,12 +345,11 @@ struct RowsKernel {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int col = 2 * c + (e & 1), row = row0 + m * 16 + (e >> 1) * 8 + g;
-                            const int j = BWD ? col * ntr + i : i * 8 + col;
-                            if (i < ntr) part[(kg * R + row) * PS + j] = acc[m][i][e];
+                            part[(kg * R + row) * PS + (BWD ? col * NT + i : i * 8 + col)] = acc[m][i][e];
                         }
                 __syncthreads();
-                for (int e = tid; e < R * 8 * ntr; e += 256) {
-                    const int row = e / (8 * ntr), j = e - row * 8 * ntr;
+                for (int e = tid; e < R * jn; e += 256) {
+                    const int row = e / jn, j = e - row * jn;
                     float s = 0.f;
 #pragma unroll
                     for (int w = 0; w < KG; ++w) s += part[(w * R + row) * PS + j];
@@ -390,8 +419,7 @@ struct RowsKernel {
 
         // -------------------------------------------------------------- second product
         if (q.out) {
-            const int ngrp = (q.c2 + 31) / 32, units = rp / UW;
-            const int n_lo = static_cast<int>(static_cast<int64_t>(ngrp) * rank / q.cs), n_hi = static_cast<int>(static_cast<int64_t>(ngrp) * (rank + 1) / q.cs);
+            const int units = rp / UW;
             const int row0 = rg * 16 * MT;
             float mul[MT][2];
 #pragma unroll
@@ -401,14 +429,32 @@ struct RowsKernel {
                     mul[m][h] = BWD ? 1.f : scale;
                     if (NATIVE && t.adapter >= 0) mul[m][h] *= rscale[row0 + m * 16 + h * 8 + g];
                 }
+            // the base rows ahead of their sums, when they have the activations' width
+            uint4 *queue = reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(frag) + frag_bytes(r)) + warp * (STAGES * BASE_PIECES * 32) + lane;
+            const bool queued = q.base && q.out_vec && (q.base_dtype == kF32) == !NATIVE;
+            auto ahead = [&](int b, int slot) {
+                const int n = b * 32 + c * 8;
+                if (queued && b < n_hi && n + 8 <= q.c2) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int row = row0 + m * 16 + h * 8 + g;
+                            const bool in = row < t.rows;
+                            const char *src = static_cast<const char *>(q.base) + (in ? (static_cast<size_t>(t.t0 + row) * q.ld_base + n) * (NATIVE ? 2 : 4) : 0);
+#pragma unroll
+                            for (int o = 0; o < BW; ++o) queue_copy<16>(queue + (slot * BASE_PIECES + (m * 2 + h) * BW + o) * 32, src + 16 * o, in);
+                        }
+                }
+                queue_commit();
+            };
+#pragma unroll
+            for (int i = 0; i < STAGES - 1; ++i) ahead(n_lo + kg + i * KG, i);
+            int slot = 0;
             for (int b = n_lo + kg; b < n_hi; b += KG) {
+                ahead(b + (STAGES - 1) * KG, slot == 0 ? STAGES - 1 : slot - 1);
                 const int n0 = b * 32, n = n0 + c * 8;
                 const bool vec = q.out_vec && n + 8 <= q.c2;
-                float base[MT][2][8];
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) load_base(q, t.t0 + row0 + m * 16 + h * 8 + g, row0 + m * 16 + h * 8 + g < t.rows, n, vec, base[m][h]);
                 float acc[MT][4][4] = {};
                 if (t.adapter >= 0)
                     for (int u = 0; u < units; ++u) {
@@ -430,6 +476,7 @@ struct RowsKernel {
                             }
                         }
                     }
+                queue_wait<STAGES - 1>();
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -437,10 +484,15 @@ struct RowsKernel {
                         const int row = row0 + m * 16 + h * 8 + g;
                         if (row >= t.rows) continue;
                         float y[8];
+                        if (queued && vec) take_base(q, queue + (slot * BASE_PIECES + (m * 2 + h) * BW) * 32, y);
+                        else load_base(q, t.t0 + row, n, vec, y);
+                        if (t.adapter >= 0) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = t.adapter >= 0 ? fmaf(acc[m][e >> 1][h * 2 + (e & 1)], mul[m][h], base[m][h][e]) : base[m][h][e];
+                            for (int e = 0; e < 8; ++e) y[e] = fmaf(acc[m][e >> 1][h * 2 + (e & 1)], mul[m][h], y[e]);
+                        }
                         store_out(q, t.t0 + row, n, vec, y);
                     }
+                slot = slot == STAGES - 1 ? 0 : slot + 1;
             }
         }
         if (q.cs > 1 && t.adapter >= 0) {
@@ -449,10 +501,43 @@ struct RowsKernel {
         }
     }
 
-    static __device__ __forceinline__ void load_base(const RowsArgs &q, int t, bool in, int n, bool vec, float (&v)[8]) {
+    // What the second product will read of its adapter, into the L2 while the first one runs.
+    static __device__ __forceinline__ void prefetch_w2(const RowsArgs &q, int a, int n_lo, int n_hi) {
+        constexpr int WS = WT == kF32 ? 4 : 2;
+        const int r = q.p.r;
+        if (n_hi <= n_lo) return;
+        const char *w = static_cast<const char *>(q.w2) + static_cast<size_t>(a) * r * q.c2 * WS;
+        const size_t row = static_cast<size_t>(BWD ? n_hi - n_lo : (n_hi - n_lo) * r) * WS;  // contiguous bytes
+        const int lines = static_cast<int>((row + 127) / 128), rows = BWD ? r : 1;
+        for (int e = threadIdx.x; e < lines * rows; e += 256) {
+            const int j = e / lines, l = e - j * lines;
+            const size_t off = min(static_cast<size_t>(l) * 128, row - 1);
+            prefetch_l2(w + (BWD ? (static_cast<size_t>(j) * q.c2 + n_lo) : static_cast<size_t>(n_lo) * r) * WS + off);
+        }
+    }
+
+    // 8 base values from the lane's queue
+    static __device__ __forceinline__ void take_base(const RowsArgs &q, const uint4 *from, float (&v)[8]) {
+        const uint4 a = from[0];
+        if constexpr (NATIVE) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t x = word(a, i);
+                const uint16_t x0 = static_cast<uint16_t>(x & 0xFFFFu), x1 = static_cast<uint16_t>(x >> 16);
+                v[2 * i] = q.base_dtype == kF16 ? h2f(x0) : bf2f(x0);
+                v[2 * i + 1] = q.base_dtype == kF16 ? h2f(x1) : bf2f(x1);
+            }
+        } else {
+            const uint4 b = from[32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(word(a, i)), v[4 + i] = __uint_as_float(word(b, i));
+        }
+    }
+
+    static __device__ __forceinline__ void load_base(const RowsArgs &q, int t, int n, bool vec, float (&v)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        if (!in || !q.base) return;
+        if (!q.base) return;
         const size_t at = static_cast<size_t>(t) * q.ld_base + n;
         if (vec) {
             if (q.base_dtype == kF32) {

@@ -40,7 +40,10 @@ struct WgradKernel {
     static constexpr int QS = NATIVE ? kWgChunk + 16 : kWgChunk + 16;  // row stride of the staged factor: banks of 8 (4) rows differ
     static constexpr int QBYTES = RJ * QS * (NATIVE ? 2 : 4);          // one term
     static constexpr int OS = COLS + 4;                                // row stride of the sums
-    static constexpr int SMEM = (4 * QBYTES > RJ * OS * 4) ? 4 * QBYTES : RJ * OS * 4;
+    static constexpr int PB = CPL * (XT == kF32 ? 4 : 2);              // bytes of a lane's piece of a row: 16 or 8
+    static constexpr int STAGES = 3;
+    static constexpr int WIDE_BYTES = 8 * STAGES * 8 * 32 * PB;        // the lanes' queues: 8 rows a step
+    static constexpr int SMEM = (4 * QBYTES + WIDE_BYTES > RJ * OS * 4) ? 4 * QBYTES + WIDE_BYTES : RJ * OS * 4;
     static constexpr int QPT = kWgChunk * RJ / 256;                    // staged values of a thread
 
     // Walks the 64-row chunks of the adapter's requests.
@@ -79,27 +82,19 @@ struct WgradKernel {
         }
     }
 
-    static __device__ __forceinline__ void load_wide(const WgradArgs &q, int which, int t, bool in, int col, uint32_t (&v)[XT == kF32 ? 4 : CPL / 2]) {
-        constexpr int W = XT == kF32 ? 4 : CPL / 2;
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = 0;
-        if (!in) return;
+    // Puts CPL values of a row into the lane's queue, zeros outside.
+    static __device__ __forceinline__ void queue_wide(const WgradArgs &q, int which, unsigned char *dst, int t, bool in, int col) {
         const size_t at = static_cast<size_t>(t) * q.ld[which] + col;
-        if (q.vec[which] && col + CPL <= q.cols[which]) {
-            if constexpr (W == 4) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(q.wide[which]) + at * (XT == kF32 ? 4 : 2)));
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-            } else {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(static_cast<const char *>(q.wide[which]) + at * 2));
-                v[0] = x.x, v[1] = x.y;
-            }
+        const int cols = q.cols[which];
+        if (!in || col >= cols || (q.vec[which] && col + CPL <= cols)) {
+            in = in && col < cols;
+            queue_copy<PB>(dst, static_cast<const char *>(q.wide[which]) + (in ? at * (XT == kF32 ? 4 : 2) : 0), in);
             return;
         }
 #pragma unroll
         for (int i = 0; i < CPL; ++i) {
-            if (col + i >= q.cols[which]) continue;
-            if constexpr (XT == kF32) v[i] = __ldg(static_cast<const unsigned int *>(q.wide[which]) + at + i);
-            else v[i >> 1] |= static_cast<uint32_t>(__ldg(static_cast<const unsigned short *>(q.wide[which]) + at + i)) << (16 * (i & 1));
+            if constexpr (XT == kF32) reinterpret_cast<uint32_t *>(dst)[i] = col + i < cols ? __ldg(static_cast<const unsigned int *>(q.wide[which]) + at + i) : 0u;
+            else reinterpret_cast<uint16_t *>(dst)[i] = col + i < cols ? __ldg(static_cast<const unsigned short *>(q.wide[which]) + at + i) : uint16_t(0);
         }
     }
 
@@ -148,27 +143,59 @@ struct WgradKernel {
                 }
             }
         };
-        Walk w{0, 0, 0u, 0, 0, rank};
-        int t0 = 0, rows = 0;
+        // Two walks over the same 32-row steps: one loads, STAGES - 1 steps ahead of the one that multiplies.
+        Walk w{0, 0, 0u, 0, 0, rank}, wl = w;
+        unsigned char *queue = sm + 4 * QBYTES + (warp * STAGES * 8 * 32 + lane) * PB;
+        int lt = 0, lrows = 0, lst = kWgChunk;
+        bool lmore = true;
+        auto ahead = [&](int slot) {
+            if (lmore && (lst >= kWgChunk || lst >= lrows)) {
+                lmore = advance(p, a, q.cs, wl, lt, lrows);
+                lst = 0;
+            }
+            if (lmore) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = lst + s * 16 + c * 4 + e;
+                        queue_wide(q, which, queue + (slot * 8 + s * 4 + e) * 32 * PB, lt + t, t < lrows, col);
+                    }
+                lst += 32;
+            }
+            queue_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) ahead(i);
+        int slot = 0, t0 = 0, rows = 0;
         bool more = advance(p, a, q.cs, w, t0, rows);
         if (more) fetch(t0, rows);
         for (int b = 0; more; b ^= 1) {
             put(b);
             __syncthreads();
-            const int ct = t0, cr = rows;
+            const int cr = rows;
             more = advance(p, a, q.cs, w, t0, rows);
             if (more) fetch(t0, rows);
             const unsigned char *hi = sm + 2 * b * QBYTES, *lo = hi + QBYTES;
 #pragma unroll 1
             for (int st = 0; st < kWgChunk && st < cr; st += 32) {
+                ahead(slot == 0 ? STAGES - 1 : slot - 1);
+                queue_wait<STAGES - 1>();
                 uint32_t x[2][4][W];
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int t = st + s * 16 + c * 4 + e;
-                        load_wide(q, which, ct + t, t < cr, col, x[s][e]);
+                        const unsigned char *from = queue + (slot * 8 + s * 4 + e) * 32 * PB;
+                        if constexpr (W == 4) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(from);
+                            x[s][e][0] = v.x, x[s][e][1] = v.y, x[s][e][2] = v.z, x[s][e][3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(from);
+                            x[s][e][0] = v.x, x[s][e][1] = v.y;
+                        }
                     }
+                slot = slot == STAGES - 1 ? 0 : slot + 1;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const int tt = st + s * 16 + c * 4;
@@ -230,6 +257,7 @@ struct WgradKernel {
             }
         }
         // ------------------------------------------------------------------ sums of the cluster, and out
+        queue_wait<0>();
         __syncthreads();
         float *sums = reinterpret_cast<float *>(sm);
 #pragma unroll
