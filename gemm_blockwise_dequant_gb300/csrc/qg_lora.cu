@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "qg_lora_rows.cuh"
+#include "qg_lora_tc.h"
 #include "qg_lora_wgrad.cuh"
 
 namespace qg {
@@ -15,6 +16,8 @@ template <> cudaError_t launch_rows<kF32, kBF16>(const RowsArgs &, bool, const R
 cudaError_t launch_wgrad(const WgradArgs &q, int x_dtype, cudaStream_t s);
 
 namespace {
+
+constexpr int kTcRows = 512;  // rows from which on the tensor-core kernels take over
 
 size_t esize(int d) { return d == kF32 ? 4 : 2; }
 
@@ -36,9 +39,36 @@ RowsPlan make_plan(int T, int S, int c1) {
     return plan;
 }
 
+// The second product alone: 64-row tiles, and columns shared so that the SMs have
+// about four CTAs each to take in turn.
+RowsPlan expand_plan(int T, int S, int c2) {
+    RowsPlan plan{};
+    plan.rows = 64;
+    plan.tiles = (T + 63) / 64 + S;
+    plan.cs = 1;
+    while (plan.cs < 16 && (T / 64) * plan.cs < 4 * device_info().sm_count && c2 >= 512 * plan.cs) plan.cs *= 2;
+    return plan;
+}
+
+// Many rows of 16-bit activations: the first product, and the adapters'
+// gradients, on the tensor cores.
+bool many_rows(const LoraProblem &p, int x_dtype, bool aligned) {
+    return x_dtype != kF32 && aligned && p.T >= kTcRows && p.T / kTcRows >= p.S / 4 && lora_tc_available();
+}
+
+// CTAs that share a tile's contraction: enough for two an SM, of eight steps or more.
+int shrink_splits(int T, int S, int c1) {
+    const int tiles = std::max(T / 128, std::min(S, T));
+    int cs = 1;
+    while (cs < 8 && tiles * cs * 2 <= 2 * device_info().sm_count && c1 >= 1024 * cs) cs *= 2;
+    return cs;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
 cudaError_t rows(const RowsArgs &args, int x_dtype, bool bwd, cudaStream_t s) {
     RowsArgs q = args;
-    const RowsPlan plan = make_plan(q.p.T, q.p.S, std::max(q.c1, q.c2));
+    const RowsPlan plan = q.given ? expand_plan(q.p.T, q.p.S, q.c2) : make_plan(q.p.T, q.p.S, std::max(q.c1, q.c2));
     q.cs = plan.cs;
     if (x_dtype == kBF16) return launch_rows<kBF16, kBF16>(q, bwd, plan, s);
     if (x_dtype == kF16) return launch_rows<kF16, kF16>(q, bwd, plan, s);
@@ -48,9 +78,10 @@ cudaError_t rows(const RowsArgs &args, int x_dtype, bool bwd, cudaStream_t s) {
 
 }  // namespace
 
-size_t lora_apply_workspace_bytes(int, int, int) { return 0; }
+// V between the two products of many rows
+size_t lora_apply_workspace_bytes(int T, int, int r) { return T >= kTcRows ? static_cast<size_t>(T) * r * 4 : 0; }
 
-cudaError_t lora_apply(const LoraApply &a, void *, cudaStream_t s) {
+cudaError_t lora_apply(const LoraApply &a, void *ws, cudaStream_t s) {
     RowsArgs q{};
     q.p = a.p;
     q.in = a.X;
@@ -68,12 +99,26 @@ cudaError_t lora_apply(const LoraApply &a, void *, cudaStream_t s) {
     q.sums = a.V;
     q.in_vec = rows16(a.X, a.ldx, a.x_dtype);
     q.out_vec = rows16(a.Y, a.ldy, a.y_dtype) && (!a.Yin || rows16(a.Yin, a.ldyin, a.yin_dtype));
+    if (many_rows(a.p, a.x_dtype, q.in_vec)) {
+        ShrinkTc t{};
+        t.p = a.p;
+        t.sums = a.V ? a.V : static_cast<float *>(ws);
+        t.bf16 = a.x_dtype == kBF16;
+        t.cs = shrink_splits(a.p.T, a.p.S, a.p.K);
+        const cudaError_t e = launch_shrink_tc(t, a.X, a.ldx, a.p.A, s);
+        if (e != cudaSuccess) return e;
+        q.given = t.sums;
+        q.sums = nullptr;
+    }
     const cudaError_t e = rows(q, a.x_dtype, false, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// G, the rows' gradients inside the adapter
-size_t lora_grad_workspace_bytes(int T, int, int, int r, int, int) { return static_cast<size_t>(T) * r * 4; }
+// G, the rows' gradients inside the adapter, and for many rows the largest
+// values and the adapters of the tiles that made them
+size_t lora_grad_workspace_bytes(int T, int S, int, int r, int, int) {
+    return align256(static_cast<size_t>(T) * r * 4) + (T >= kTcRows ? static_cast<size_t>(shrink_tc_tiles(T, S)) * 8 * 12 : 0);
+}
 
 cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
     RowsArgs q{};
@@ -93,9 +138,40 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
     q.sums = static_cast<float *>(ws);
     q.in_vec = rows16(a.dY, a.lddy, a.x_dtype);
     q.out_vec = 1;
-    cudaError_t e = rows(q, a.x_dtype, true, s);
+    const bool tc = many_rows(a.p, a.x_dtype, q.in_vec);
+    ShrinkTc t{};
+    cudaError_t e = cudaSuccess;
+    if (tc) {
+        t.p = a.p;
+        t.sums = q.sums;
+        t.V = a.V;
+        t.bwd = 1;
+        t.bf16 = a.x_dtype == kBF16;
+        t.cs = shrink_splits(a.p.T, a.p.S, a.p.N);
+        t.tile_adapter = reinterpret_cast<int *>(static_cast<char *>(ws) + align256(static_cast<size_t>(a.p.T) * a.p.r * 4));
+        t.tile_max = reinterpret_cast<float *>(t.tile_adapter + shrink_tc_tiles(a.p.T, a.p.S) * t.cs);
+        e = launch_shrink_tc(t, a.dY, a.lddy, a.p.B, s);
+        q.given = q.sums;
+        q.sums = nullptr;
+    }
+    if (e == cudaSuccess && (!tc || a.dX)) e = rows(q, a.x_dtype, true, s);
     if (e != cudaSuccess) return e;
     if (a.p.na == 0) return cudaGetLastError();
+    if (tc) {
+        WgradTc w{};
+        w.p = a.p;
+        w.skinny[0] = t.sums;
+        w.skinny[1] = a.V;
+        w.out[0] = a.dA;
+        w.out[1] = a.dB;
+        w.g_dtype = a.g_dtype;
+        w.accumulate = a.accumulate;
+        w.tile_max = t.tile_max;
+        w.tile_adapter = t.tile_adapter;
+        w.parts = shrink_tc_tiles(a.p.T, a.p.S) * t.cs;
+        e = launch_wgrad_tc(w, a.X, a.ldx, a.dY, a.lddy, t.bf16, s);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
     WgradArgs w{};
     w.p = a.p;
     w.wide[0] = a.X;

@@ -35,7 +35,8 @@ struct RowsArgs {
     int out_dtype;
     int64_t ld_out;
     float *sums;         // V_out / G or null, [T][rank]
-    int cs;              // CTAs of a cluster
+    const float *given;  // the first product's sums where they are known, or null
+    int cs;              // CTAs that share a tile: a cluster, unless the sums are given
     int in_vec, out_vec; // rows at 16-byte boundaries: vector accesses
 };
 
@@ -241,7 +242,8 @@ struct RowsKernel {
     static constexpr int BASE_PIECES = 2 * MT * BW;  // of a lane and group
     static constexpr int BASE_BYTES = 8 * STAGES * BASE_PIECES * 512;
     static __host__ __device__ int queue_offset(int r) { return r > RC ? sums_bytes(r) : 0; }  // several passes: their sums stay
-    static __host__ __device__ int smem_bytes(int r) {
+    static __host__ __device__ int smem_bytes(int r, bool given) {
+        if (given) return sums_bytes(r) + frag_bytes(r) + BASE_BYTES;
         const int later = PART_BYTES > frag_bytes(r) + BASE_BYTES ? PART_BYTES : frag_bytes(r) + BASE_BYTES;
         return sums_bytes(r) + later > queue_offset(r) + IN_BYTES ? sums_bytes(r) + later : queue_offset(r) + IN_BYTES;
     }
@@ -267,7 +269,13 @@ struct RowsKernel {
         const int ngrp = (q.c2 + 31) / 32;  // 32-column groups of the second product, and this CTA's
         const int n_lo = static_cast<int>(static_cast<int64_t>(ngrp) * rank / q.cs), n_hi = static_cast<int>(static_cast<int64_t>(ngrp) * (rank + 1) / q.cs);
 
-        if (t.adapter >= 0) {
+        if (t.adapter >= 0 && q.given) {
+            for (int e = tid; e < R * rp; e += 256) {
+                const int row = e / rp, j = e - row * rp;
+                whole[e] = row < t.rows && j < r ? __ldg(q.given + static_cast<size_t>(t.t0 + row) * r + j) : 0.f;
+            }
+            __syncthreads();
+        } else if (t.adapter >= 0) {
             // ---------------------------------------------------------- first product
             if (R == 16 && q.out) prefetch_w2(q, t.adapter, n_lo * 32, min(n_hi * 32, q.c2));
             const int nblk = (q.c1 + BLK - 1) / BLK;
@@ -379,6 +387,10 @@ struct RowsKernel {
             }
             __syncthreads();
             if (q.cs > 1) cluster_arrive();  // done with the peers' memory; awaited before leaving
+        } else if (!BWD && q.sums && rank == 0) {
+            for (int e = tid; e < t.rows * r; e += 256) q.sums[static_cast<size_t>(t.t0) * r + e] = 0.f;
+        }
+        if (t.adapter >= 0) {
             // ---------------------------------------------------------- operand fragments of the sums
             if (q.out) {
                 if constexpr (NATIVE) {
@@ -413,8 +425,6 @@ struct RowsKernel {
                 }
                 __syncthreads();
             }
-        } else if (!BWD && q.sums && rank == 0) {
-            for (int e = tid; e < t.rows * r; e += 256) q.sums[static_cast<size_t>(t.t0) * r + e] = 0.f;
         }
 
         // -------------------------------------------------------------- second product
@@ -495,7 +505,7 @@ struct RowsKernel {
                 slot = slot == STAGES - 1 ? 0 : slot + 1;
             }
         }
-        if (q.cs > 1 && t.adapter >= 0) {
+        if (q.cs > 1 && t.adapter >= 0 && !q.given) {
             __syncwarp();
             cluster_wait();
         }
@@ -596,11 +606,10 @@ __global__ void __launch_bounds__(256, 2) lora_rows_kernel(const RowsArgs q) {
 template <int XT, int WT, bool BWD, int MT, int RG, int NT>
 cudaError_t launch_rows_one(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
     auto kern = lora_rows_kernel<XT, WT, BWD, MT, RG, NT>;
-    const int smem = RowsKernel<XT, WT, BWD, MT, RG, NT>::smem_bytes(q.p.r);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && q.cs > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const int smem = RowsKernel<XT, WT, BWD, MT, RG, NT>::smem_bytes(q.p.r, q.given != nullptr);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_cluster(kern, dim3(static_cast<unsigned>(plan.tiles) * q.cs), dim3(256), smem, s, q.cs, q);
+    return launch_cluster(kern, dim3(static_cast<unsigned>(plan.tiles) * q.cs), dim3(256), smem, s, q.given ? 1 : q.cs, q);
 }
 
 template <int XT, int WT, bool BWD>

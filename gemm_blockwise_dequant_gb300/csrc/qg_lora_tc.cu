@@ -1,0 +1,558 @@
+// qg_lora_tc.cu -- the adapters' contractions on the tensor cores (tcgen05 +
+// TMA), for 16-bit activations in batches of many rows:
+//
+//   shrink  V = X A^T  (forward)  or  G = scaling dY B  (backward)
+//   wgrad   dA = G^T X  and  dB = scaling V^T dY
+//
+// Each reads a wide matrix once and is bound by that read; a ring of TMA stages
+// keeps about 100 to 200 KB an SM in flight, which loads through registers or
+// per-lane queues cannot, and no thread touches the wide operand.
+//
+// Layouts (128-byte swizzle).  K-major operands have the contraction along
+// their rows; MN-major ones come as [64-column block][row] straight from
+// row-major memory, so nothing is transposed:
+//             wide operand (A)                 thin operand (B)
+//   forward   X, K-major, 128 rows             A[a], K-major
+//   backward  dY, K-major, 128 rows            B[a], MN-major
+//   wgrad     X or dY, MN-major, 2 x 128 cols  G or V, MN-major, in 16-bit terms
+// The thin operand of wgrad is fp32: converting warps split it in two 16-bit
+// terms (three for fp32 gradients of bf16 activations), after scaling it, for
+// fp16, by the power of two that the adapter's largest value gives.
+#include <algorithm>
+#include <atomic>
+
+#include "qg_lora_tc.h"
+#include "qg_tc_common.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kStep = 64;            // contraction values of a step
+constexpr int kTileRows = 128;       // rows of a shrink tile
+constexpr int kInBytes = kTileRows * kStep * 2;
+constexpr int kBlock = kStep * 128;  // 64 rows of a 64-column block
+constexpr int kShrinkThreads = 192;  // TMA, MMA, four warps that read the sums back
+constexpr int kBars = 256;           // bytes of barriers and flags
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// MN-major operand: 64-column blocks kBlock bytes apart, 8-row groups 1024.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kBlock >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ int pow2_cols(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+
+// ------------------------------------------------------------------ shrink
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap in_map,
+                                                                        const __grid_constant__ CUtensorMap w_map, const ShrinkTc q) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int stage_bytes = kInBytes + q.w_bytes;
+    unsigned char *bars = sm + q.stages * stage_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + q.stages, *accf = empty + q.stages;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    unsigned *smax = tmem_slot + 2;  // largest sums and V of this CTA's rows, as bits
+    const LoraProblem &p = q.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = p.r;
+    const int rank = blockIdx.x % q.cs, tile = blockIdx.x / q.cs;
+    pdl_launch_dependents();
+    pdl_wait();
+    RowTile t;
+    const bool fine = find_tile(p, tile, kTileRows, blockIdx.x == 0, t);
+    if (!fine || t.rows == 0 || t.adapter < 0) {  // the whole cluster
+        if (q.tile_adapter && tid == 0) q.tile_adapter[blockIdx.x] = -1;
+        if (fine && t.rows > 0 && rank == 0)
+            for (int e = tid; e < t.rows * r; e += kShrinkThreads) q.sums[static_cast<size_t>(t.t0) * r + e] = 0.f;
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < q.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(accf, 1);
+        *abort_flag = 0;
+        smax[0] = smax[1] = 0;
+        mbar_fence_init();
+    }
+    const uint32_t cols = pow2_cols(q.n);
+    if (warp == 1) tmem_alloc(tmem_slot, cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int s0 = static_cast<int>(static_cast<int64_t>(q.steps) * rank / q.cs), ns = static_cast<int>(static_cast<int64_t>(q.steps) * (rank + 1) / q.cs) - s0;
+
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0)
+            for (int i = 0; i < ns; ++i) {
+                const int s = i % q.stages, k = (s0 + i) * kStep;
+                if (!mbar_wait(&empty[s], ((i / q.stages) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC)) break;
+                unsigned char *dst = sm + s * stage_bytes;
+                mbar_arrive_expect_tx(&full[s], stage_bytes);
+                tma_load_2d(dst, &in_map, k, t.t0, &full[s]);  // rows past the tensor come as zeros, later requests' are ignored
+                if (!q.bwd) {
+                    tma_load_3d(dst + kInBytes, &w_map, k, 0, t.adapter, &full[s]);
+                } else {
+                    for (int b = 0; b * kBlock < q.w_bytes; ++b) tma_load_3d(dst + kInBytes + b * kBlock, &w_map, 64 * b, k, t.adapter, &full[s]);
+                }
+            }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_f16(128, q.n, q.bf16) | (q.bwd ? 1u << 16 : 0u);
+            for (int i = 0; i < ns; ++i) {
+                const int s = i % q.stages;
+                ok = mbar_wait(&full[s], (i / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = smem_u32(sm + s * stage_bytes);
+                const uint64_t ad = sdesc_k128(at), bd = q.bwd ? sdesc_mn(at + kInBytes) : sdesc_k128(at + kInBytes);
+#pragma unroll
+                for (int k = 0; k < kStep / 16; ++k) umma_f16(tmem, ad + 2 * k, bd + (q.bwd ? 128 : 2) * k, idesc, (i | k) != 0);
+                umma_commit(&empty[s]);
+            }
+            umma_commit(accf);
+        }
+    } else {
+        ok = mbar_wait(accf, 0, abort_flag, q.fault, FAULT_WAIT_TC);
+    }
+    __syncwarp();
+    // The CTA's sums to shared memory (over the ring: every stage has been read), then the cluster's.
+    float *mine = reinterpret_cast<float *>(sm);
+    const int stride = q.n + 4;
+    if (warp >= 2) {
+        tc_fence_after();
+        const int sub = warp & 3;
+        for (int c = 0; c < q.n; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + c, v);
+            float4 *dst = reinterpret_cast<float4 *>(mine + (sub * 32 + lane) * stride + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + 4 * i < q.n)
+                    dst[i] = ok && ns > 0 ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
+        __syncwarp();
+    }
+    if (q.cs > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    const float scale = q.bwd && p.scaling ? __ldg(p.scaling + t.adapter) : 1.f;
+    const int r_lo = kTileRows * rank / q.cs, r_hi = min(kTileRows * (rank + 1) / q.cs, t.rows);
+    float mx = 0.f, mv = 0.f;
+    for (int e = tid; e < (r_hi - r_lo) * r; e += kShrinkThreads) {
+        const int row = r_lo + e / r, j = e % r;
+        float s = 0.f;
+        if (q.cs > 1)
+            for (int w = 0; w < q.cs; ++w) s += peer_float(mine + row * stride + j, w);
+        else
+            s = mine[row * stride + j];
+        s *= scale;
+        const size_t at = static_cast<size_t>(t.t0 + row) * r + j;
+        q.sums[at] = s;
+        if (q.V_copy) q.V_copy[at] = s;
+        mx = fmaxf(mx, fabsf(s));
+        if (q.V) mv = fmaxf(mv, fabsf(__ldg(q.V + at)));
+    }
+    if (q.tile_adapter) {
+        atomicMax(&smax[0], __float_as_uint(mx));  // of values that are not negative: the order does not matter
+        atomicMax(&smax[1], __float_as_uint(mv));
+        __syncthreads();
+        if (tid == 0) {
+            q.tile_adapter[blockIdx.x] = t.adapter;
+            q.tile_max[blockIdx.x] = __uint_as_float(smax[0]);
+            q.tile_max[gridDim.x + blockIdx.x] = __uint_as_float(smax[1]);
+        }
+    }
+    if (q.cs > 1) {  // the peers have read this CTA's sums
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// ------------------------------------------------------------------ wgrad
+constexpr int kCols = 256;                       // of a CTA: two halves of 128
+constexpr int kWideBytes = kStep * kCols * 2;    // a step: four 64-column blocks
+constexpr int kWideStages = 4;
+constexpr int kThinBufs = 2;
+constexpr int kConvWarps = 8;
+constexpr int kWgThreads = 64 + 32 * kConvWarps;
+
+// The 64-row steps of an adapter's requests that belong to CTA `rank` of `cs`, walked by a whole warp.
+struct StepWalk {
+    int s = 0, base = 0, left;
+    unsigned mask = 0;
+    int64_t t = 0, end = 0;
+    __device__ explicit StepWalk(int rank) : left(rank) {}
+    __device__ bool next(const LoraProblem &p, int a, int cs, int &t0, int &rows) {
+        for (;;) {
+            if (t < end) {
+                const int64_t n = (end - t + kStep - 1) / kStep;
+                if (left < n) {
+                    const int64_t at = t + static_cast<int64_t>(left) * kStep;
+                    t0 = static_cast<int>(at);
+                    rows = static_cast<int>(end - at < kStep ? end - at : kStep);
+                    t = at + kStep;
+                    left = cs - 1;
+                    return true;
+                }
+                left -= static_cast<int>(n);
+                t = end;
+            }
+            while (!mask) {
+                if (s >= p.S) return false;
+                const int i = s + (threadIdx.x & 31);
+                mask = __ballot_sync(0xffffffffu, i < p.S && __ldg(p.ids + min(i, p.S - 1)) == a);
+                base = s;
+                s += 32;
+            }
+            const int seg = base + __ffs(mask) - 1;
+            mask &= mask - 1;
+            t = __ldg(p.offs + seg);
+            end = __ldg(p.offs + seg + 1);
+        }
+    }
+};
+
+template <int TERMS, bool BF16>
+__global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map,
+                                                                      const __grid_constant__ CUtensorMap dy_map, const WgradTc q) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const LoraProblem &p = q.p;
+    const int blocks = q.n > 64 ? 2 : 1;             // 64-column blocks of the thin operand
+    const int term_bytes = blocks * kBlock, thin_bytes = TERMS * term_bytes;
+    unsigned char *wide = sm, *thin = sm + kWideStages * kWideBytes;
+    unsigned char *bars = thin + kThinBufs * thin_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + kWideStages;
+    uint64_t *tfull = empty + kWideStages, *tempty = tfull + kThinBufs, *accf = tempty + kThinBufs;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    unsigned *smax = tmem_slot + 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = blockIdx.x % q.cs;
+    int tile = blockIdx.x / q.cs;
+    const int which = tile >= q.tiles[0];
+    if (which) tile -= q.tiles[0];
+    const int a = blockIdx.y, col0 = tile * kCols, r = p.r;
+    const float *skinny = q.skinny[which];
+    pdl_launch_dependents();
+    pdl_wait();
+    int bad = 0;
+    for (int s = tid; s < p.S; s += kWgThreads) {
+        const int64_t lo = __ldg(p.offs + s), hi = __ldg(p.offs + s + 1);
+        bad |= hi < lo || lo < 0 || hi > p.T || (s == 0 && lo != 0);
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kWideStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kThinBufs; ++i) {
+            mbar_init(&tfull[i], kConvWarps);
+            mbar_init(&tempty[i], 1);
+        }
+        mbar_init(accf, 1);
+        *abort_flag = 0;
+        *smax = 0;
+        mbar_fence_init();
+    }
+    if (__syncthreads_or(bad)) return;  // the whole cluster
+    const uint32_t cols = pow2_cols(2 * q.n);
+    if (warp == 1) tmem_alloc(tmem_slot, cols);
+    // Columns j >= r of the thin operand stay zero for the whole kernel.
+    for (int e = tid; e < kThinBufs * thin_bytes / 16; e += kWgThreads) reinterpret_cast<uint4 *>(thin)[e] = make_uint4(0, 0, 0, 0);
+    if (!BF16) {  // the adapter's largest value
+        float mx = 0.f;
+        for (int i = tid; i < q.parts; i += kWgThreads)
+            if (__ldcg(q.tile_adapter + i) == a) mx = fmaxf(mx, __ldcg(q.tile_max + which * q.parts + i));
+        atomicMax(smax, __float_as_uint(mx));
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    int exponent = 0;  // fp16: the thin operand times 2^exponent lies within [2^14, 2^15) at most
+    if (!BF16) {
+        const int ef = static_cast<int>((*smax >> 23) & 0xFFu);
+        exponent = ef == 0 || ef == 255 ? 0 : min(max(14 - (ef - 127), -100), 100);
+    }
+    StepWalk walk(rank);
+    int t0, rows, steps = 0;
+    bool ok = true;
+    if (warp == 0) {
+        const CUtensorMap *map = which ? &dy_map : &x_map;
+        while (walk.next(p, a, q.cs, t0, rows)) {
+            if (lane == 0) {
+                const int s = steps % kWideStages;
+                ok = mbar_wait(&empty[s], ((steps / kWideStages) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC);
+                if (ok) {
+                    mbar_arrive_expect_tx(&full[s], kWideBytes);
+#pragma unroll
+                    for (int b = 0; b < kCols / 64; ++b) tma_load_2d(wide + s * kWideBytes + b * kBlock, map, col0 + 64 * b, t0, &full[s]);
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            ++steps;
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_f16(128, q.n, BF16) | (1u << 15) | (1u << 16);  // both MN-major
+        const bool two = col0 + 128 < q.cols[which];
+        while (walk.next(p, a, q.cs, t0, rows)) {
+            if (lane == 0) {
+                const int s = steps % kWideStages, b = steps % kThinBufs;
+                ok = mbar_wait(&full[s], (steps / kWideStages) & 1, abort_flag, q.fault, FAULT_WAIT_TC) &&
+                     mbar_wait(&tfull[b], (steps / kThinBufs) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
+                if (ok) {
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_mn(smem_u32(wide + s * kWideBytes)), ad1 = sdesc_mn(smem_u32(wide + s * kWideBytes + 2 * kBlock));
+                    const uint64_t bd = sdesc_mn(smem_u32(thin + b * thin_bytes));
+                    for (int m = TERMS - 1; m >= 0; --m)
+#pragma unroll
+                        for (int k = 0; k < kStep / 16; ++k) {
+                            const uint64_t bk = bd + m * (term_bytes >> 4) + 128 * k;
+                            const uint32_t acc = steps > 0 || k > 0 || m < TERMS - 1;
+                            umma_f16(tmem, ad + 128 * k, bk, idesc, acc);
+                            if (two) umma_f16(tmem + q.n, ad1 + 128 * k, bk, idesc, acc);
+                        }
+                    umma_commit(&empty[s]);
+                    umma_commit(&tempty[b]);
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            ++steps;
+        }
+        if (lane == 0) umma_commit(accf);
+        __syncwarp();
+    } else {
+        // Converters: task = 8 values j of a row; 8 lanes of a quarter warp write 8 rows' chunks without conflicts.
+        const int u = tid - 64, tasks = kStep * (r / 8);
+        const float up = exp2i(exponent);
+        constexpr int MAXT = 4;  // tasks of a thread: rank 128
+        float4 v[MAXT][2];
+        int nt0, nrows;
+        bool more = walk.next(p, a, q.cs, nt0, nrows);
+        auto fetch = [&]() {
+#pragma unroll
+            for (int i = 0; i < MAXT; ++i) {
+                const int e = u + i * 32 * kConvWarps;
+                if (e >= tasks) break;
+                const int t = e & 63, c = e >> 6;
+                v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t < nrows) {
+                    const float4 *src = reinterpret_cast<const float4 *>(skinny + static_cast<size_t>(nt0 + t) * r + c * 8);
+                    v[i][0] = __ldcg(src);
+                    v[i][1] = __ldcg(src + 1);
+                }
+            }
+        };
+        if (more) fetch();
+        while (more) {
+            const int b = steps % kThinBufs, s = steps % kWideStages;
+            rows = nrows;
+            ok = mbar_wait(&tempty[b], ((steps / kThinBufs) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC);
+            if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+            for (int i = 0; i < MAXT; ++i) {
+                const int e = u + i * 32 * kConvWarps;
+                if (e >= tasks) break;
+                const int t = e & 63, c = e >> 6;
+                float x[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+                unsigned char *dst = thin + b * thin_bytes + (c >> 3) * kBlock + (t >> 3) * 1024 + (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4);
+                if (!BF16) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] *= up;
+                }
+#pragma unroll
+                for (int m = 0; m < TERMS; ++m) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {  // the next 8 or 11 bits of each value; an infinity or NaN is its own first term
+                        const uint16_t h = BF16 ? f2bf(x[k]) : f2h(x[k]);
+                        const float f = BF16 ? bf2f(h) : h2f(h);
+                        x[k] = fabsf(f) < __int_as_float(0x7f800000) ? x[k] - f : 0.f;
+                        w[k >> 1] = (k & 1) ? w[k >> 1] | static_cast<uint32_t>(h) << 16 : h;
+                    }
+                    *reinterpret_cast<uint4 *>(dst + m * term_bytes) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (rows < kStep) {  // the request ends inside the step: what follows it must not meet the zeros as a NaN
+                ok = mbar_wait(&full[s], (steps / kWideStages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                const int gone = kStep - rows;
+                for (int e = u; e < gone * (kCols / 8); e += 32 * kConvWarps) {
+                    const int row = rows + e / (kCols / 8), c = e % (kCols / 8);
+                    *reinterpret_cast<uint4 *>(wide + s * kWideBytes + (c >> 3) * kBlock + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tfull[b]);
+            ++steps;
+            more = walk.next(p, a, q.cs, nt0, nrows);
+            if (more) fetch();
+        }
+        ok = mbar_wait(accf, 0, abort_flag, q.fault, FAULT_WAIT_TC) && ok;
+    }
+    __syncwarp();
+    // The CTA's sums [j][column] to shared memory (over the ring), then the cluster's, and out.
+    float *sums = reinterpret_cast<float *>(sm);
+    constexpr int OS = kCols + 4;
+    __syncthreads();
+    if (warp >= 2) {
+        tc_fence_after();
+        const int sub = warp & 3, half = (warp - 2) >> 2;  // 32 columns of a half; the half
+        for (int c = 0; c < q.n; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + half * q.n + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < q.n) sums[(c + i) * OS + half * 128 + sub * 32 + lane] = ok && steps > 0 ? __uint_as_float(v[i]) : 0.f;
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
+        __syncwarp();
+    }
+    if (q.cs > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    const int ncol = min(kCols, q.cols[which] - col0), width = kCols / q.cs;
+    const float scale = (which && p.scaling ? __ldg(p.scaling + a) : 1.f) * (BF16 ? 1.f : exp2i(-exponent));
+    for (int e = tid; e < r * width; e += kWgThreads) {
+        const int j = which ? e % r : e / width, cc = rank * width + (which ? e / r : e % width);
+        if (cc >= ncol) continue;
+        float s = 0.f;
+        if (q.cs > 1)
+            for (int k = 0; k < q.cs; ++k) s += peer_float(sums + j * OS + cc, k);
+        else
+            s = sums[j * OS + cc];
+        s *= scale;
+        const size_t at = which ? (static_cast<size_t>(a) * p.N + col0 + cc) * r + j : (static_cast<size_t>(a) * r + j) * p.K + col0 + cc;
+        if (q.accumulate) s += load_elem(q.out[which], q.g_dtype, at);
+        store_y_elem(q.out[which], q.g_dtype, at, s);
+    }
+    if (q.cs > 1) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// ------------------------------------------------------------------ host side
+bool make_map(CUtensorMap &m, bool bf16, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+    const cuuint32_t es[3] = {1, 1, 1};
+    return encode_fn()(&m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank),
+                       const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<unsigned long long> &done, int bytes) {
+    const int slot = device_slot();
+    const unsigned long long bit = slot < 0 ? 0 : 1ull << slot;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+int thin_cols(int r) { return (r + 15) / 16 * 16; }
+
+}  // namespace
+
+bool lora_tc_available() { return encode_fn() != nullptr; }
+
+int shrink_tc_tiles(int T, int S) { return (T + kTileRows - 1) / kTileRows + S; }
+
+cudaError_t launch_shrink_tc(ShrinkTc q, const void *in, int64_t ld, const void *w, cudaStream_t s) {
+    const LoraProblem &p = q.p;
+    const int c1 = q.bwd ? p.N : p.K;
+    q.n = thin_cols(p.r);
+    q.steps = (c1 + kStep - 1) / kStep;
+    q.w_bytes = q.bwd ? (p.r > 64 ? 2 : 1) * kBlock : q.n * 128;
+    q.stages = 4;
+    q.fault = fault_word();
+    CUtensorMap in_map, w_map;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c1), static_cast<cuuint64_t>(p.T)}, strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {kStep, kTileRows};
+    const cuuint64_t wd[3] = {static_cast<cuuint64_t>(q.bwd ? p.r : p.K), static_cast<cuuint64_t>(q.bwd ? p.N : p.r), static_cast<cuuint64_t>(p.na)};
+    const cuuint64_t ws[2] = {wd[0] * 2, wd[0] * wd[1] * 2};
+    const cuuint32_t wb[3] = {64, static_cast<cuuint32_t>(q.bwd ? kStep : q.n), 1};
+    if (!make_map(in_map, q.bf16, in, 2, dims, strides, box) || !make_map(w_map, q.bf16, w, 3, wd, ws, wb)) return cudaErrorInvalidValue;
+    const int ring = q.stages * (kInBytes + q.w_bytes);
+    const int smem = 1024 + std::max(ring, kTileRows * (q.n + 4) * 4) + kBars;
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(lora_shrink_tc_kernel, done, 4 * (kInBytes + 2 * kBlock) + 1024 + kBars);
+    if (e != cudaSuccess) return e;
+    return launch_cluster(lora_shrink_tc_kernel, dim3(static_cast<unsigned>(shrink_tc_tiles(p.T, p.S)) * q.cs), dim3(kShrinkThreads), smem, s, q.cs, in_map,
+                          w_map, q);
+}
+
+cudaError_t launch_wgrad_tc(WgradTc q, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16, cudaStream_t s) {
+    const LoraProblem &p = q.p;
+    q.n = thin_cols(p.r);
+    q.cols[0] = p.K;
+    q.cols[1] = p.N;
+    for (int w = 0; w < 2; ++w) q.tiles[w] = (q.cols[w] + kCols - 1) / kCols;
+    q.fault = fault_word();
+    // A CTA an SM, while each still has eight steps.
+    const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * p.na;
+    q.cs = 1;
+    while (q.cs < 8 && ctas * q.cs * 2 <= device_info().sm_count && p.T / p.na >= 16 * kStep * q.cs) q.cs *= 2;
+    CUtensorMap maps[2];
+    const cuuint32_t box[2] = {64, kStep};
+    for (int w = 0; w < 2; ++w) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(q.cols[w]), static_cast<cuuint64_t>(p.T)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(w ? lddy : ldx) * 2};
+        if (!make_map(maps[w], bf16, w ? dy : x, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    const int terms = bf16 && q.g_dtype == kF32 ? 3 : 2;
+    const int thin = terms * (q.n > 64 ? 2 : 1) * kBlock;
+    const int smem = 1024 + std::max(kWideStages * kWideBytes + kThinBufs * thin, q.n * (kCols + 4) * 4) + kBars;
+    const dim3 grid(static_cast<unsigned>(q.tiles[0] + q.tiles[1]) * q.cs, p.na);
+    constexpr int kMost = 227 * 1024;
+    if (terms == 3) {
+        static std::atomic<unsigned long long> done{0};
+        const cudaError_t e = allow_smem(lora_wgrad_tc_kernel<3, true>, done, kMost);
+        return e != cudaSuccess ? e : launch_cluster(lora_wgrad_tc_kernel<3, true>, grid, dim3(kWgThreads), smem, s, q.cs, maps[0], maps[1], q);
+    }
+    if (bf16) {
+        static std::atomic<unsigned long long> done{0};
+        const cudaError_t e = allow_smem(lora_wgrad_tc_kernel<2, true>, done, kMost);
+        return e != cudaSuccess ? e : launch_cluster(lora_wgrad_tc_kernel<2, true>, grid, dim3(kWgThreads), smem, s, q.cs, maps[0], maps[1], q);
+    }
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(lora_wgrad_tc_kernel<2, false>, done, kMost);
+    return e != cudaSuccess ? e : launch_cluster(lora_wgrad_tc_kernel<2, false>, grid, dim3(kWgThreads), smem, s, q.cs, maps[0], maps[1], q);
+}
+
+}  // namespace qg

@@ -1,0 +1,37 @@
+// qg_lora_tc.h -- launches of the adapters' tensor-core contractions (qg_lora_tc.cu).
+#pragma once
+
+#include "qg_lora_common.cuh"
+
+namespace qg {
+
+struct ShrinkTc {
+    LoraProblem p;
+    float *sums;             // [T][rank]: V (unscaled) or G (scaled)
+    float *V_copy;           // a second place for them, or null
+    const float *V;          // backward: the forward pass's V, for its largest values
+    float *tile_max;         // [2][CTAs]: largest sum and largest V of a CTA's rows; or null
+    int *tile_adapter;       // [CTAs] or null
+    int bwd, bf16, cs;
+    int n, steps, stages, w_bytes;  // filled in by the launch
+    unsigned *fault;
+};
+
+struct WgradTc {
+    LoraProblem p;
+    const float *skinny[2];  // G, V
+    void *out[2];            // dA, dB
+    int g_dtype, accumulate;
+    const float *tile_max;   // of the shrink launch before it
+    const int *tile_adapter;
+    int parts;               // its CTAs
+    int cols[2], tiles[2], n, cs;  // filled in by the launch
+    unsigned *fault;
+};
+
+bool lora_tc_available();
+int shrink_tc_tiles(int T, int S);
+cudaError_t launch_shrink_tc(ShrinkTc q, const void *in, int64_t ld, const void *w, cudaStream_t s);
+cudaError_t launch_wgrad_tc(WgradTc q, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16, cudaStream_t s);
+
+}  // namespace qg

@@ -1,0 +1,118 @@
+"""qg_lora_apply and qg_lora_grad on batches of many rows (the tensor-core kernels of 16-bit activations) against fp64."""
+import pytest
+import torch
+
+from lora_util import DT, apply64, check, grad64, lora_case
+from test_lora_gpu import check_apply, check_grad, forward_v, qg, run_apply  # noqa: F401  (qg: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = {
+    "one request": ([1000], [0]),
+    "packed": ([512, 0, 130, 259, 1, 64, 128, 127], [1, 0, 2, -1, 1, 0, 2, 1]),
+    "short and long": ([700] + [3] * 8, [2, 0, 1, -1, 0, 1, 2, 0, 1]),
+    "none": ([600, 100], [-1, -1]),
+}
+
+
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+@pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
+def test_layouts(qg, x, layout):
+    lens, ids = LAYOUTS[layout]
+    c = lora_case(lens, ids, na=4, r=16, N=328, K=520, x=x, seed=21, extra=9)
+    check_apply(qg, c, c["Yin"].to(DT[x]), DT[x])
+    check_grad(qg, c, forward_v(c), c["dXin"], DT[x])
+    check_grad(qg, c, forward_v(c), None, torch.float32)
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 48, 64, 72, 104, 128])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_ranks(qg, x, r):
+    c = lora_case([300, 450], [0, 1], na=2, r=r, N=392, K=640, x=x, seed=22)
+    check_apply(qg, c, c["Yin"].to(DT[x]), DT[x])
+    check_grad(qg, c, forward_v(c), c["dXin"], DT[x])
+    check_grad(qg, c, forward_v(c), c["dXin"], torch.float32)
+
+
+@pytest.mark.parametrize("N,K", [(1, 8), (8, 64), (64, 72), (256, 256), (257, 200), (1000, 136), (72, 2056), (3000, 1024)])
+@pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
+def test_widths(qg, x, N, K):
+    c = lora_case([190, 65, 390], [1, -1, 0], na=2, r=8, N=N, K=K, x=x, seed=23, extra=2)
+    check_apply(qg, c, c["Yin"].to(DT[x]), DT[x])
+    check_grad(qg, c, forward_v(c), c["dXin"], torch.float32)
+
+
+def test_strides_bases_and_no_input_gradient(qg):
+    c = lora_case([533, 77], [0, 1], na=2, r=16, N=96, K=160, x="bf16", seed=24, pad=24)
+    for base in (None, c["Yin"], c["Yin"].bfloat16()):
+        check_apply(qg, c, base, torch.bfloat16)
+        check_apply(qg, c, base if base is None or base.dtype == torch.float32 else None, torch.float32)
+        Y, _ = run_apply(qg, c, base, torch.bfloat16, v=False)
+        wy, _, mag = apply64(c, base)
+        check(Y, wy, mag)
+    check_grad(qg, c, forward_v(c), c["dXin"], torch.bfloat16)
+    check_grad(qg, c, forward_v(c), None, torch.bfloat16, want_dx=False)
+    out = torch.randn(c["T"], 96, device="cuda").bfloat16()
+    keep = out.clone()
+    qg.qg_lora_apply(c["X"], c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], out, out)
+    wy, _, mag = apply64(c, keep)
+    check(out, wy, mag)
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_other_rows_and_adapters_do_not_leak(qg, x):
+    lens, ids = [300, 61, 200, 77], [0, -1, 2, 0]
+    c = lora_case(lens, ids, na=4, r=24, N=136, K=160, x=x, seed=25, extra=40)
+    V = forward_v(c)
+    for t in (slice(300, 361), slice(638, 678)):
+        c["X"][t], c["dY"][t], V[t] = float("nan"), float("inf"), float("nan")
+    c["A"][1], c["B"][3] = float("nan"), float("inf")
+    check_apply(qg, c, c["Yin"].to(DT[x]), DT[x])
+    _, dA, dB = check_grad(qg, c, V, c["dXin"], torch.float32)
+    assert not dA[1].any() and not dB[1].any() and not dA[3].any() and not dB[3].any()
+
+
+def test_scales_of_half(qg):
+    """fp16 keeps V and G scaled by each adapter's largest value: sums far outside fp16's range, in two adapters whose
+    values are 2^20 apart."""
+    c = lora_case([400, 400], [0, 1], na=2, r=16, N=64, K=256, x="f16", seed=26)
+    c["scaling"] = torch.tensor([2.0 ** 12, 2.0 ** -8], device="cuda")
+    check_grad(qg, c, forward_v(c), None, torch.float32)
+    c["dY"] = (c["dY"].float() * 2.0 ** -12).half()
+    check_grad(qg, c, forward_v(c) * 2.0 ** 18, None, torch.float32)
+    check_grad(qg, c, forward_v(c) * 2.0 ** -30, None, torch.float32)
+    zero = torch.zeros(800, 16, device="cuda")
+    _, _, dB = check_grad(qg, c, zero, None, torch.float32)
+    assert not dB.any()
+
+
+def test_accumulate_repeat_and_many_adapters(qg):
+    n = 12
+    c = lora_case([60 + 7 * i for i in range(n)], [(5 * i) % 7 for i in range(n)], na=8, r=8, N=200, K=64, x="bf16", seed=27)
+    V = forward_v(c)
+    (_, wa, wb), (_, ma, mb) = grad64(c, V, None)
+    dA, dB = torch.full(c["A"].shape, 2.0, device="cuda"), torch.full(c["B"].shape, -3.0, device="cuda")
+    for _ in range(2):
+        qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], None, None, dA, dB, accumulate=True)
+    check(dA, 2 * wa + 2, 2 * ma + 2)
+    check(dB, 2 * wb - 3, 2 * mb + 3)
+    first = run_apply(qg, c, None, torch.bfloat16), check_grad(qg, c, V, c["dXin"], torch.bfloat16)
+    for _ in range(2):
+        again = run_apply(qg, c, None, torch.bfloat16), check_grad(qg, c, V, c["dXin"], torch.bfloat16)
+        assert all(torch.equal(a, b) for x, y in zip(first, again) for a, b in zip(x, y))
+
+
+def test_offsets_that_break_the_rule_compute_nothing(qg):
+    for off in ([0, 500, 400], [0, 300, 1001], [2, 300, 900]):
+        c = lora_case([400, 600], [0, 1], na=2, r=8, N=16, K=32, x="f16", seed=28)
+        c["offsets"] = torch.tensor(off, dtype=torch.int64, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        Y, V = run_apply(qg, c, None, torch.float16, status=status)
+        assert int(status) == 1 and bool(Y.isnan().all()) and bool(V.isnan().all())
+        status.zero_()
+        dX = torch.full((1000, 32), float("nan"), dtype=torch.float16, device="cuda")
+        dA, dB = torch.full_like(c["A"], 7), torch.full_like(c["B"], 7)
+        qg.qg_lora_grad(c["dY"], c["X"], torch.zeros(1000, 8, device="cuda"), c["offsets"], c["ids"], c["A"], c["B"], None, None, dX,
+                        dA, dB, status=status)
+        assert int(status) == 1 and bool(dX.isnan().all()) and bool((dA == 7).all()) and bool((dB == 7).all())
+    assert qg.qg_read_device_fault() == 0
