@@ -39,14 +39,15 @@ RowsPlan make_plan(int T, int S, int c1) {
     return plan;
 }
 
-// The second product alone: 64-row tiles, and columns shared so that the SMs have
-// about four CTAs each to take in turn.
+// The second product alone: 64-row tiles, whose columns as many CTAs share as
+// keep two on every SM (a CTA's start, with its sums' fragments, costs about
+// as much as 8 of its 32-column groups).
 RowsPlan expand_plan(int T, int S, int c2) {
     RowsPlan plan{};
     plan.rows = 64;
     plan.tiles = (T + 63) / 64 + S;
     plan.cs = 1;
-    while (plan.cs < 16 && (T / 64) * plan.cs < 4 * device_info().sm_count && c2 >= 512 * plan.cs) plan.cs *= 2;
+    while (plan.cs < 64 && (T / 64) * plan.cs * 2 <= 2 * device_info().sm_count && c2 >= 512 * plan.cs) plan.cs *= 2;
     return plan;
 }
 
@@ -115,9 +116,11 @@ cudaError_t lora_apply(const LoraApply &a, void *ws, cudaStream_t s) {
 }
 
 // G, the rows' gradients inside the adapter, and for many rows the largest
-// values and the adapters of the tiles that made them
+// values and the adapters of the tiles that made them, and the 16-bit terms of
+// G and V
 size_t lora_grad_workspace_bytes(int T, int S, int, int r, int, int) {
-    return align256(static_cast<size_t>(T) * r * 4) + (T >= kTcRows ? static_cast<size_t>(shrink_tc_tiles(T, S)) * 8 * 12 : 0);
+    const size_t sums = align256(static_cast<size_t>(T) * r * 4);
+    return T < kTcRows ? sums : sums + align256(static_cast<size_t>(shrink_tc_tiles(T, S)) * 8 * 12) + wgrad_tc_terms_bytes(T, r);
 }
 
 cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
@@ -160,8 +163,6 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
     if (tc) {
         WgradTc w{};
         w.p = a.p;
-        w.skinny[0] = t.sums;
-        w.skinny[1] = a.V;
         w.out[0] = a.dA;
         w.out[1] = a.dB;
         w.g_dtype = a.g_dtype;
@@ -169,7 +170,8 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
         w.tile_max = t.tile_max;
         w.tile_adapter = t.tile_adapter;
         w.parts = shrink_tc_tiles(a.p.T, a.p.S) * t.cs;
-        e = launch_wgrad_tc(w, a.X, a.ldx, a.dY, a.lddy, t.bf16, s);
+        uint16_t *terms = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(t.tile_adapter) + align256(static_cast<size_t>(shrink_tc_tiles(a.p.T, a.p.S)) * 8 * 12));
+        e = launch_wgrad_tc(w, t.sums, a.V, terms, a.X, a.ldx, a.dY, a.lddy, t.bf16, s);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     WgradArgs w{};

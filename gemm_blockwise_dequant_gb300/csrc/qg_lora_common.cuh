@@ -7,8 +7,8 @@
 // as both operands share it, so a lane takes 16 contiguous bytes where the
 // fragment layout asks for scattered pairs.
 //  * NATIVE (16-bit activations and adapters of one type): m16n8k16.  An fp32
-//    factor (V, G) is split in two 16-bit terms after its row has been scaled
-//    to [1, 2) by a power of two: 16 bits of it are kept for bf16, 22 for fp16.
+//    factor (V, G) is split in two 16-bit terms, for fp16 after its row has been
+//    scaled to [1, 2) by a power of two: 16 bits of it are kept for bf16, 22 for fp16.
 //  * TF32 (fp32 activations, adapters of any type): m16n8k8.  An fp32 value is
 //    split in two TF32 terms (22 bits); 16-bit values are TF32 values as they
 //    are.  The product of two second terms (2^-22) is left out.

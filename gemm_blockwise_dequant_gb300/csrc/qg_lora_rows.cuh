@@ -393,13 +393,14 @@ struct RowsKernel {
         if (t.adapter >= 0) {
             // ---------------------------------------------------------- operand fragments of the sums
             if (q.out) {
-                if constexpr (NATIVE) {
-                    for (int row = tid; row < R; row += 256) {
-                        float mx = 0.f;
-                        for (int j = 0; j < r; ++j) mx = fmaxf(mx, fabsf(whole[row * rp + j]));
-                        const int ef = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu);
-                        rscale[row] = exp2i(ef == 255 || mx == 0.f ? 0 : min(max(ef - 127, -126), 126));
-                    }
+                if constexpr (XT == kF16) {  // bf16 has fp32's range
+                    constexpr int TPR = 256 / R;  // threads of a row: neighbours in a warp
+                    float mx = 0.f;
+                    for (int j = tid % TPR; j < r; j += TPR) mx = fmaxf(mx, fabsf(whole[(tid / TPR) * rp + j]));
+#pragma unroll
+                    for (int o = TPR / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const int ef = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu);
+                    if (tid % TPR == 0) rscale[tid / TPR] = exp2i(ef == 255 || mx == 0.f ? 0 : min(max(ef - 127, -126), 126));
                     __syncthreads();
                 }
                 const int units = rp / UW;
@@ -411,7 +412,7 @@ struct RowsKernel {
                         const int row = m * 16 + (l >> 2) + (x & 1) * 8;
                         const float *v = whole + row * rp + u * UW + (l & 3) * EU + (x >> 1) * (EU / 2);
                         if constexpr (NATIVE) {
-                            const float inv = 1.f / rscale[row];
+                            const float inv = XT == kF16 ? 1.f / rscale[row] : 1.f;
                             uint16_t h0, l0, h1, l1;
                             split16<XT>(v[0] * inv, h0, l0);
                             split16<XT>(v[1] * inv, h1, l1);
@@ -437,7 +438,7 @@ struct RowsKernel {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     mul[m][h] = BWD ? 1.f : scale;
-                    if (NATIVE && t.adapter >= 0) mul[m][h] *= rscale[row0 + m * 16 + h * 8 + g];
+                    if (XT == kF16 && t.adapter >= 0) mul[m][h] *= rscale[row0 + m * 16 + h * 8 + g];
                 }
             // the base rows ahead of their sums, when they have the activations' width
             uint4 *queue = reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(frag) + frag_bytes(r)) + warp * (STAGES * BASE_PIECES * 32) + lane;
@@ -460,32 +461,52 @@ struct RowsKernel {
             };
 #pragma unroll
             for (int i = 0; i < STAGES - 1; ++i) ahead(n_lo + kg + i * KG, i);
+            constexpr int UH = NT * 8 / UW <= 4 ? NT * 8 / UW : 1;  // units whose operands a lane holds for the next group
+            const bool held = units <= UH;
+            uint32_t w2[UH][4][2];
+            auto hold = [&](int b) {
+#pragma unroll
+                for (int u = 0; u < UH; ++u)
+                    if (u < units) load_w2(q, t.adapter, u, b * 32, g, c, w2[u]);
+            };
+            if (held && t.adapter >= 0 && n_lo + kg < n_hi) hold(n_lo + kg);
             int slot = 0;
             for (int b = n_lo + kg; b < n_hi; b += KG) {
                 ahead(b + (STAGES - 1) * KG, slot == 0 ? STAGES - 1 : slot - 1);
                 const int n0 = b * 32, n = n0 + c * 8;
                 const bool vec = q.out_vec && n + 8 <= q.c2;
                 float acc[MT][4][4] = {};
-                if (t.adapter >= 0)
-                    for (int u = 0; u < units; ++u) {
-                        uint32_t w[4][2];
-                        load_w2(q, t.adapter, u, n0, g, c, w);
+                auto multiply = [&](int u, const uint32_t (&w)[4][2]) {
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            const int mt = rg * MT + m;
-                            const uint4 h = frag[((mt * units + u) * 2) * 32 + lane], l = frag[((mt * units + u) * 2 + 1) * 32 + lane];
+                    for (int m = 0; m < MT; ++m) {
+                        const int mt = rg * MT + m;
+                        const uint4 h = frag[((mt * units + u) * 2) * 32 + lane], l = frag[((mt * units + u) * 2 + 1) * 32 + lane];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if constexpr (NATIVE) {
-                                    mma16<XT>(acc[m][i], l.x, l.y, l.z, l.w, w[i][0], w[i][1]);
-                                    mma16<XT>(acc[m][i], h.x, h.y, h.z, h.w, w[i][0], w[i][1]);
-                                } else {
-                                    const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
-                                    mma_tf32_split(acc[m][i], hh, ll, w[i][0], w[i][1]);
-                                }
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (NATIVE) {
+                                mma16<XT>(acc[m][i], l.x, l.y, l.z, l.w, w[i][0], w[i][1]);
+                                mma16<XT>(acc[m][i], h.x, h.y, h.z, h.w, w[i][0], w[i][1]);
+                            } else {
+                                const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
+                                mma_tf32_split(acc[m][i], hh, ll, w[i][0], w[i][1]);
                             }
                         }
                     }
+                };
+                if (t.adapter >= 0) {
+                    if (held) {
+#pragma unroll
+                        for (int u = 0; u < UH; ++u)
+                            if (u < units) multiply(u, w2[u]);
+                        if (b + KG < n_hi) hold(b + KG);  // the next group's, while this one's rows are written
+                    } else {
+                        for (int u = 0; u < units; ++u) {
+                            uint32_t w[4][2];
+                            load_w2(q, t.adapter, u, n0, g, c, w);
+                            multiply(u, w);
+                        }
+                    }
+                }
                 queue_wait<STAGES - 1>();
 #pragma unroll
                 for (int m = 0; m < MT; ++m)

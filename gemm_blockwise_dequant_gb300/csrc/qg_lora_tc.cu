@@ -15,9 +15,11 @@
 //   forward   X, K-major, 128 rows             A[a], K-major
 //   backward  dY, K-major, 128 rows            B[a], MN-major
 //   wgrad     X or dY, MN-major, 2 x 128 cols  G or V, MN-major, in 16-bit terms
-// The thin operand of wgrad is fp32: converting warps split it in two 16-bit
-// terms (three for fp32 gradients of bf16 activations), after scaling it, for
-// fp16, by the power of two that the adapter's largest value gives.
+// The thin operand of wgrad is fp32.  A small kernel between the two splits G and
+// V once in two 16-bit terms (three for fp32 gradients of bf16 activations),
+// after scaling them, for fp16, by the power of two that the adapter's largest
+// value gives; done by every CTA of wgrad for itself, that work took longer than
+// its wide operand (125 us of 8192 x (4096 + 14336) bf16 at rank 64).
 #include <algorithm>
 #include <atomic>
 
@@ -195,10 +197,61 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
 // ------------------------------------------------------------------ wgrad
 constexpr int kCols = 256;                       // of a CTA: two halves of 128
 constexpr int kWideBytes = kStep * kCols * 2;    // a step: four 64-column blocks
-constexpr int kWideStages = 4;
-constexpr int kThinBufs = 2;
-constexpr int kConvWarps = 8;
-constexpr int kWgThreads = 64 + 32 * kConvWarps;
+constexpr int kWgThreads = 64 + 8 * 32;          // TMA, MMA, eight warps that mask and read the sums back
+
+// ------------------------------------------------------------------ terms
+// 2^exponent brings values up to `largest` (as bits) within [2^14, 2^15).
+__device__ __forceinline__ int fp16_exponent(unsigned largest) {
+    const int ef = static_cast<int>((largest >> 23) & 0xFFu);
+    return ef == 0 || ef == 255 ? 0 : min(max(14 - (ef - 127), -100), 100);
+}
+
+// The largest |value| of an adapter's G (which = 0) or V (1), from the shrink launch; every thread of the block calls it.
+__device__ __forceinline__ unsigned largest_of(const float *tile_max, const int *tile_adapter, int parts, int which, int a, unsigned *smax) {
+    float mx = 0.f;
+    for (int i = threadIdx.x; i < parts; i += blockDim.x)
+        if (__ldcg(tile_adapter + i) == a) mx = fmaxf(mx, __ldcg(tile_max + which * parts + i));
+    atomicMax(smax, __float_as_uint(mx));  // of values that are not negative: the order does not matter
+    __syncthreads();
+    return *smax;
+}
+
+// G and V of a tile of rows as 16-bit terms [which][term][T][rank].
+template <int TERMS, bool BF16>
+__global__ void __launch_bounds__(256) lora_terms_kernel(const TermsTc q) {
+    __shared__ unsigned smax[2];
+    const LoraProblem &p = q.p;
+    pdl_launch_dependents();
+    pdl_wait();
+    RowTile t;
+    if (!find_tile(p, blockIdx.x, kTileRows, false, t) || t.rows == 0 || t.adapter < 0) return;
+    const int which = blockIdx.y;
+    float up = 1.f;
+    if (!BF16) {
+        if (threadIdx.x == 0) smax[which] = 0;
+        __syncthreads();
+        up = exp2i(fp16_exponent(largest_of(q.tile_max, q.tile_adapter, q.parts, which, t.adapter, smax + which)));
+    }
+    const size_t all = static_cast<size_t>(p.T) * p.r, first = static_cast<size_t>(t.t0) * p.r;
+    const float *src = q.skinny[which] + first;
+    uint16_t *dst = q.terms + which * TERMS * all + first;
+    for (int e = threadIdx.x * 4; e < t.rows * p.r; e += 1024) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + e));
+        float x[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
+#pragma unroll
+        for (int m = 0; m < TERMS; ++m) {
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // the next 8 or 11 bits of each value; an infinity or NaN is its own first term
+                const uint16_t h = BF16 ? f2bf(x[k]) : f2h(x[k]);
+                const float f = BF16 ? bf2f(h) : h2f(h);
+                x[k] = fabsf(f) < __int_as_float(0x7f800000) ? x[k] - f : 0.f;
+                w[k >> 1] = (k & 1) ? w[k >> 1] | static_cast<uint32_t>(h) << 16 : h;
+            }
+            *reinterpret_cast<uint2 *>(dst + m * all + e) = make_uint2(w[0], w[1]);
+        }
+    }
+}
 
 // The 64-row steps of an adapter's requests that belong to CTA `rank` of `cs`, walked by a whole warp.
 struct StepWalk {
@@ -237,17 +290,15 @@ struct StepWalk {
 };
 
 template <int TERMS, bool BF16>
-__global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map,
-                                                                      const __grid_constant__ CUtensorMap dy_map, const WgradTc q) {
+__global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap dy_map,
+                                                                      const __grid_constant__ CUtensorMap thin_map, const WgradTc q) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const LoraProblem &p = q.p;
-    const int blocks = q.n > 64 ? 2 : 1;             // 64-column blocks of the thin operand
-    const int term_bytes = blocks * kBlock, thin_bytes = TERMS * term_bytes;
-    unsigned char *wide = sm, *thin = sm + kWideStages * kWideBytes;
-    unsigned char *bars = thin + kThinBufs * thin_bytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + kWideStages;
-    uint64_t *tfull = empty + kWideStages, *tempty = tfull + kThinBufs, *accf = tempty + kThinBufs;
+    const int blocks = q.n > 64 ? 2 : 1;  // 64-column blocks of the thin operand
+    const int term_bytes = blocks * kBlock, thin_bytes = TERMS * term_bytes, stage_bytes = kWideBytes + thin_bytes;
+    unsigned char *bars = sm + q.stages * stage_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + q.stages, *masked = empty + q.stages, *accf = masked + q.stages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     unsigned *smax = tmem_slot + 2;
@@ -257,7 +308,6 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
     const int which = tile >= q.tiles[0];
     if (which) tile -= q.tiles[0];
     const int a = blockIdx.y, col0 = tile * kCols, r = p.r;
-    const float *skinny = q.skinny[which];
     pdl_launch_dependents();
     pdl_wait();
     int bad = 0;
@@ -266,13 +316,10 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
         bad |= hi < lo || lo < 0 || hi > p.T || (s == 0 && lo != 0);
     }
     if (tid == 0) {
-        for (int i = 0; i < kWideStages; ++i) {
+        for (int i = 0; i < q.stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < kThinBufs; ++i) {
-            mbar_init(&tfull[i], kConvWarps);
-            mbar_init(&tempty[i], 1);
+            mbar_init(&masked[i], 8);
         }
         mbar_init(accf, 1);
         *abort_flag = 0;
@@ -282,24 +329,12 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
     if (__syncthreads_or(bad)) return;  // the whole cluster
     const uint32_t cols = pow2_cols(2 * q.n);
     if (warp == 1) tmem_alloc(tmem_slot, cols);
-    // Columns j >= r of the thin operand stay zero for the whole kernel.
-    for (int e = tid; e < kThinBufs * thin_bytes / 16; e += kWgThreads) reinterpret_cast<uint4 *>(thin)[e] = make_uint4(0, 0, 0, 0);
-    if (!BF16) {  // the adapter's largest value
-        float mx = 0.f;
-        for (int i = tid; i < q.parts; i += kWgThreads)
-            if (__ldcg(q.tile_adapter + i) == a) mx = fmaxf(mx, __ldcg(q.tile_max + which * q.parts + i));
-        atomicMax(smax, __float_as_uint(mx));
-    }
-    fence_async_smem();
+    float down = 1.f;
+    if (!BF16) down = exp2i(-fp16_exponent(largest_of(q.tile_max, q.tile_adapter, q.parts, which, a, smax)));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    int exponent = 0;  // fp16: the thin operand times 2^exponent lies within [2^14, 2^15) at most
-    if (!BF16) {
-        const int ef = static_cast<int>((*smax >> 23) & 0xFFu);
-        exponent = ef == 0 || ef == 255 ? 0 : min(max(14 - (ef - 127), -100), 100);
-    }
     StepWalk walk(rank);
     int t0, rows, steps = 0;
     bool ok = true;
@@ -307,12 +342,16 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
         const CUtensorMap *map = which ? &dy_map : &x_map;
         while (walk.next(p, a, q.cs, t0, rows)) {
             if (lane == 0) {
-                const int s = steps % kWideStages;
-                ok = mbar_wait(&empty[s], ((steps / kWideStages) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC);
+                const int s = steps % q.stages;
+                ok = mbar_wait(&empty[s], ((steps / q.stages) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC);
                 if (ok) {
-                    mbar_arrive_expect_tx(&full[s], kWideBytes);
+                    unsigned char *dst = sm + s * stage_bytes;
+                    mbar_arrive_expect_tx(&full[s], stage_bytes);
 #pragma unroll
-                    for (int b = 0; b < kCols / 64; ++b) tma_load_2d(wide + s * kWideBytes + b * kBlock, map, col0 + 64 * b, t0, &full[s]);
+                    for (int b = 0; b < kCols / 64; ++b) tma_load_2d(dst + b * kBlock, map, col0 + 64 * b, t0, &full[s]);
+                    for (int m = 0; m < TERMS; ++m)
+                        for (int b = 0; b < blocks; ++b)
+                            tma_load_3d(dst + kWideBytes + m * term_bytes + b * kBlock, &thin_map, 64 * b, t0, which * TERMS + m, &full[s]);
                 }
             }
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -323,13 +362,14 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
         const bool two = col0 + 128 < q.cols[which];
         while (walk.next(p, a, q.cs, t0, rows)) {
             if (lane == 0) {
-                const int s = steps % kWideStages, b = steps % kThinBufs;
-                ok = mbar_wait(&full[s], (steps / kWideStages) & 1, abort_flag, q.fault, FAULT_WAIT_TC) &&
-                     mbar_wait(&tfull[b], (steps / kThinBufs) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
+                const int s = steps % q.stages;
+                ok = mbar_wait(&full[s], (steps / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC) &&
+                     mbar_wait(&masked[s], (steps / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
                 if (ok) {
                     tc_fence_after();
-                    const uint64_t ad = sdesc_mn(smem_u32(wide + s * kWideBytes)), ad1 = sdesc_mn(smem_u32(wide + s * kWideBytes + 2 * kBlock));
-                    const uint64_t bd = sdesc_mn(smem_u32(thin + b * thin_bytes));
+                    const uint32_t at = smem_u32(sm + s * stage_bytes);
+                    const uint64_t ad = sdesc_mn(at), ad1 = sdesc_mn(at + 2 * kBlock), bd = sdesc_mn(at + kWideBytes);
+#pragma unroll
                     for (int m = TERMS - 1; m >= 0; --m)
 #pragma unroll
                         for (int k = 0; k < kStep / 16; ++k) {
@@ -339,7 +379,6 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
                             if (two) umma_f16(tmem + q.n, ad1 + 128 * k, bk, idesc, acc);
                         }
                     umma_commit(&empty[s]);
-                    umma_commit(&tempty[b]);
                 }
             }
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -348,72 +387,23 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
         if (lane == 0) umma_commit(accf);
         __syncwarp();
     } else {
-        // Converters: task = 8 values j of a row; 8 lanes of a quarter warp write 8 rows' chunks without conflicts.
-        const int u = tid - 64, tasks = kStep * (r / 8);
-        const float up = exp2i(exponent);
-        constexpr int MAXT = 4;  // tasks of a thread: rank 128
-        float4 v[MAXT][2];
-        int nt0, nrows;
-        bool more = walk.next(p, a, q.cs, nt0, nrows);
-        auto fetch = [&]() {
-#pragma unroll
-            for (int i = 0; i < MAXT; ++i) {
-                const int e = u + i * 32 * kConvWarps;
-                if (e >= tasks) break;
-                const int t = e & 63, c = e >> 6;
-                v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (t < nrows) {
-                    const float4 *src = reinterpret_cast<const float4 *>(skinny + static_cast<size_t>(nt0 + t) * r + c * 8);
-                    v[i][0] = __ldcg(src);
-                    v[i][1] = __ldcg(src + 1);
-                }
-            }
-        };
-        if (more) fetch();
-        while (more) {
-            const int b = steps % kThinBufs, s = steps % kWideStages;
-            rows = nrows;
-            ok = mbar_wait(&tempty[b], ((steps / kThinBufs) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC);
+        // A request that ends inside a step: the rows behind it become zeros in both operands (either may hold a NaN).
+        const int u = tid - 64;
+        while (walk.next(p, a, q.cs, t0, rows)) {
+            const int s = steps % q.stages;
+            ok = mbar_wait(&full[s], (steps / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
             if (!__all_sync(0xffffffffu, ok)) break;
-#pragma unroll
-            for (int i = 0; i < MAXT; ++i) {
-                const int e = u + i * 32 * kConvWarps;
-                if (e >= tasks) break;
-                const int t = e & 63, c = e >> 6;
-                float x[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-                unsigned char *dst = thin + b * thin_bytes + (c >> 3) * kBlock + (t >> 3) * 1024 + (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4);
-                if (!BF16) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] *= up;
+            if (rows < kStep) {
+                const int gone = kStep - rows, chunks = (kCols / 64 + TERMS * blocks) * 8;
+                for (int e = u; e < gone * chunks; e += 256) {
+                    const int row = rows + e / chunks, c = e % chunks;
+                    *reinterpret_cast<uint4 *>(sm + s * stage_bytes + (c >> 3) * kBlock + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
-#pragma unroll
-                for (int m = 0; m < TERMS; ++m) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {  // the next 8 or 11 bits of each value; an infinity or NaN is its own first term
-                        const uint16_t h = BF16 ? f2bf(x[k]) : f2h(x[k]);
-                        const float f = BF16 ? bf2f(h) : h2f(h);
-                        x[k] = fabsf(f) < __int_as_float(0x7f800000) ? x[k] - f : 0.f;
-                        w[k >> 1] = (k & 1) ? w[k >> 1] | static_cast<uint32_t>(h) << 16 : h;
-                    }
-                    *reinterpret_cast<uint4 *>(dst + m * term_bytes) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                fence_async_smem();
+                __syncwarp();
             }
-            if (rows < kStep) {  // the request ends inside the step: what follows it must not meet the zeros as a NaN
-                ok = mbar_wait(&full[s], (steps / kWideStages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                const int gone = kStep - rows;
-                for (int e = u; e < gone * (kCols / 8); e += 32 * kConvWarps) {
-                    const int row = rows + e / (kCols / 8), c = e % (kCols / 8);
-                    *reinterpret_cast<uint4 *>(wide + s * kWideBytes + (c >> 3) * kBlock + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tfull[b]);
+            if (lane == 0) mbar_arrive(&masked[s]);
             ++steps;
-            more = walk.next(p, a, q.cs, nt0, nrows);
-            if (more) fetch();
         }
         ok = mbar_wait(accf, 0, abort_flag, q.fault, FAULT_WAIT_TC) && ok;
     }
@@ -445,7 +435,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
         cluster_wait();
     }
     const int ncol = min(kCols, q.cols[which] - col0), width = kCols / q.cs;
-    const float scale = (which && p.scaling ? __ldg(p.scaling + a) : 1.f) * (BF16 ? 1.f : exp2i(-exponent));
+    const float scale = (which && p.scaling ? __ldg(p.scaling + a) : 1.f) * down;
     for (int e = tid; e < r * width; e += kWgThreads) {
         const int j = which ? e % r : e / width, cc = rank * width + (which ? e / r : e % width);
         if (cc >= ncol) continue;
@@ -517,8 +507,33 @@ cudaError_t launch_shrink_tc(ShrinkTc q, const void *in, int64_t ld, const void 
                           w_map, q);
 }
 
-cudaError_t launch_wgrad_tc(WgradTc q, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16, cudaStream_t s) {
+namespace {
+
+template <int TERMS, bool BF16>
+cudaError_t launch_wgrad_terms(WgradTc q, const TermsTc &c, const CUtensorMap *maps, cudaStream_t s) {
     const LoraProblem &p = q.p;
+    cudaError_t e = launch_pdl(lora_terms_kernel<TERMS, BF16>, dim3(static_cast<unsigned>(shrink_tc_tiles(p.T, p.S)), 2), dim3(256), 0, s, c);
+    if (e != cudaSuccess) return e;
+    const int stage = kWideBytes + TERMS * (q.n > 64 ? 2 : 1) * kBlock;
+    q.stages = std::min(4, (227 * 1024 - 1024 - kBars) / stage);
+    const int smem = 1024 + std::max(q.stages * stage, q.n * (kCols + 4) * 4) + kBars;
+    static std::atomic<unsigned long long> done{0};
+    e = allow_smem(lora_wgrad_tc_kernel<TERMS, BF16>, done, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_cluster(lora_wgrad_tc_kernel<TERMS, BF16>, dim3(static_cast<unsigned>(q.tiles[0] + q.tiles[1]) * q.cs, p.na), dim3(kWgThreads), smem, s, q.cs,
+                          maps[0], maps[1], maps[2], q);
+}
+
+int terms_of(bool bf16, int g_dtype) { return bf16 && g_dtype == kF32 ? 3 : 2; }
+
+}  // namespace
+
+size_t wgrad_tc_terms_bytes(int T, int r) { return static_cast<size_t>(2) * 3 * T * r * 2; }
+
+cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t *terms, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16,
+                            cudaStream_t s) {
+    const LoraProblem &p = q.p;
+    const int nt = terms_of(bf16, q.g_dtype);
     q.n = thin_cols(p.r);
     q.cols[0] = p.K;
     q.cols[1] = p.N;
@@ -528,31 +543,26 @@ cudaError_t launch_wgrad_tc(WgradTc q, const void *x, int64_t ldx, const void *d
     const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * p.na;
     q.cs = 1;
     while (q.cs < 8 && ctas * q.cs * 2 <= device_info().sm_count && p.T / p.na >= 16 * kStep * q.cs) q.cs *= 2;
-    CUtensorMap maps[2];
-    const cuuint32_t box[2] = {64, kStep};
+    CUtensorMap maps[3];
+    const cuuint32_t box[3] = {64, kStep, 1};
     for (int w = 0; w < 2; ++w) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(q.cols[w]), static_cast<cuuint64_t>(p.T)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(w ? lddy : ldx) * 2};
         if (!make_map(maps[w], bf16, w ? dy : x, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    const int terms = bf16 && q.g_dtype == kF32 ? 3 : 2;
-    const int thin = terms * (q.n > 64 ? 2 : 1) * kBlock;
-    const int smem = 1024 + std::max(kWideStages * kWideBytes + kThinBufs * thin, q.n * (kCols + 4) * 4) + kBars;
-    const dim3 grid(static_cast<unsigned>(q.tiles[0] + q.tiles[1]) * q.cs, p.na);
-    constexpr int kMost = 227 * 1024;
-    if (terms == 3) {
-        static std::atomic<unsigned long long> done{0};
-        const cudaError_t e = allow_smem(lora_wgrad_tc_kernel<3, true>, done, kMost);
-        return e != cudaSuccess ? e : launch_cluster(lora_wgrad_tc_kernel<3, true>, grid, dim3(kWgThreads), smem, s, q.cs, maps[0], maps[1], q);
-    }
-    if (bf16) {
-        static std::atomic<unsigned long long> done{0};
-        const cudaError_t e = allow_smem(lora_wgrad_tc_kernel<2, true>, done, kMost);
-        return e != cudaSuccess ? e : launch_cluster(lora_wgrad_tc_kernel<2, true>, grid, dim3(kWgThreads), smem, s, q.cs, maps[0], maps[1], q);
-    }
-    static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = allow_smem(lora_wgrad_tc_kernel<2, false>, done, kMost);
-    return e != cudaSuccess ? e : launch_cluster(lora_wgrad_tc_kernel<2, false>, grid, dim3(kWgThreads), smem, s, q.cs, maps[0], maps[1], q);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.r), static_cast<cuuint64_t>(p.T), static_cast<cuuint64_t>(2 * nt)};
+    const cuuint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
+    if (!make_map(maps[2], bf16, terms, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    TermsTc c{};
+    c.p = p;
+    c.skinny[0] = G;
+    c.skinny[1] = V;
+    c.terms = terms;
+    c.tile_max = q.tile_max;
+    c.tile_adapter = q.tile_adapter;
+    c.parts = q.parts;
+    if (nt == 3) return launch_wgrad_terms<3, true>(q, c, maps, s);
+    return bf16 ? launch_wgrad_terms<2, true>(q, c, maps, s) : launch_wgrad_terms<2, false>(q, c, maps, s);
 }
 
 }  // namespace qg

@@ -17,21 +17,31 @@ struct ShrinkTc {
     unsigned *fault;
 };
 
-struct WgradTc {
+struct TermsTc {
     LoraProblem p;
     const float *skinny[2];  // G, V
+    uint16_t *terms;         // [2][terms][T][rank]
+    const float *tile_max;
+    const int *tile_adapter;
+    int parts;
+};
+
+struct WgradTc {
+    LoraProblem p;
     void *out[2];            // dA, dB
     int g_dtype, accumulate;
     const float *tile_max;   // of the shrink launch before it
     const int *tile_adapter;
     int parts;               // its CTAs
-    int cols[2], tiles[2], n, cs;  // filled in by the launch
+    int cols[2], tiles[2], n, cs, stages;  // filled in by the launch
     unsigned *fault;
 };
 
 bool lora_tc_available();
 int shrink_tc_tiles(int T, int S);
 cudaError_t launch_shrink_tc(ShrinkTc q, const void *in, int64_t ld, const void *w, cudaStream_t s);
-cudaError_t launch_wgrad_tc(WgradTc q, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16, cudaStream_t s);
+size_t wgrad_tc_terms_bytes(int T, int r);  // room for the 16-bit terms of G and V
+cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t *terms, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16,
+                            cudaStream_t s);
 
 }  // namespace qg
