@@ -11,10 +11,12 @@
 // Layouts (128-byte swizzle).  K-major operands have the contraction along
 // their rows; MN-major ones come as [64-column block][row] straight from
 // row-major memory, so nothing is transposed:
-//             wide operand (A)                 thin operand (B)
-//   forward   X, K-major, 128 rows             A[a], K-major
-//   backward  dY, K-major, 128 rows            B[a], MN-major
-//   wgrad     X or dY, MN-major, 2 x 128 cols  G or V, MN-major, in 16-bit terms
+//             MMA operand A (128)          MMA operand B
+//   forward   X, K-major, 128 rows         A[a], K-major
+//   backward  dY, K-major, 128 rows        B[a], MN-major
+//   wgrad     G or V, MN-major, 16-bit     X or dY, MN-major, 256 columns
+// (wgrad the other way round, the wide operand as A in two halves and N = the
+// rank, kept the tensor pipe busy for 116 cycles an MMA and was bound by it.)
 // The thin operand of wgrad is fp32.  A small kernel between the two splits G and
 // V once in two 16-bit terms (three for fp32 gradients of bf16 activations),
 // after scaling them, for fp16, by the power of two that the adapter's largest
@@ -43,10 +45,10 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// MN-major operand: 64-column blocks kBlock bytes apart, 8-row groups 1024.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+// MN-major operand: 64-column blocks `block` bytes apart, 8-row groups 1024.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, int block = kBlock) {
     uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(kBlock >> 4) << 16;
+    d |= static_cast<uint64_t>(block >> 4) << 16;
     d |= static_cast<uint64_t>(1024 >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
 }
 
 // ------------------------------------------------------------------ wgrad
-constexpr int kCols = 256;                       // of a CTA: two halves of 128
+constexpr int kCols = 256;                       // of a CTA
 constexpr int kWideBytes = kStep * kCols * 2;    // a step: four 64-column blocks
 constexpr int kWgThreads = 64 + 8 * 32;          // TMA, MMA, eight warps that mask and read the sums back
 
@@ -327,8 +329,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
         mbar_fence_init();
     }
     if (__syncthreads_or(bad)) return;  // the whole cluster
-    const uint32_t cols = pow2_cols(2 * q.n);
-    if (warp == 1) tmem_alloc(tmem_slot, cols);
+    if (warp == 1) tmem_alloc(tmem_slot, kCols);
     float down = 1.f;
     if (!BF16) down = exp2i(-fp16_exponent(largest_of(q.tile_max, q.tile_adapter, q.parts, which, a, smax)));
     tc_fence_before();
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
             ++steps;
         }
     } else if (warp == 1) {
-        const uint32_t idesc = idesc_f16(128, q.n, BF16) | (1u << 15) | (1u << 16);  // both MN-major
-        const bool two = col0 + 128 < q.cols[which];
+        constexpr uint32_t idesc = idesc_f16(128, kCols, BF16) | (1u << 15) | (1u << 16);  // both MN-major
+        const int thin_block = blocks == 2 ? kBlock : 0;  // up to rank 64 rows 64 .. 127 repeat the first ones, unread
         while (walk.next(p, a, q.cs, t0, rows)) {
             if (lane == 0) {
                 const int s = steps % q.stages;
@@ -368,16 +369,12 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
                 if (ok) {
                     tc_fence_after();
                     const uint32_t at = smem_u32(sm + s * stage_bytes);
-                    const uint64_t ad = sdesc_mn(at), ad1 = sdesc_mn(at + 2 * kBlock), bd = sdesc_mn(at + kWideBytes);
+                    const uint64_t ad = sdesc_mn(at + kWideBytes, thin_block), bd = sdesc_mn(at);
 #pragma unroll
                     for (int m = TERMS - 1; m >= 0; --m)
 #pragma unroll
-                        for (int k = 0; k < kStep / 16; ++k) {
-                            const uint64_t bk = bd + m * (term_bytes >> 4) + 128 * k;
-                            const uint32_t acc = steps > 0 || k > 0 || m < TERMS - 1;
-                            umma_f16(tmem, ad + 128 * k, bk, idesc, acc);
-                            if (two) umma_f16(tmem + q.n, ad1 + 128 * k, bk, idesc, acc);
-                        }
+                        for (int k = 0; k < kStep / 16; ++k)
+                            umma_f16(tmem, ad + m * (term_bytes >> 4) + 128 * k, bd + 128 * k, idesc, steps > 0 || k > 0 || m < TERMS - 1);
                     umma_commit(&empty[s]);
                 }
             }
@@ -414,20 +411,25 @@ __global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __gr
     __syncthreads();
     if (warp >= 2) {
         tc_fence_after();
-        const int sub = warp & 3, half = (warp - 2) >> 2;  // 32 columns of a half; the half
-        for (int c = 0; c < q.n; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + half * q.n + c, v);
+        const int sub = warp & 3, half = (warp - 2) >> 2;  // 32 values j; the half of the columns
+        if (sub * 32 < r)
+#pragma unroll 1
+            for (int c = half * 128; c < half * 128 + 128; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + c, v);
+                if (sub * 32 + lane >= r) continue;
+                float4 *dst = reinterpret_cast<float4 *>(sums + (sub * 32 + lane) * OS + c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (c + i < q.n) sums[(c + i) * OS + half * 128 + sub * 32 + lane] = ok && steps > 0 ? __uint_as_float(v[i]) : 0.f;
-        }
+                for (int i = 0; i < 8; ++i)
+                    dst[i] = ok && steps > 0 ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         tc_fence_before();
     }
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, cols);
+        tmem_dealloc(tmem, kCols);
         __syncwarp();
     }
     if (q.cs > 1) {
