@@ -292,7 +292,7 @@ struct StepWalk {
 };
 
 template <int TERMS, bool BF16>
-__global__ void __launch_bounds__(kWgThreads, 1) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap dy_map,
+__global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap dy_map,
                                                                       const __grid_constant__ CUtensorMap thin_map, const WgradTc q) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -517,7 +517,11 @@ cudaError_t launch_wgrad_terms(WgradTc q, const TermsTc &c, const CUtensorMap *m
     cudaError_t e = launch_pdl(lora_terms_kernel<TERMS, BF16>, dim3(static_cast<unsigned>(shrink_tc_tiles(p.T, p.S)), 2), dim3(256), 0, s, c);
     if (e != cudaSuccess) return e;
     const int stage = kWideBytes + TERMS * (q.n > 64 ? 2 : 1) * kBlock;
-    q.stages = std::min(4, (227 * 1024 - 1024 - kBars) / stage);
+    // More CTAs than SMs: two on an SM, with half the ring each, so that one's start and end run under the other's loads.
+    constexpr int kOverhead = 1024 + kBars;
+    q.stages = std::min(4, (227 * 1024 - kOverhead) / stage);
+    const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * q.cs * p.na;
+    if (ctas > device_info().sm_count && 2 * stage + kOverhead <= 111 * 1024) q.stages = 2;
     const int smem = 1024 + std::max(q.stages * stage, q.n * (kCols + 4) * 4) + kBars;
     static std::atomic<unsigned long long> done{0};
     e = allow_smem(lora_wgrad_tc_kernel<TERMS, BF16>, done, 227 * 1024);
