@@ -40,7 +40,8 @@ struct RowsArgs {
     int in_vec, out_vec; // rows at 16-byte boundaries: vector accesses
 };
 
-template <int XT, int WT, bool BWD, int MT, int RG, int NT>
+// GIVEN: the sums of the first product are known (another launch made them).
+template <int XT, int WT, bool BWD, int MT, int RG, int NT, bool GIVEN>
 struct RowsKernel {
     static constexpr bool NATIVE = XT != kF32;
     static constexpr int KG = 8 / RG;              // warps sharing the rows of a group
@@ -242,8 +243,8 @@ struct RowsKernel {
     static constexpr int BASE_PIECES = 2 * MT * BW;  // of a lane and group
     static constexpr int BASE_BYTES = 8 * STAGES * BASE_PIECES * 512;
     static __host__ __device__ int queue_offset(int r) { return r > RC ? sums_bytes(r) : 0; }  // several passes: their sums stay
-    static __host__ __device__ int smem_bytes(int r, bool given) {
-        if (given) return sums_bytes(r) + frag_bytes(r) + BASE_BYTES;
+    static __host__ __device__ int smem_bytes(int r) {
+        if (GIVEN) return sums_bytes(r) + frag_bytes(r) + BASE_BYTES;
         const int later = PART_BYTES > frag_bytes(r) + BASE_BYTES ? PART_BYTES : frag_bytes(r) + BASE_BYTES;
         return sums_bytes(r) + later > queue_offset(r) + IN_BYTES ? sums_bytes(r) + later : queue_offset(r) + IN_BYTES;
     }
@@ -269,126 +270,129 @@ struct RowsKernel {
         const int ngrp = (q.c2 + 31) / 32;  // 32-column groups of the second product, and this CTA's
         const int n_lo = static_cast<int>(static_cast<int64_t>(ngrp) * rank / q.cs), n_hi = static_cast<int>(static_cast<int64_t>(ngrp) * (rank + 1) / q.cs);
 
-        if (t.adapter >= 0 && q.given) {
+        if (GIVEN && t.adapter >= 0) {
             for (int e = tid; e < R * rp; e += 256) {
                 const int row = e / rp, j = e - row * rp;
                 whole[e] = row < t.rows && j < r ? __ldg(q.given + static_cast<size_t>(t.t0 + row) * r + j) : 0.f;
             }
             __syncthreads();
-        } else if (t.adapter >= 0) {
-            // ---------------------------------------------------------- first product
-            if (R == 16 && q.out) prefetch_w2(q, t.adapter, n_lo * 32, min(n_hi * 32, q.c2));
-            const int nblk = (q.c1 + BLK - 1) / BLK;
-            const int b0 = static_cast<int>(static_cast<int64_t>(nblk) * rank / q.cs), b1 = static_cast<int>(static_cast<int64_t>(nblk) * (rank + 1) / q.cs);
-            const int row0 = rg * 16 * MT;
-            const char *rowp[MT][2];
-            bool rin[MT][2];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = row0 + m * 16 + h * 8 + g;
-                    rin[m][h] = row < t.rows;
-                    rowp[m][h] = static_cast<const char *>(q.in) + static_cast<size_t>(t.t0 + (rin[m][h] ? row : 0)) * q.ld_in * (NATIVE ? 2 : 4);
-                }
-            for (int j0 = 0; j0 < r; j0 += RC) {
-                float acc[MT][NT][4] = {};
-                uint4 *queue = reinterpret_cast<uint4 *>(sm + queue_offset(r)) + warp * (STAGES * PIECES * 32) + lane;
-                auto ahead = [&](int b, int slot) {
-                    if (b < b1) {
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-#pragma unroll
-                            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    queue_in(q, queue + (slot * PIECES + (s * MT + m) * 2 + h) * 32, rowp[m][h], b * BLK + s * CH + c * EL, rin[m][h]);
-                    }
-                    queue_commit();
-                };
-                if (j0) __syncthreads();  // the queues lie over the partial sums of the previous pass
-#pragma unroll
-                for (int i = 0; i < STAGES - 1; ++i) ahead(b0 + kg + i * KG, i);
-                int slot = 0;
-                for (int b = b0 + kg; b < b1; b += KG) {
-                    ahead(b + (STAGES - 1) * KG, slot == 0 ? STAGES - 1 : slot - 1);
-                    queue_wait<STAGES - 1>();
-                    const uint4 *x = queue + slot * PIECES * 32;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        W1 w;
-                        load_w1(q, t.adapter, j0, b * BLK + s * CH + c * EL, g, w);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            const uint4 x0 = x[((s * MT + m) * 2) * 32], x1 = x[((s * MT + m) * 2 + 1) * 32];
-                            if constexpr (NATIVE) {
-#pragma unroll
-                                for (int i = 0; i < NT; ++i) {
-                                    mma16<XT>(acc[m][i], x0.x, x1.x, x0.y, x1.y, w1_word(w, i, 0), w1_word(w, i, 1));
-                                    mma16<XT>(acc[m][i], x0.z, x1.z, x0.w, x1.w, w1_word(w, i, 2), w1_word(w, i, 3));
-                                }
-                            } else {
-#pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    uint32_t hi[4], lo[4];
-                                    split_tf32(__uint_as_float(half ? x0.z : x0.x), hi[0], lo[0]);
-                                    split_tf32(__uint_as_float(half ? x1.z : x1.x), hi[1], lo[1]);
-                                    split_tf32(__uint_as_float(half ? x0.w : x0.y), hi[2], lo[2]);
-                                    split_tf32(__uint_as_float(half ? x1.w : x1.y), hi[3], lo[3]);
-#pragma unroll
-                                    for (int i = 0; i < NT; ++i) mma_tf32_split(acc[m][i], hi, lo, w1_word(w, i, 2 * half), w1_word(w, i, 2 * half + 1));
-                                }
-                            }
-                        }
-                    }
-                    slot = slot == STAGES - 1 ? 0 : slot + 1;
-                }
-                queue_wait<0>();
-                __syncthreads();  // every lane is done with its queue
-                const int jn = min(RC, r - j0);
+        }
+        if constexpr (!GIVEN) {
+            if (t.adapter >= 0) {
+                // ---------------------------------------------------------- first product
+                if (R == 16 && q.out) prefetch_w2(q, t.adapter, n_lo * 32, min(n_hi * 32, q.c2));
+                const int nblk = (q.c1 + BLK - 1) / BLK;
+                const int b0 = static_cast<int>(static_cast<int64_t>(nblk) * rank / q.cs), b1 = static_cast<int>(static_cast<int64_t>(nblk) * (rank + 1) / q.cs);
+                const int row0 = rg * 16 * MT;
+                const char *rowp[MT][2];
+                bool rin[MT][2];
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = row0 + m * 16 + h * 8 + g;
+                        rin[m][h] = row < t.rows;
+                        rowp[m][h] = static_cast<const char *>(q.in) + static_cast<size_t>(t.t0 + (rin[m][h] ? row : 0)) * q.ld_in * (NATIVE ? 2 : 4);
+                    }
+                for (int j0 = 0; j0 < r; j0 += RC) {
+                    float acc[MT][NT][4] = {};
+                    uint4 *queue = reinterpret_cast<uint4 *>(sm + queue_offset(r)) + warp * (STAGES * PIECES * 32) + lane;
+                    auto ahead = [&](int b, int slot) {
+                        if (b < b1) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int col = 2 * c + (e & 1), row = row0 + m * 16 + (e >> 1) * 8 + g;
-                            part[(kg * R + row) * PS + (BWD ? col * NT + i : i * 8 + col)] = acc[m][i][e];
+                            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h)
+                                        queue_in(q, queue + (slot * PIECES + (s * MT + m) * 2 + h) * 32, rowp[m][h], b * BLK + s * CH + c * EL, rin[m][h]);
                         }
-                __syncthreads();
-                for (int e = tid; e < R * jn; e += 256) {
-                    const int row = e / jn, j = e - row * jn;
-                    float s = 0.f;
+                        queue_commit();
+                    };
+                    if (j0) __syncthreads();  // the queues lie over the partial sums of the previous pass
 #pragma unroll
-                    for (int w = 0; w < KG; ++w) s += part[(w * R + row) * PS + j];
-                    mine[row * rp + j0 + j] = s;
+                    for (int i = 0; i < STAGES - 1; ++i) ahead(b0 + kg + i * KG, i);
+                    int slot = 0;
+                    for (int b = b0 + kg; b < b1; b += KG) {
+                        ahead(b + (STAGES - 1) * KG, slot == 0 ? STAGES - 1 : slot - 1);
+                        queue_wait<STAGES - 1>();
+                        const uint4 *x = queue + slot * PIECES * 32;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            W1 w;
+                            load_w1(q, t.adapter, j0, b * BLK + s * CH + c * EL, g, w);
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) {
+                                const uint4 x0 = x[((s * MT + m) * 2) * 32], x1 = x[((s * MT + m) * 2 + 1) * 32];
+                                if constexpr (NATIVE) {
+#pragma unroll
+                                    for (int i = 0; i < NT; ++i) {
+                                        mma16<XT>(acc[m][i], x0.x, x1.x, x0.y, x1.y, w1_word(w, i, 0), w1_word(w, i, 1));
+                                        mma16<XT>(acc[m][i], x0.z, x1.z, x0.w, x1.w, w1_word(w, i, 2), w1_word(w, i, 3));
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        uint32_t hi[4], lo[4];
+                                        split_tf32(__uint_as_float(half ? x0.z : x0.x), hi[0], lo[0]);
+                                        split_tf32(__uint_as_float(half ? x1.z : x1.x), hi[1], lo[1]);
+                                        split_tf32(__uint_as_float(half ? x0.w : x0.y), hi[2], lo[2]);
+                                        split_tf32(__uint_as_float(half ? x1.w : x1.y), hi[3], lo[3]);
+#pragma unroll
+                                        for (int i = 0; i < NT; ++i) mma_tf32_split(acc[m][i], hi, lo, w1_word(w, i, 2 * half), w1_word(w, i, 2 * half + 1));
+                                    }
+                                }
+                            }
+                        }
+                        slot = slot == STAGES - 1 ? 0 : slot + 1;
+                    }
+                    queue_wait<0>();
+                    __syncthreads();  // every lane is done with its queue
+                    const int jn = min(RC, r - j0);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int col = 2 * c + (e & 1), row = row0 + m * 16 + (e >> 1) * 8 + g;
+                                part[(kg * R + row) * PS + (BWD ? col * NT + i : i * 8 + col)] = acc[m][i][e];
+                            }
+                    __syncthreads();
+                    for (int e = tid; e < R * jn; e += 256) {
+                        const int row = e / jn, j = e - row * jn;
+                        float s = 0.f;
+#pragma unroll
+                        for (int w = 0; w < KG; ++w) s += part[(w * R + row) * PS + j];
+                        mine[row * rp + j0 + j] = s;
+                    }
                 }
-            }
-            // ---------------------------------------------------------- the cluster's sums
-            if (q.cs > 1) {
-                __syncwarp();
-                cluster_arrive();
-                cluster_wait();
-            } else {
+                // ---------------------------------------------------------- the cluster's sums
+                if (q.cs > 1) {
+                    __syncwarp();
+                    cluster_arrive();
+                    cluster_wait();
+                } else {
+                    __syncthreads();
+                }
+                for (int e = tid; e < R * rp; e += 256) {
+                    const int row = e / rp, j = e - row * rp;
+                    float s = 0.f;
+                    if (j < r) {
+                        if (q.cs > 1)
+                            for (int w = 0; w < q.cs; ++w) s += peer_float(mine + e, w);
+                        else
+                            s = mine[e];
+                        if (BWD) s *= scale;
+                        if (q.sums && rank == 0 && row < t.rows) q.sums[static_cast<size_t>(t.t0 + row) * r + j] = s;
+                    }
+                    whole[e] = s;
+                }
                 __syncthreads();
+                if (q.cs > 1) cluster_arrive();  // done with the peers' memory; awaited before leaving
+            } else if (!BWD && q.sums && rank == 0) {
+                for (int e = tid; e < t.rows * r; e += 256) q.sums[static_cast<size_t>(t.t0) * r + e] = 0.f;
             }
-            for (int e = tid; e < R * rp; e += 256) {
-                const int row = e / rp, j = e - row * rp;
-                float s = 0.f;
-                if (j < r) {
-                    if (q.cs > 1)
-                        for (int w = 0; w < q.cs; ++w) s += peer_float(mine + e, w);
-                    else
-                        s = mine[e];
-                    if (BWD) s *= scale;
-                    if (q.sums && rank == 0 && row < t.rows) q.sums[static_cast<size_t>(t.t0 + row) * r + j] = s;
-                }
-                whole[e] = s;
-            }
-            __syncthreads();
-            if (q.cs > 1) cluster_arrive();  // done with the peers' memory; awaited before leaving
-        } else if (!BWD && q.sums && rank == 0) {
-            for (int e = tid; e < t.rows * r; e += 256) q.sums[static_cast<size_t>(t.t0) * r + e] = 0.f;
         }
         if (t.adapter >= 0) {
             // ---------------------------------------------------------- operand fragments of the sums
@@ -440,9 +444,13 @@ struct RowsKernel {
                     mul[m][h] = BWD ? 1.f : scale;
                     if (XT == kF16 && t.adapter >= 0) mul[m][h] *= rscale[row0 + m * 16 + h * 8 + g];
                 }
-            // the base rows ahead of their sums, when they have the activations' width
             uint4 *queue = reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(frag) + frag_bytes(r)) + warp * (STAGES * BASE_PIECES * 32) + lane;
-            const bool queued = q.base && q.out_vec && (q.base_dtype == kF32) == !NATIVE;
+            int first = n_lo + kg;
+            if (t.adapter >= 0 && q.out_vec && q.out_dtype == XT && (!q.base || q.base_dtype == XT) && units <= UM)
+                first = whole_groups(q, t, first, n_hi, row0, rg, g, c, lane, units, mul, frag, queue);
+            // What is left: the columns that do not fill a group, other types, rows at odd addresses.
+            // The base rows ahead of their sums, when they have the activations' type.
+            const bool queued = q.base && q.out_vec && q.base_dtype == XT;
             auto ahead = [&](int b, int slot) {
                 const int n = b * 32 + c * 8;
                 if (queued && b < n_hi && n + 8 <= q.c2) {
@@ -460,53 +468,19 @@ struct RowsKernel {
                 queue_commit();
             };
 #pragma unroll
-            for (int i = 0; i < STAGES - 1; ++i) ahead(n_lo + kg + i * KG, i);
-            constexpr int UH = NT * 8 / UW <= 4 ? NT * 8 / UW : 1;  // units whose operands a lane holds for the next group
-            const bool held = units <= UH;
-            uint32_t w2[UH][4][2];
-            auto hold = [&](int b) {
-#pragma unroll
-                for (int u = 0; u < UH; ++u)
-                    if (u < units) load_w2(q, t.adapter, u, b * 32, g, c, w2[u]);
-            };
-            if (held && t.adapter >= 0 && n_lo + kg < n_hi) hold(n_lo + kg);
+            for (int i = 0; i < STAGES - 1; ++i) ahead(first + i * KG, i);
             int slot = 0;
-            for (int b = n_lo + kg; b < n_hi; b += KG) {
+            for (int b = first; b < n_hi; b += KG) {
                 ahead(b + (STAGES - 1) * KG, slot == 0 ? STAGES - 1 : slot - 1);
                 const int n0 = b * 32, n = n0 + c * 8;
                 const bool vec = q.out_vec && n + 8 <= q.c2;
                 float acc[MT][4][4] = {};
-                auto multiply = [&](int u, const uint32_t (&w)[4][2]) {
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const int mt = rg * MT + m;
-                        const uint4 h = frag[((mt * units + u) * 2) * 32 + lane], l = frag[((mt * units + u) * 2 + 1) * 32 + lane];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if constexpr (NATIVE) {
-                                mma16<XT>(acc[m][i], l.x, l.y, l.z, l.w, w[i][0], w[i][1]);
-                                mma16<XT>(acc[m][i], h.x, h.y, h.z, h.w, w[i][0], w[i][1]);
-                            } else {
-                                const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
-                                mma_tf32_split(acc[m][i], hh, ll, w[i][0], w[i][1]);
-                            }
-                        }
+                if (t.adapter >= 0)
+                    for (int u = 0; u < units; ++u) {
+                        uint32_t w[4][2];
+                        load_w2(q, t.adapter, u, n0, g, c, w);
+                        multiply(acc, frag, u, units, rg, lane, w);
                     }
-                };
-                if (t.adapter >= 0) {
-                    if (held) {
-#pragma unroll
-                        for (int u = 0; u < UH; ++u)
-                            if (u < units) multiply(u, w2[u]);
-                        if (b + KG < n_hi) hold(b + KG);  // the next group's, while this one's rows are written
-                    } else {
-                        for (int u = 0; u < units; ++u) {
-                            uint32_t w[4][2];
-                            load_w2(q, t.adapter, u, n0, g, c, w);
-                            multiply(u, w);
-                        }
-                    }
-                }
                 queue_wait<STAGES - 1>();
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -515,7 +489,7 @@ struct RowsKernel {
                         const int row = row0 + m * 16 + h * 8 + g;
                         if (row >= t.rows) continue;
                         float y[8];
-                        if (queued && vec) take_base(q, queue + (slot * BASE_PIECES + (m * 2 + h) * BW) * 32, y);
+                        if (queued && vec) take_base(queue + (slot * BASE_PIECES + (m * 2 + h) * BW) * 32, y);
                         else load_base(q, t.t0 + row, n, vec, y);
                         if (t.adapter >= 0) {
 #pragma unroll
@@ -526,10 +500,175 @@ struct RowsKernel {
                 slot = slot == STAGES - 1 ? 0 : slot + 1;
             }
         }
-        if (q.cs > 1 && t.adapter >= 0 && !q.given) {
+        if (!GIVEN && q.cs > 1 && t.adapter >= 0) {
             __syncwarp();
             cluster_wait();
         }
+    }
+
+    static constexpr int UM = NT * 8 / UW;  // most units of a rank up to RC
+
+    static __device__ __forceinline__ void multiply(float (&acc)[MT][4][4], const uint4 *frag, int u, int units, int rg, int lane, const uint32_t (&w)[4][2]) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int mt = rg * MT + m;
+            const uint4 h = frag[((mt * units + u) * 2) * 32 + lane], l = frag[((mt * units + u) * 2 + 1) * 32 + lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (NATIVE) {
+                    mma16<XT>(acc[m][i], l.x, l.y, l.z, l.w, w[i][0], w[i][1]);
+                    mma16<XT>(acc[m][i], h.x, h.y, h.z, h.w, w[i][0], w[i][1]);
+                } else {
+                    const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
+                    mma_tf32_split(acc[m][i], hh, ll, w[i][0], w[i][1]);
+                }
+            }
+        }
+    }
+
+    // The second product over whole 32-column groups, base and outputs in the
+    // activations' type at 16-byte boundaries: addresses are steps from pointers
+    // set up once (computed anew for every group they were two thirds of the
+    // instructions).  Returns the first group that it leaves.
+    static __device__ __forceinline__ int whole_groups(const RowsArgs &q, const RowTile &t, int first, int n_hi, int row0, int rg, int g, int c, int lane,
+                                                       int units, const float (&mul)[MT][2], const uint4 *frag, uint4 *queue) {
+        constexpr int XS = NATIVE ? 2 : 4, WS = WT == kF32 ? 4 : 2;
+        const int end = min(n_hi, q.c2 / 32), r = q.p.r;
+        if (first >= end) return first;
+        const size_t row = static_cast<size_t>(t.t0 + row0 + g);
+        const int64_t base_step = q.ld_base * (8 * XS), out_step = q.ld_out * (8 * XS);  // eight rows
+        const char *base = static_cast<const char *>(q.base) + (row * q.ld_base + first * 32 + c * 8) * XS;
+        char *out = static_cast<char *>(q.out) + (row * q.ld_out + first * 32 + c * 8) * XS;
+        bool in[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) in[m][h] = row0 + m * 16 + h * 8 + g < t.rows;
+        // the lane's adapter values: forward rows n (r values each), backward rows j (c2 values each)
+        const char *w2 = static_cast<const char *>(q.w2) +
+                         (BWD ? (static_cast<size_t>(t.adapter) * r + c * EU) * q.c2 + first * 32 + (g >> 1) * 8
+                              : (static_cast<size_t>(t.adapter) * q.c2 + first * 32 + (g >> 1) * 8 + (g & 1)) * r + c * EU) * WS;
+        const int64_t w_row = static_cast<int64_t>(BWD ? q.c2 : 2 * r) * WS, w_unit = static_cast<int64_t>(BWD ? static_cast<int64_t>(UW) * q.c2 : UW) * WS;
+        const int w_group = KG * 32 * (BWD ? 1 : r) * WS;
+        uint32_t w[UM][4][2];
+        auto load = [&](const char *p) {
+#pragma unroll
+            for (int u = 0; u < UM; ++u) {
+                const bool jin = u * UW + c * EU < r;
+                const char *pu = p + u * w_unit;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[u][i][0] = w[u][i][1] = 0;
+                if (!jin) continue;
+                if constexpr (!BWD) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (NATIVE || WT == kF32) {
+                            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(pu + i * w_row));
+                            w[u][i][0] = v.x, w[u][i][1] = v.y;
+                        } else {
+                            widen(__ldg(reinterpret_cast<const unsigned int *>(pu + i * w_row)), w[u][i][0], w[u][i][1]);
+                        }
+                    }
+                } else if constexpr (NATIVE) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = __ldg(reinterpret_cast<const uint4 *>(pu + e * w_row));
+                    const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[u][i][0] = __byte_perm(word(x[0], i), word(x[1], i), sel);
+                        w[u][i][1] = __byte_perm(word(x[2], i), word(x[3], i), sel);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if constexpr (WT == kF32) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[u][i][e] = __ldg(reinterpret_cast<const unsigned int *>(pu + e * w_row) + 2 * i + (g & 1));
+                        } else {
+                            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(pu + e * w_row));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w[u][i][e] = __float_as_uint(to_float<WT>(static_cast<uint16_t>((g & 1) ? word(x, i) >> 16 : word(x, i) & 0xFFFFu)));
+                        }
+                    }
+                }
+            }
+        };
+        auto ahead = [&](int slot) {  // the base rows at `base`, which moves on
+            if (q.base) {
+                const char *p = base;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int o = 0; o < BW; ++o)
+                            queue_copy<16>(queue + (slot * BASE_PIECES + (m * 2 + h) * BW + o) * 32, in[m][h] ? p + 16 * o : static_cast<const char *>(q.base), in[m][h]);
+                        p += base_step;
+                    }
+                base += KG * 32 * XS;
+            }
+            queue_commit();
+        };
+        int loaded = first;
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i, loaded += KG) {
+            if (loaded < end) ahead(i);
+            else queue_commit();
+        }
+        constexpr bool EARLY = UM <= 4;  // the next group's adapter values while this one's rows are written
+        if (EARLY) load(w2);
+        int slot = 0, b = first;
+        for (; b < end; b += KG, loaded += KG) {
+            if (loaded < end) ahead(slot == 0 ? STAGES - 1 : slot - 1);
+            else queue_commit();
+            if (!EARLY) load(w2);
+            float acc[MT][4][4] = {};
+#pragma unroll
+            for (int u = 0; u < UM; ++u)
+                if (u < units) multiply(acc, frag, u, units, rg, lane, w[u]);
+            w2 += w_group;
+            if (EARLY && b + KG < end) load(w2);
+            queue_wait<STAGES - 1>();
+            char *o = out;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h, o += out_step) {
+                    float y[8];
+                    if (q.base) {
+                        take_base(queue + (slot * BASE_PIECES + (m * 2 + h) * BW) * 32, y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = fmaf(acc[m][e >> 1][h * 2 + (e & 1)], mul[m][h], y[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = acc[m][e >> 1][h * 2 + (e & 1)] * mul[m][h];
+                    }
+                    if (!in[m][h]) continue;
+                    if constexpr (NATIVE) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (XT == kF16) {
+                                const __half2 p = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
+                                v[e] = *reinterpret_cast<const uint32_t *>(&p);
+                            } else {
+                                const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+                                v[e] = *reinterpret_cast<const uint32_t *>(&p);
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(o) = make_uint4(v[0], v[1], v[2], v[3]);
+                    } else {
+                        reinterpret_cast<float4 *>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        reinterpret_cast<float4 *>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    }
+                }
+            out += KG * 32 * XS;
+            slot = slot == STAGES - 1 ? 0 : slot + 1;
+        }
+        queue_wait<0>();
+        return b;
     }
 
     // What the second product will read of its adapter, into the L2 while the first one runs.
@@ -547,17 +686,19 @@ struct RowsKernel {
         }
     }
 
-    // 8 base values from the lane's queue
-    static __device__ __forceinline__ void take_base(const RowsArgs &q, const uint4 *from, float (&v)[8]) {
+    // 8 base values of the activations' type from the lane's queue
+    static __device__ __forceinline__ void take_base(const uint4 *from, float (&v)[8]) {
         const uint4 a = from[0];
-        if constexpr (NATIVE) {
+        if constexpr (XT == kF16) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t x = word(a, i);
-                const uint16_t x0 = static_cast<uint16_t>(x & 0xFFFFu), x1 = static_cast<uint16_t>(x >> 16);
-                v[2 * i] = q.base_dtype == kF16 ? h2f(x0) : bf2f(x0);
-                v[2 * i + 1] = q.base_dtype == kF16 ? h2f(x1) : bf2f(x1);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
             }
+        } else if constexpr (XT == kBF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(word(a, i) << 16), v[2 * i + 1] = __uint_as_float(word(a, i) & 0xFFFF0000u);
         } else {
             const uint4 b = from[32];
 #pragma unroll
@@ -619,28 +760,32 @@ struct RowsPlan {
     int rows, cs, tiles;
 };
 
-template <int XT, int WT, bool BWD, int MT, int RG, int NT>
+template <int XT, int WT, bool BWD, int MT, int RG, int NT, bool GIVEN>
 __global__ void __launch_bounds__(256, 2) lora_rows_kernel(const RowsArgs q) {
-    RowsKernel<XT, WT, BWD, MT, RG, NT>::run(q);
+    RowsKernel<XT, WT, BWD, MT, RG, NT, GIVEN>::run(q);
 }
 
-template <int XT, int WT, bool BWD, int MT, int RG, int NT>
+template <int XT, int WT, bool BWD, int MT, int RG, int NT, bool GIVEN>
 cudaError_t launch_rows_one(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
-    auto kern = lora_rows_kernel<XT, WT, BWD, MT, RG, NT>;
-    const int smem = RowsKernel<XT, WT, BWD, MT, RG, NT>::smem_bytes(q.p.r, q.given != nullptr);
+    auto kern = lora_rows_kernel<XT, WT, BWD, MT, RG, NT, GIVEN>;
+    const int smem = RowsKernel<XT, WT, BWD, MT, RG, NT, GIVEN>::smem_bytes(q.p.r);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_cluster(kern, dim3(static_cast<unsigned>(plan.tiles) * q.cs), dim3(256), smem, s, q.given ? 1 : q.cs, q);
+    return launch_cluster(kern, dim3(static_cast<unsigned>(plan.tiles) * q.cs), dim3(256), smem, s, GIVEN ? 1 : q.cs, q);
+}
+
+template <int XT, int WT, bool BWD, int MT, int RG, bool GIVEN>
+cudaError_t launch_rows_rank(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
+    const int r = q.p.r;
+    return r <= 16 ? launch_rows_one<XT, WT, BWD, MT, RG, 2, GIVEN>(q, plan, s)
+                   : r <= 32 ? launch_rows_one<XT, WT, BWD, MT, RG, 4, GIVEN>(q, plan, s) : launch_rows_one<XT, WT, BWD, MT, RG, 8, GIVEN>(q, plan, s);
 }
 
 template <int XT, int WT, bool BWD>
 cudaError_t launch_rows_shape(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
-    const int r = q.p.r;
-    if (plan.rows == 16)
-        return r <= 16 ? launch_rows_one<XT, WT, BWD, 1, 1, 2>(q, plan, s)
-                       : r <= 32 ? launch_rows_one<XT, WT, BWD, 1, 1, 4>(q, plan, s) : launch_rows_one<XT, WT, BWD, 1, 1, 8>(q, plan, s);
-    return r <= 16 ? launch_rows_one<XT, WT, BWD, 2, 2, 2>(q, plan, s)
-                   : r <= 32 ? launch_rows_one<XT, WT, BWD, 2, 2, 4>(q, plan, s) : launch_rows_one<XT, WT, BWD, 2, 2, 8>(q, plan, s);
+    if constexpr (XT != kF32)  // many rows of 16-bit activations take their sums from the tensor cores
+        if (q.given) return launch_rows_rank<XT, WT, BWD, 2, 2, true>(q, plan, s);
+    return plan.rows == 16 ? launch_rows_rank<XT, WT, BWD, 1, 1, false>(q, plan, s) : launch_rows_rank<XT, WT, BWD, 2, 2, false>(q, plan, s);
 }
 
 // Defined once for each pair of types (qg_lora_bf16.cu and its siblings).
