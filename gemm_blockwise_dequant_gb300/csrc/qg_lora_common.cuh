@@ -14,12 +14,27 @@
 //    are.  The product of two second terms (2^-22) is left out.
 #pragma once
 
+#include <atomic>
+
 #include "qg_device.cuh"
 #include "qg_internal.h"
 
 namespace qg {
 
 constexpr int kF32 = 0, kF16 = 1, kBF16 = 2;
+constexpr int kMaxRank = 128;
+
+// Raises a kernel's shared-memory limit (and allows clusters of 16) once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<unsigned long long> &done, int bytes, bool clusters16 = false) {
+    const int slot = device_slot();
+    const unsigned long long bit = slot < 0 ? 0 : 1ull << slot;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && clusters16) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
 
 template <int T>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -135,8 +150,6 @@ template <int N>
 __device__ __forceinline__ void queue_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }

@@ -280,7 +280,6 @@ struct RowsKernel {
         if constexpr (!GIVEN) {
             if (t.adapter >= 0) {
                 // ---------------------------------------------------------- first product
-                if (R == 16 && q.out) prefetch_w2(q, t.adapter, n_lo * 32, min(n_hi * 32, q.c2));
                 const int nblk = (q.c1 + BLK - 1) / BLK;
                 const int b0 = static_cast<int>(static_cast<int64_t>(nblk) * rank / q.cs), b1 = static_cast<int>(static_cast<int64_t>(nblk) * (rank + 1) / q.cs);
                 const int row0 = rg * 16 * MT;
@@ -315,12 +314,18 @@ struct RowsKernel {
                     int slot = 0;
                     for (int b = b0 + kg; b < b1; b += KG) {
                         ahead(b + (STAGES - 1) * KG, slot == 0 ? STAGES - 1 : slot - 1);
+                        constexpr bool TOGETHER = NT <= 4;  // both chunks' adapter values, under the wait for the row
+                        W1 wb[TOGETHER ? 2 : 1];
+                        if (TOGETHER) {
+                            load_w1(q, t.adapter, j0, b * BLK + c * EL, g, wb[0]);
+                            load_w1(q, t.adapter, j0, b * BLK + CH + c * EL, g, wb[TOGETHER ? 1 : 0]);
+                        }
                         queue_wait<STAGES - 1>();
                         const uint4 *x = queue + slot * PIECES * 32;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            W1 w;
-                            load_w1(q, t.adapter, j0, b * BLK + s * CH + c * EL, g, w);
+                            if (!TOGETHER) load_w1(q, t.adapter, j0, b * BLK + s * CH + c * EL, g, wb[0]);
+                            const W1 &w = wb[TOGETHER ? s : 0];
 #pragma unroll
                             for (int m = 0; m < MT; ++m) {
                                 const uint4 x0 = x[((s * MT + m) * 2) * 32], x1 = x[((s * MT + m) * 2 + 1) * 32];
@@ -671,21 +676,6 @@ struct RowsKernel {
         return b;
     }
 
-    // What the second product will read of its adapter, into the L2 while the first one runs.
-    static __device__ __forceinline__ void prefetch_w2(const RowsArgs &q, int a, int n_lo, int n_hi) {
-        constexpr int WS = WT == kF32 ? 4 : 2;
-        const int r = q.p.r;
-        if (n_hi <= n_lo) return;
-        const char *w = static_cast<const char *>(q.w2) + static_cast<size_t>(a) * r * q.c2 * WS;
-        const size_t row = static_cast<size_t>(BWD ? n_hi - n_lo : (n_hi - n_lo) * r) * WS;  // contiguous bytes
-        const int lines = static_cast<int>((row + 127) / 128), rows = BWD ? r : 1;
-        for (int e = threadIdx.x; e < lines * rows; e += 256) {
-            const int j = e / lines, l = e - j * lines;
-            const size_t off = min(static_cast<size_t>(l) * 128, row - 1);
-            prefetch_l2(w + (BWD ? (static_cast<size_t>(j) * q.c2 + n_lo) : static_cast<size_t>(n_lo) * r) * WS + off);
-        }
-    }
-
     // 8 base values of the activations' type from the lane's queue
     static __device__ __forceinline__ void take_base(const uint4 *from, float (&v)[8]) {
         const uint4 a = from[0];
@@ -769,7 +759,8 @@ template <int XT, int WT, bool BWD, int MT, int RG, int NT, bool GIVEN>
 cudaError_t launch_rows_one(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
     auto kern = lora_rows_kernel<XT, WT, BWD, MT, RG, NT, GIVEN>;
     const int smem = RowsKernel<XT, WT, BWD, MT, RG, NT, GIVEN>::smem_bytes(q.p.r);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(kern, done, RowsKernel<XT, WT, BWD, MT, RG, NT, GIVEN>::smem_bytes(kMaxRank), true);
     if (e != cudaSuccess) return e;
     return launch_cluster(kern, dim3(static_cast<unsigned>(plan.tiles) * q.cs), dim3(256), smem, s, GIVEN ? 1 : q.cs, q);
 }

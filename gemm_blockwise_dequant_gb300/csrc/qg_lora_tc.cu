@@ -466,17 +466,6 @@ bool make_map(CUtensorMap &m, bool bf16, const void *base, int rank, const cuuin
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Raises a kernel's shared-memory limit once per device.
-template <typename K>
-cudaError_t allow_smem(K kern, std::atomic<unsigned long long> &done, int bytes) {
-    const int slot = device_slot();
-    const unsigned long long bit = slot < 0 ? 0 : 1ull << slot;
-    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
-    return e;
-}
-
 int thin_cols(int r) { return (r + 15) / 16 * 16; }
 
 }  // namespace

@@ -17,7 +17,8 @@ cudaError_t launch_one(WgradArgs q, cudaStream_t s) {
     const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * p.na * chunks;
     q.cs = 1;
     while (q.cs < 8 && ctas * q.cs < 2 * device_info().sm_count && p.T / p.na > 2 * kWgChunk * q.cs) q.cs *= 2;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Kern::SMEM);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(kern, done, Kern::SMEM);
     if (e != cudaSuccess) return e;
     return launch_cluster(kern, dim3(static_cast<unsigned>(q.tiles[0] + q.tiles[1]) * q.cs, p.na, chunks), dim3(256), Kern::SMEM, s, q.cs, q);
 }
