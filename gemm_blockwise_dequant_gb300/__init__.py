@@ -123,10 +123,16 @@ def lib():
 
 
 # ---------------------------------------------------------------- marshalling
-def _torch():
-    import torch
+_TORCH = None
 
-    return torch
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+
+        _TORCH = torch
+    return _TORCH
 
 
 _DTYPE_CODES = None
@@ -391,6 +397,8 @@ def qg_gather_block_quantized(indices, W, scales, zero_points, Y, *, w_format, b
 
 
 # ---------------------------------------------------------------- adapters and fine-tuning
+# These calls take tens of arguments and a few microseconds on the device, so their marshalling is kept short: plain
+# integers for addresses (ctypes converts them) and no call of PyTorch's that is not needed.
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -398,32 +406,30 @@ def _addr(t):
 def _stream_and_workspace(need, workspace, t, stream):
     """(raw stream, workspace address, its bytes, the workspace): on `stream`, or on the device's current one.
     A workspace made here is not given away again before the work on `stream` that uses it is done."""
-    torch = _torch()
+    raw = _torch()._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
     if workspace is not None:
-        nbytes = workspace.numel() * workspace.element_size()
-    elif need:
-        workspace, nbytes = torch.empty(need, dtype=torch.uint8, device=t.device), need
-        if stream is not None:
-            workspace.record_stream(stream)
-    else:
-        nbytes = 0
-    raw = torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
-    return raw, _addr(workspace), nbytes, workspace
+        return raw, workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if not need:
+        return raw, None, 0, None
+    workspace = _torch().empty(need, dtype=_torch().uint8, device=t.device)
+    if stream is not None:
+        workspace.record_stream(stream)
+    return raw, workspace.data_ptr(), need, workspace
 
 
-def _rows2d(t, cols, what):
+def _rows2d(t, rows, cols, what):
     """The distance between the rows of a 2-D tensor whose rows are contiguous (the C calls take no other)."""
-    if t.dim() != 2 or t.shape[1] != cols or (t.stride(1) != 1 and cols > 1):
-        raise ValueError("%s: a 2-D tensor with rows of %d contiguous values is wanted" % (what, cols))
-    ld = t.stride(0)
-    return ld if ld >= cols or t.shape[0] > 1 else cols  # the stride of a single row says nothing
+    ld, step = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != (rows, cols) or (step != 1 and cols > 1):
+        raise ValueError("%s: a tensor of %d rows of %d contiguous values is wanted" % (what, rows, cols))
+    return ld if rows > 1 or ld >= cols else cols  # the stride of a single row says nothing
 
 
 def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter):
     torch = _torch()
     na, r, K = A.shape
     N = B.shape[1]
-    if B.shape[0] != na or B.shape[2] != r or A.dtype != B.dtype or not A.is_contiguous() or not B.is_contiguous():
+    if B.shape != (na, N, r) or A.dtype != B.dtype or not A.is_contiguous() or not B.is_contiguous():
         raise ValueError("A [adapters, rank, K] and B [adapters, N, rank] of one type, contiguous, are wanted")
     if scaling is not None and (scaling.dtype != torch.float32 or scaling.shape != (na,) or not scaling.is_contiguous()):
         raise ValueError("scaling: [adapters] float32 is wanted")
@@ -450,16 +456,16 @@ def qg_lora_apply(X, seg_offsets, seg_adapter, A, B, scaling, Y_in, Y, *, V=None
     """
     na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter)
     T = X.shape[0]
-    if Y.shape[0] != T or (Y_in is not None and Y_in.shape[0] != T):
-        raise ValueError("X, Y_in and Y: one number of rows is wanted")
+    ldx, ldy = _rows2d(X, T, K, "X"), _rows2d(Y, T, N, "Y")
+    yin = (None, 0, 0) if Y_in is None else (Y_in.data_ptr(), _dtype_code(Y_in), _rows2d(Y_in, T, N, "Y_in"))
     if V is not None and (V.shape != (T, r) or V.dtype != _torch().float32 or not V.is_contiguous()):
         raise ValueError("V: [rows, rank] float32 is wanted")
     L = lib()
-    st, wp, wb, _ = _stream_and_workspace(L.qg_lora_apply_workspace_bytes(T, S, r), workspace, X, stream)
-    s = L.qg_lora_apply(_addr(X), _dtype_code(X), _rows2d(X, K, "X"), _addr(seg_offsets), _addr(seg_adapter), S,
-                        _addr(A), _addr(B), _dtype_code(A), _addr(scaling), na, r, _addr(Y_in),
-                        0 if Y_in is None else _dtype_code(Y_in), 0 if Y_in is None else _rows2d(Y_in, N, "Y_in"),
-                        _addr(Y), _dtype_code(Y), _rows2d(Y, N, "Y"), _addr(V), T, N, K, _addr(status), wp, wb, st)
+    need = L.qg_lora_apply_workspace_bytes(T, S, r) if workspace is None else 0
+    st, wp, wb, _ = _stream_and_workspace(need, workspace, X, stream)
+    s = L.qg_lora_apply(X.data_ptr(), _dtype_code(X), ldx, seg_offsets.data_ptr(), seg_adapter.data_ptr(), S, A.data_ptr(),
+                        B.data_ptr(), _dtype_code(A), _addr(scaling), na, r, yin[0], yin[1], yin[2], Y.data_ptr(),
+                        _dtype_code(Y), ldy, _addr(V), T, N, K, _addr(status), wp, wb, st)
     return s if raw else _check(s, "qg_lora_apply")
 
 
@@ -477,21 +483,22 @@ def qg_lora_grad(dY, X, V, seg_offsets, seg_adapter, A, B, scaling, dX_in, dX, d
     """
     na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter)
     T = X.shape[0]
-    if dY.shape[0] != T or dY.dtype != X.dtype or V.shape != (T, r) or V.dtype != _torch().float32 or not V.is_contiguous():
-        raise ValueError("dY and X of one type and number of rows and V [rows, rank] float32 are wanted")
+    xt = X.dtype
+    if dY.dtype != xt or V.shape != (T, r) or V.dtype != _torch().float32 or not V.is_contiguous():
+        raise ValueError("dY of X's type and V [rows, rank] float32 are wanted")
     if dA.shape != A.shape or dB.shape != B.shape or dA.dtype != dB.dtype or not dA.is_contiguous() or not dB.is_contiguous():
         raise ValueError("dA and dB: the shapes of A and B, contiguous and of one type, are wanted")
-    lddx = 0
+    lddy, ldx, lddx = _rows2d(dY, T, N, "dY"), _rows2d(X, T, K, "X"), 0
     if dX is not None:
-        lddx = _rows2d(dX, K, "dX")
-        for t in (dX, dX if dX_in is None else dX_in):
-            if t.shape[0] != T or t.dtype != X.dtype or _rows2d(t, K, "dX_in") != lddx:
-                raise ValueError("dX_in and dX: X's type and rows, and one distance between rows, are wanted")
+        lddx = _rows2d(dX, T, K, "dX")
+        if dX.dtype != xt or (dX_in is not None and (dX_in.dtype != xt or _rows2d(dX_in, T, K, "dX_in") != lddx)):
+            raise ValueError("dX_in and dX: X's type, and one distance between rows, are wanted")
     L = lib()
-    st, wp, wb, _ = _stream_and_workspace(L.qg_lora_grad_workspace_bytes(T, S, na, r, N, K), workspace, X, stream)
-    s = L.qg_lora_grad(_addr(dY), _dtype_code(X), _rows2d(dY, N, "dY"), _addr(X), _rows2d(X, K, "X"), _addr(V),
-                       _addr(seg_offsets), _addr(seg_adapter), S, _addr(A), _addr(B), _dtype_code(A), _addr(scaling), na, r,
-                       _addr(dX_in), _addr(dX), lddx, _addr(dA), _addr(dB), _dtype_code(dA), 1 if accumulate else 0,
+    need = L.qg_lora_grad_workspace_bytes(T, S, na, r, N, K) if workspace is None else 0
+    st, wp, wb, _ = _stream_and_workspace(need, workspace, X, stream)
+    s = L.qg_lora_grad(dY.data_ptr(), _dtype_code(X), lddy, X.data_ptr(), ldx, V.data_ptr(), seg_offsets.data_ptr(),
+                       seg_adapter.data_ptr(), S, A.data_ptr(), B.data_ptr(), _dtype_code(A), _addr(scaling), na, r,
+                       _addr(dX_in), _addr(dX), lddx, dA.data_ptr(), dB.data_ptr(), _dtype_code(dA), 1 if accumulate else 0,
                        T, N, K, _addr(status), wp, wb, st)
     return s if raw else _check(s, "qg_lora_grad")
 
@@ -513,7 +520,8 @@ def qgemm_nbits_dgrad(dY, W, scales, zero_points, dX, *, bits, block_size, works
     """dX[M,K] = dY[M,N] . dequant(W)[N,K]: the gradient of the activations through the frozen weight of qgemm_nbits."""
     M, N, K = _dgrad_sizes(dY, W, scales, dX, bits, block_size)
     L = lib()
-    st, wp, wb, _ = _stream_and_workspace(L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits), workspace, dY, stream)
+    need = L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits) if workspace is None else 0
+    st, wp, wb, _ = _stream_and_workspace(need, workspace, dY, stream)
     s = L.qgemm_nbits_dgrad(_addr(dY), _dtype_code(dY), _addr(W), _addr(scales), _addr(zero_points), _addr(dX),
                             _dtype_code(dX), M, N, K, bits, block_size, wp, wb, st)
     return s if raw else _check(s, "qgemm_nbits_dgrad")
@@ -523,7 +531,8 @@ def qgemm_nbits_uniform_zp_dgrad(dY, W, scales, uniform_zp, dX, *, bits, block_s
     """As qgemm_nbits_dgrad with every zero point equal to the scalar uniform_zp."""
     M, N, K = _dgrad_sizes(dY, W, scales, dX, bits, block_size)
     L = lib()
-    st, wp, wb, _ = _stream_and_workspace(L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits), workspace, dY, stream)
+    need = L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits) if workspace is None else 0
+    st, wp, wb, _ = _stream_and_workspace(need, workspace, dY, stream)
     s = L.qgemm_nbits_uniform_zp_dgrad(_addr(dY), _dtype_code(dY), _addr(W), _addr(scales), float(uniform_zp), _addr(dX),
                                        _dtype_code(dX), M, N, K, bits, block_size, wp, wb, st)
     return s if raw else _check(s, "qgemm_nbits_uniform_zp_dgrad")
@@ -533,7 +542,8 @@ def qgemm_codebook4_dgrad(dY, W, codebook, absmax, dX, *, block_size, workspace=
     """dX = dY . (codebook[q] * absmax): the gradient of the activations through the frozen weight of qgemm_codebook4."""
     M, N, K = _dgrad_sizes(dY, W, absmax, dX, 4, block_size)
     L = lib()
-    st, wp, wb, _ = _stream_and_workspace(L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, 4), workspace, dY, stream)
+    need = L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, 4) if workspace is None else 0
+    st, wp, wb, _ = _stream_and_workspace(need, workspace, dY, stream)
     s = L.qgemm_codebook4_dgrad(_addr(dY), _dtype_code(dY), _addr(W), _addr(codebook), _addr(absmax), _addr(dX),
                                 _dtype_code(dX), M, N, K, block_size, wp, wb, st)
     return s if raw else _check(s, "qgemm_codebook4_dgrad")
