@@ -25,8 +25,10 @@
 //    product of the second terms, 2^-22, is left out).  A row of dY is first
 //    scaled by a power of two, and all weights by one that their largest
 //    parameters give, so that neither term leaves fp16's range.
-//  * Tiles that do not fill a wave are split along n; their fp32 pieces are
-//    added in a fixed order by a second kernel.
+//  * Tiles that do not fill a wave are split along n and their fp32 pieces added
+//    in a fixed order: with up to 128 rows by the cluster of CTAs that made them,
+//    through distributed shared memory (one launch, no workspace); with more, by
+//    a second kernel.
 #include <algorithm>
 #include <atomic>
 
@@ -150,6 +152,27 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
                 return false;
             }
         }
+    }
+}
+
+// Four floats of CTA `rank`'s shared memory, at the place of `p` in this CTA's.
+__device__ __forceinline__ float4 peer_float4(const float *p, int rank) {
+    float4 v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(smem_u32(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// Four outputs, `at` a multiple of four.
+__device__ __forceinline__ void store4(void *dX, int x_dtype, size_t at, const float4 &s) {
+    if (x_dtype == 0) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(dX) + at) = s;
+    } else {
+        const uint16_t a = x_dtype == 1 ? f2h(s.x) : f2bf(s.x), b = x_dtype == 1 ? f2h(s.y) : f2bf(s.y);
+        const uint16_t c = x_dtype == 1 ? f2h(s.z) : f2bf(s.z), d = x_dtype == 1 ? f2h(s.w) : f2bf(s.w);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dX) + at) = make_uint2(a | static_cast<uint32_t>(b) << 16, c | static_cast<uint32_t>(d) << 16);
     }
 }
 
@@ -318,8 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
-    int tile = blockIdx.x / PAIR, s0 = 0, ns = p.steps, piece = -1;
-    if (tile >= p.full_tiles) {
+    int tile = blockIdx.x / PAIR, s0 = 0, ns = p.steps, piece = -1, part = 0;
+    if (PAIR == 1) {  // the CTAs of a cluster share a tile
+        part = tile % p.splits;
+        tile /= p.splits;
+        s0 = part * p.split_steps;
+        ns = max(0, min(p.steps, s0 + p.split_steps) - s0);
+    } else if (tile >= p.full_tiles) {
         const int q = tile - p.full_tiles;
         tile = p.full_tiles + q / p.splits;
         s0 = (q % p.splits) * p.split_steps;
@@ -352,7 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // A split tile's sums, [row][column] over the dY ring, which is read by then.
+    constexpr int SS = kCols + 4;
+    float *sums = reinterpret_cast<float *>(a_s);
+    const bool shared_tile = PAIR == 1 && p.splits > 1;
+    static_assert(NA * AT + NW * WT >= kRows * SS * 4, "the sums fit");
 
+    bool ok = true;
     if (warp == 0) {
         if (lane == 0)
             for (int i = 0; i < ns; ++i) {
@@ -368,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_f16(PAIR * kRows, BN, BF16) | (1u << 16);  // B MN-major
             const bool two = H == 2 && m0 + PAIR * kRows < p.M;  // the second half holds rows
-            bool ok = true;
             for (int i = 0; i < ns && ok; ++i) {
                 const int s = i % NA, b = i % NW;
                 ok = mbar_wait(&full[s], (i / NA) & 1, abort_flag, p.fault, FAULT_WAIT_TC) &&
@@ -513,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
             if (lane == 0) mbar_arrive(&wfull[b]);
         }
         // ---------------------------------------------------------------- epilogue
-        const bool ok = mbar_wait(accf, 0, abort_flag, p.fault, FAULT_WAIT_TC);
+        ok = mbar_wait(accf, 0, abort_flag, p.fault, FAULT_WAIT_TC);
         tc_fence_after();
         const int sub = warp & 3, cq = (warp - 2) >> 2;  // tensor-memory sub-partition; share of the columns
         constexpr int CW = H * BN / (kDequantWarps / 4);
@@ -524,13 +557,24 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
             tmem_ld32(lane_addr + cc, v);
             const int h = cc / BN, c0 = cc - h * BN;
             const int row = h * PAIR * kRows + rank * kRows + sub * 32 + lane, m = m0 + row, kc = k0 + c0;
-            if (!ok || ns == 0 || m >= p.M || kc >= p.K) continue;  // K is a multiple of 32: a column group is in or out
+            if (m >= p.M || kc >= p.K) continue;  // K is a multiple of 32: a column group is in or out
+            if (!ok || ns == 0) {
+                if (!shared_tile) continue;
+#pragma unroll
+                for (int q = 0; q < 32; ++q) v[q] = 0;
+            }
             if constexpr (TERMS == 2) {
                 const float rs = p.row_scale[m];
 #pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * rs / wscale);
             }
-            if (piece >= 0) {
+            if (shared_tile) {
+                float4 *dst = reinterpret_cast<float4 *>(sums + row * SS + c0);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
+                                         __uint_as_float(v[4 * q + 3]));
+            } else if (piece >= 0) {
                 float4 *dst = reinterpret_cast<float4 *>(p.partial + (static_cast<size_t>(piece) * (H * PAIR * kRows) + row) * BN + c0);
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -565,6 +609,22 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
     if (warp == 1) {
         tc_fence_after();
         free_tmem<PAIR>(tmem, TMEM_COLS);
+        __syncwarp();
+    }
+    if (shared_tile) {
+        cluster_sync();  // every CTA's sums are written
+        const int rows = min(kRows, p.M - m0), cols = min(kCols, p.K - k0) / 4;
+        const int lo = rows * part / p.splits, hi = rows * (part + 1) / p.splits;
+        for (int e = threadIdx.x; e < (hi - lo) * cols; e += kThreads) {
+            const int row = lo + e / cols, c = (e % cols) * 4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int z = 0; z < p.splits; ++z) {
+                const float4 v = peer_float4(sums + row * SS + c, z);
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            store4(p.dX, p.x_dtype, static_cast<size_t>(m0 + row) * p.K + k0 + c, s);
+        }
+        cluster_sync();  // and read
     }
 }
 
@@ -585,15 +645,7 @@ __global__ void __launch_bounds__(256) dgrad_reduce_kernel(const float *__restri
             const float4 v = *reinterpret_cast<const float4 *>(partial + ((static_cast<size_t>(q) * splits + z) * rows + row) * bn + c);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
-        const size_t at = static_cast<size_t>(m) * K + k;
-        if (x_dtype == 0) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(dX) + at) = s;
-        } else {
-            const uint16_t a = x_dtype == 1 ? f2h(s.x) : f2bf(s.x), b = x_dtype == 1 ? f2h(s.y) : f2bf(s.y);
-            const uint16_t cc = x_dtype == 1 ? f2h(s.z) : f2bf(s.z), d = x_dtype == 1 ? f2h(s.w) : f2bf(s.w);
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dX) + at) =
-                make_uint2(a | static_cast<uint32_t>(b) << 16, cc | static_cast<uint32_t>(d) << 16);
-        }
+        store4(dX, x_dtype, static_cast<size_t>(m) * K + k, s);
     }
 }
 
@@ -662,8 +714,9 @@ struct Plan {
 
 // Rows decide the tile: up to 128 rows one CTA a tile (128 x 128), up to 256 a
 // pair (256 x 256), above that two halves a pair (512 x 256; fp32 dY needs the
-// second half's room for its second term).  Whole tiles fill complete waves, the
-// others are split along n over the SMs, at least four steps a piece.
+// second half's room for its second term).  Of the pairs' tiles whole ones fill
+// complete waves and the others are split along n over the SMs, at least four
+// steps a piece.
 Plan make_plan(int dy_dtype, int M, int N, int K) {
     Plan c{};
     c.terms = dy_dtype == 0 ? 2 : 1;
@@ -680,12 +733,17 @@ Plan make_plan(int dy_dtype, int M, int N, int K) {
     c.tail_tiles = static_cast<int>(tiles - c.full_tiles);
     c.splits = 1;
     c.split_steps = c.steps;
-    if (c.tail_tiles) {
+    if (c.pair == 1) {  // every tile is shared by a cluster of as many CTAs as leave each two steps and all of them resident
+        c.full_tiles = 0;
+        c.tail_tiles = static_cast<int>(tiles);
+        while (c.splits < 16 && tiles * c.splits * 2 <= units && c.steps >= 4 * c.splits) c.splits *= 2;
+        c.split_steps = (c.steps + c.splits - 1) / c.splits;
+    } else if (c.tail_tiles) {
         const int sp = std::max(1, std::min(units / c.tail_tiles, c.steps / 4));
         c.split_steps = (c.steps + sp - 1) / sp;
         c.splits = (c.steps + c.split_steps - 1) / c.split_steps;
     }
-    if (c.splits > 1) c.partial_bytes = sizeof(float) * c.tail_tiles * c.splits * static_cast<size_t>(c.rows) * c.bn;
+    if (c.pair == 2 && c.splits > 1) c.partial_bytes = sizeof(float) * c.tail_tiles * c.splits * static_cast<size_t>(c.rows) * c.bn;
     c.ld = (N + 7) / 8 * 8;
     if (c.ld != N || c.terms == 2) c.copy_bytes = (static_cast<size_t>(M) * c.ld * 2 + 255) / 256 * 256;
     c.front_bytes = c.terms * c.copy_bytes;
@@ -705,9 +763,13 @@ cudaError_t launch(const CUtensorMap *maps, const DgradArgs &a, int tiles, cudaS
     if (!(configured.load(std::memory_order_acquire) & bit)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(H, TERMS));
         if (e != cudaSuccess) return e;
+        if (PAIR == 1) {
+            const cudaError_t e16 = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e16 != cudaSuccess) return e16;
+        }
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_cluster(kern, dim3(tiles * PAIR), dim3(kThreads), smem_bytes(H, TERMS), s, PAIR, maps[0], maps[1], a);
+    return launch_cluster(kern, dim3(tiles * PAIR), dim3(kThreads), smem_bytes(H, TERMS), s, PAIR == 1 ? a.splits : PAIR, maps[0], maps[1], a);
 }
 
 template <int WK, int BITS, bool BF16>
@@ -791,7 +853,7 @@ cudaError_t dgrad(const GemmProblem &p, void *ws, cudaStream_t s) {
     a.fault = fault_word();
     e = p.a_dtype == 2 ? launch_kind<true>(p, c, maps, a, s) : launch_kind<false>(p, c, maps, a, s);
     if (e != cudaSuccess) return e;
-    if (c.splits > 1) {
+    if (c.pair == 2 && c.splits > 1) {
         const int64_t work = static_cast<int64_t>(c.tail_tiles) * c.rows * (c.bn / 4);
         e = launch_pdl(dgrad_reduce_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, device_info().sm_count * 16))),
                        dim3(256), 0, s, static_cast<const float *>(a.partial), c.tail_tiles, c.splits, c.rows, c.bn, c.full_tiles, c.mt, p.M, p.K,
