@@ -84,7 +84,7 @@ _SIGS = {
     "qmoe_ragged_mm_workspace_bytes": ([_I, _P, _I, _I, _I, _I, _I], _SZ),
     "qmoe_ragged_mm_device_offsets": ([_P, _I, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _SZ, _P, _P], _I),
     "qmoe_ragged_mm_device_offsets_workspace_bytes": ([_I], _SZ),
-    "qg_lora_apply_workspace_bytes": ([_I, _I, _I], _SZ),
+    "qg_lora_apply_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "qg_lora_apply": ([_P, _I, _L, _P, _P, _I, _P, _P, _I, _P, _I, _I, _P, _I, _L, _P, _I, _L, _P, _I, _I, _I, _P, _P,
                        _SZ, _P], _I),
     "qg_lora_grad_workspace_bytes": ([_I, _I, _I, _I, _I, _I], _SZ),
@@ -440,8 +440,8 @@ def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter):
     return na, r, K, N, S
 
 
-def qg_lora_apply_workspace_bytes(rows: int, num_segments: int, rank: int) -> int:
-    return lib().qg_lora_apply_workspace_bytes(rows, num_segments, rank)
+def qg_lora_apply_workspace_bytes(rows: int, num_segments: int, rank: int, N: int, K: int) -> int:
+    return lib().qg_lora_apply_workspace_bytes(rows, num_segments, rank, N, K)
 
 
 def qg_lora_apply(X, seg_offsets, seg_adapter, A, B, scaling, Y_in, Y, *, V=None, status=None, workspace=None,
@@ -461,7 +461,7 @@ def qg_lora_apply(X, seg_offsets, seg_adapter, A, B, scaling, Y_in, Y, *, V=None
     if V is not None and (V.shape != (T, r) or V.dtype != _torch().float32 or not V.is_contiguous()):
         raise ValueError("V: [rows, rank] float32 is wanted")
     L = lib()
-    need = L.qg_lora_apply_workspace_bytes(T, S, r) if workspace is None else 0
+    need = L.qg_lora_apply_workspace_bytes(T, S, r, N, K) if workspace is None else 0
     st, wp, wb, _ = _stream_and_workspace(need, workspace, X, stream)
     s = L.qg_lora_apply(X.data_ptr(), _dtype_code(X), ldx, seg_offsets.data_ptr(), seg_adapter.data_ptr(), S, A.data_ptr(),
                         B.data_ptr(), _dtype_code(A), _addr(scaling), na, r, yin[0], yin[1], yin[2], Y.data_ptr(),

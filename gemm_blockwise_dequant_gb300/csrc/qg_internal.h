@@ -204,7 +204,7 @@ struct LoraGrad {
     void *dA, *dB;
     int g_dtype, accumulate;
 };
-size_t lora_apply_workspace_bytes(int T, int S, int r);
+size_t lora_apply_workspace_bytes(int T, int S, int r, int N, int K);
 cudaError_t lora_apply(const LoraApply &q, void *ws, cudaStream_t s);
 size_t lora_grad_workspace_bytes(int T, int S, int na, int r, int N, int K);
 cudaError_t lora_grad(const LoraGrad &q, void *ws, cudaStream_t s);

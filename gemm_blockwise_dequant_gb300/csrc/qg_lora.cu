@@ -17,7 +17,19 @@ cudaError_t launch_wgrad(const WgradArgs &q, int x_dtype, cudaStream_t s);
 
 namespace {
 
-constexpr int kTcRows = 512;  // rows from which on the tensor-core kernels take over
+// Rows of 16-bit activations from which on the tensor cores (tcgen05) make dA and
+// dB faster: 24.6 against 26.1 us at 128 x (4096, 1024), rank 16, 38 against 59 at
+// rank 64.
+constexpr int kTcGradRows = 128;
+
+// The products over rows in two launches, the first one on the tensor cores,
+// instead of one: 38.0 against 40.5 us at 2048 x (4096 -> 14336), rank 16, 35.7
+// against 36.9 at 4096 x (5120 -> 5120), 32.7 against 36.8 at half the rows and rank
+// 64; but 23.8 against 22.1 there at rank 16, and 20.2 against 18.1 at 4096 x (4096
+// -> 1024).
+bool two_launches(int T, int N, int K, int r) {
+    return T >= 1024 && static_cast<double>(T) * (static_cast<double>(N) + K) * (r + 16) >= 1.2e9;
+}
 
 size_t esize(int d) { return d == kF32 ? 4 : 2; }
 
@@ -25,38 +37,34 @@ bool rows16(const void *p, int64_t ld, int dtype) {  // rows at 16-byte boundari
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * static_cast<int64_t>(esize(dtype))) % 16 == 0;
 }
 
-// Tiles of 64 rows once requests have that many on average and there are tiles
-// for every SM, else of 16.  The cluster is as wide as leaves all CTAs resident
-// at once, two an SM, while each has at least 256 values of a row to contract:
-// 64 requests of one row at 4096 -> 14336, rank 16, take 37.2 / 23.8 / 15.9 /
-// 20.6 us with 1 / 2 / 4 / 8 CTAs a tile, one row 36 / 21.6 / 13.9 / 9.9.
+// The cluster of a tile is as wide as leaves all CTAs resident at once, two an SM,
+// while each has at least 256 values of a row to contract: 64 requests of one row
+// at 4096 -> 14336, rank 16, take 37.2 / 23.8 / 15.9 / 20.6 us with 1 / 2 / 4 / 8
+// CTAs a tile, one row 36 / 21.6 / 13.9 / 9.9 / 8.2 (16).  Clusters of 16 are few
+// at a time (256 rows: 15.2 us with them, 9.3 with 8).
 RowsPlan make_plan(int T, int S, int c1) {
     RowsPlan plan{};
     const int sms = device_info().sm_count;
-    plan.rows = T / 64 >= S && T / 64 >= sms / 2 ? 64 : 16;
-    plan.tiles = (T + plan.rows - 1) / plan.rows + S;  // the most that any offsets can need
-    const int real = std::max(T / plan.rows, std::min(S, T));
+    plan.tiles = (T + kRowsTile - 1) / kRowsTile + S;  // the most that any offsets can need
+    const int real = std::max(T / kRowsTile, std::min(S, T));
     plan.cs = 1;
-    while (plan.cs < 16 && real * plan.cs * 2 <= 2 * sms && c1 >= 512 * plan.cs) plan.cs *= 2;
+    while (plan.cs < 16 && real * plan.cs * 2 <= (plan.cs < 8 ? 2 * sms : sms) && c1 >= 512 * plan.cs) plan.cs *= 2;
     return plan;
 }
 
 // The second product alone: 64-row tiles, whose columns as many CTAs share as
-// keep two on every SM (a CTA's start, with its sums' fragments, costs about
-// as much as 8 of its 32-column groups).
+// keep two on every SM.
 RowsPlan expand_plan(int T, int S, int c2) {
     RowsPlan plan{};
-    plan.rows = 64;
     plan.tiles = (T + 63) / 64 + S;
     plan.cs = 1;
     while (plan.cs < 64 && (T / 64) * plan.cs * 2 <= 2 * device_info().sm_count && c2 >= 512 * plan.cs) plan.cs *= 2;
     return plan;
 }
 
-// Many rows of 16-bit activations: the first product, and the adapters'
-// gradients, on the tensor cores.
-bool many_rows(const LoraProblem &p, int x_dtype, bool aligned) {
-    return x_dtype != kF32 && aligned && p.T >= kTcRows && p.T / kTcRows >= p.S / 4 && lora_tc_available();
+// 16-bit activations at 16-byte boundaries, not cut into small requests.
+bool tensor_cores(const LoraProblem &p, int x_dtype, bool aligned) {
+    return x_dtype != kF32 && aligned && p.T / 128 >= p.S && lora_tc_available();
 }
 
 // CTAs that share a tile's contraction: enough for two an SM, of eight steps or more.
@@ -82,7 +90,7 @@ cudaError_t rows(const RowsArgs &args, int x_dtype, bool bwd, cudaStream_t s) {
 }  // namespace
 
 // V between the two products of many rows
-size_t lora_apply_workspace_bytes(int T, int, int r) { return T >= kTcRows ? static_cast<size_t>(T) * r * 4 : 0; }
+size_t lora_apply_workspace_bytes(int T, int, int r, int N, int K) { return two_launches(T, N, K, r) ? static_cast<size_t>(T) * r * 4 : 0; }
 
 cudaError_t lora_apply(const LoraApply &a, void *ws, cudaStream_t s) {
     RowsArgs q{};
@@ -102,7 +110,7 @@ cudaError_t lora_apply(const LoraApply &a, void *ws, cudaStream_t s) {
     q.sums = a.V;
     q.in_vec = rows16(a.X, a.ldx, a.x_dtype);
     q.out_vec = rows16(a.Y, a.ldy, a.y_dtype) && (!a.Yin || rows16(a.Yin, a.ldyin, a.yin_dtype));
-    if (many_rows(a.p, a.x_dtype, q.in_vec)) {
+    if (two_launches(a.p.T, a.p.N, a.p.K, a.p.r) && tensor_cores(a.p, a.x_dtype, q.in_vec)) {
         ShrinkTc t{};
         t.p = a.p;
         t.sums = a.V ? a.V : static_cast<float *>(ws);
@@ -117,12 +125,14 @@ cudaError_t lora_apply(const LoraApply &a, void *ws, cudaStream_t s) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// G, the rows' gradients inside the adapter, and for many rows the largest
-// values and the adapters of the tiles that made them, and the 16-bit terms of
-// G and V
+// CTAs, or tiles, that write down their rows' largest values: of shrink (clusters of up to 8) or of the row kernel.
+static int grad_parts(int T, int S) { return std::max(shrink_tc_tiles(T, S) * 8, (T + kRowsTile - 1) / kRowsTile + S); }
+
+// G, the rows' gradients inside the adapter; for the tensor cores also the largest
+// values and the adapters of the tiles, and the 16-bit terms of G and V
 size_t lora_grad_workspace_bytes(int T, int S, int, int r, int, int) {
     const size_t sums = align256(static_cast<size_t>(T) * r * 4);
-    return T < kTcRows ? sums : sums + align256(static_cast<size_t>(shrink_tc_tiles(T, S)) * 8 * 12) + wgrad_tc_terms_bytes(T, r);
+    return T < kTcGradRows ? sums : sums + align256(static_cast<size_t>(grad_parts(T, S)) * 12) + wgrad_tc_terms_bytes(T, r);
 }
 
 cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
@@ -143,23 +153,36 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
     q.sums = static_cast<float *>(ws);
     q.in_vec = rows16(a.dY, a.lddy, a.x_dtype);
     q.out_vec = 1;
-    const bool tc = many_rows(a.p, a.x_dtype, q.in_vec);
-    ShrinkTc t{};
-    cudaError_t e = cudaSuccess;
+    const bool tc = a.p.T >= kTcGradRows && tensor_cores(a.p, a.x_dtype, q.in_vec),
+               two = tc && two_launches(a.p.T, a.p.N, a.p.K, a.p.r);
+    int parts = 0;
+    int *tile_adapter = nullptr;
+    float *tile_max = nullptr, *G = q.sums;
     if (tc) {
+        const int cs = two ? shrink_splits(a.p.T, a.p.S, a.p.N) : 1;
+        parts = two ? shrink_tc_tiles(a.p.T, a.p.S) * cs : (a.p.T + kRowsTile - 1) / kRowsTile + a.p.S;
+        tile_adapter = reinterpret_cast<int *>(static_cast<char *>(ws) + align256(static_cast<size_t>(a.p.T) * a.p.r * 4));
+        tile_max = reinterpret_cast<float *>(tile_adapter + parts);
+        q.tile_adapter = tile_adapter;
+        q.tile_max = tile_max;
+        q.V = a.V;
+    }
+    cudaError_t e = cudaSuccess;
+    if (two) {
+        ShrinkTc t{};
         t.p = a.p;
-        t.sums = q.sums;
+        t.sums = G;
         t.V = a.V;
         t.bwd = 1;
         t.bf16 = a.x_dtype == kBF16;
         t.cs = shrink_splits(a.p.T, a.p.S, a.p.N);
-        t.tile_adapter = reinterpret_cast<int *>(static_cast<char *>(ws) + align256(static_cast<size_t>(a.p.T) * a.p.r * 4));
-        t.tile_max = reinterpret_cast<float *>(t.tile_adapter + shrink_tc_tiles(a.p.T, a.p.S) * t.cs);
+        t.tile_adapter = tile_adapter;
+        t.tile_max = tile_max;
         e = launch_shrink_tc(t, a.dY, a.lddy, a.p.B, s);
-        q.given = q.sums;
+        q.given = G;
         q.sums = nullptr;
     }
-    if (e == cudaSuccess && (!tc || a.dX)) e = rows(q, a.x_dtype, true, s);
+    if (e == cudaSuccess && (!two || a.dX)) e = rows(q, a.x_dtype, true, s);
     if (e != cudaSuccess) return e;
     if (a.p.na == 0) return cudaGetLastError();
     if (tc) {
@@ -169,11 +192,11 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
         w.out[1] = a.dB;
         w.g_dtype = a.g_dtype;
         w.accumulate = a.accumulate;
-        w.tile_max = t.tile_max;
-        w.tile_adapter = t.tile_adapter;
-        w.parts = shrink_tc_tiles(a.p.T, a.p.S) * t.cs;
-        uint16_t *terms = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(t.tile_adapter) + align256(static_cast<size_t>(shrink_tc_tiles(a.p.T, a.p.S)) * 8 * 12));
-        e = launch_wgrad_tc(w, t.sums, a.V, terms, a.X, a.ldx, a.dY, a.lddy, t.bf16, s);
+        w.tile_max = tile_max;
+        w.tile_adapter = tile_adapter;
+        w.parts = parts;
+        uint16_t *terms = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(tile_adapter) + align256(static_cast<size_t>(grad_parts(a.p.T, a.p.S)) * 12));
+        e = launch_wgrad_tc(w, G, a.V, terms, a.X, a.ldx, a.dY, a.lddy, a.x_dtype == kBF16, s);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     WgradArgs w{};

@@ -164,4 +164,14 @@ __device__ __forceinline__ float peer_float(const float *p, int rank) {
     return v;
 }
 
+// Four of them.
+__device__ __forceinline__ float4 peer_float4(const float *p, int rank) {
+    float4 v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(smem_u32(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 }  // namespace qg

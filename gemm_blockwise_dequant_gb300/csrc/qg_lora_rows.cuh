@@ -35,6 +35,9 @@ struct RowsArgs {
     int out_dtype;
     int64_t ld_out;
     float *sums;         // V_out / G or null, [T][rank]
+    float *tile_max;     // backward: [2][tiles] largest |G| and |V| of a tile's rows, and its adapter; or null
+    int *tile_adapter;
+    const float *V;
     const float *given;  // the first product's sums where they are known, or null
     int cs;              // CTAs that share a tile: a cluster, unless the sums are given
     int in_vec, out_vec; // rows at 16-byte boundaries: vector accesses
@@ -264,7 +267,10 @@ struct RowsKernel {
         pdl_launch_dependents();
         pdl_wait();
         RowTile t;
-        if (!find_tile(p, tile, R, blockIdx.x == 0, t) || t.rows == 0) return;  // the same for the whole cluster
+        const bool fine = find_tile(p, tile, R, blockIdx.x == 0, t);
+        if (!fine || t.rows == 0 || t.adapter < 0)
+            if (BWD && !GIVEN && q.tile_adapter && rank == 0 && tid == 0) q.tile_adapter[tile] = -1;
+        if (!fine || t.rows == 0) return;  // the same for the whole cluster
         const float scale = t.adapter >= 0 && p.scaling ? __ldg(p.scaling + t.adapter) : 1.f;
 
         const int ngrp = (q.c2 + 31) / 32;  // 32-column groups of the second product, and this CTA's
@@ -380,6 +386,8 @@ struct RowsKernel {
                 } else {
                     __syncthreads();
                 }
+                const bool maxima = BWD && q.tile_adapter && rank == 0;
+                float mx = 0.f, mv = 0.f;
                 for (int e = tid; e < R * rp; e += 256) {
                     const int row = e / rp, j = e - row * rp;
                     float s = 0.f;
@@ -392,6 +400,23 @@ struct RowsKernel {
                         if (q.sums && rank == 0 && row < t.rows) q.sums[static_cast<size_t>(t.t0 + row) * r + j] = s;
                     }
                     whole[e] = s;
+                    if (maxima) {
+                        mx = fmaxf(mx, fabsf(s));
+                        if (j < r && row < t.rows) mv = fmaxf(mv, fabsf(__ldg(q.V + static_cast<size_t>(t.t0 + row) * r + j)));
+                    }
+                }
+                if (maxima) {  // at the place of the partial sums, which have been read
+                    unsigned *top = reinterpret_cast<unsigned *>(part);
+                    if (tid < 2) top[tid] = 0;
+                    __syncthreads();
+                    atomicMax(top, __float_as_uint(mx));  // of values that are not negative: the order does not matter
+                    atomicMax(top + 1, __float_as_uint(mv));
+                    __syncthreads();
+                    if (tid == 0) {
+                        q.tile_adapter[tile] = t.adapter;
+                        q.tile_max[tile] = __uint_as_float(top[0]);
+                        q.tile_max[gridDim.x / q.cs + tile] = __uint_as_float(top[1]);
+                    }
                 }
                 __syncthreads();
                 if (q.cs > 1) cluster_arrive();  // done with the peers' memory; awaited before leaving
@@ -745,9 +770,13 @@ struct RowsKernel {
     }
 };
 
-// Tiles of 16 rows (all eight warps share them) or 64 rows (two groups of 32).
+// Both products: tiles of kRowsTile rows, which all eight warps share; the second
+// one alone: 64 rows in two groups of 32.  (Tiles of 64 rows for both were slower
+// at every size measured, 256 to 4096 rows: 77 against 77 us for 4096 x 5120 x
+// 5120 fp32 at rank 16, 245 against 172 at rank 64.)
+constexpr int kRowsTile = 16;
 struct RowsPlan {
-    int rows, cs, tiles;
+    int cs, tiles;
 };
 
 template <int XT, int WT, bool BWD, int MT, int RG, int NT, bool GIVEN>
@@ -776,7 +805,7 @@ template <int XT, int WT, bool BWD>
 cudaError_t launch_rows_shape(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
     if constexpr (XT != kF32)  // many rows of 16-bit activations take their sums from the tensor cores
         if (q.given) return launch_rows_rank<XT, WT, BWD, 2, 2, true>(q, plan, s);
-    return plan.rows == 16 ? launch_rows_rank<XT, WT, BWD, 1, 1, false>(q, plan, s) : launch_rows_rank<XT, WT, BWD, 2, 2, false>(q, plan, s);
+    return launch_rows_rank<XT, WT, BWD, 1, 1, false>(q, plan, s);
 }
 
 // Defined once for each pair of types (qg_lora_bf16.cu and its siblings).

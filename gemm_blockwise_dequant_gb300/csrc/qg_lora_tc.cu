@@ -165,19 +165,25 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
     const float scale = q.bwd && p.scaling ? __ldg(p.scaling + t.adapter) : 1.f;
     const int r_lo = kTileRows * rank / q.cs, r_hi = min(kTileRows * (rank + 1) / q.cs, t.rows);
     float mx = 0.f, mv = 0.f;
-    for (int e = tid; e < (r_hi - r_lo) * r; e += kShrinkThreads) {
-        const int row = r_lo + e / r, j = e % r;
-        float s = 0.f;
-        if (q.cs > 1)
-            for (int w = 0; w < q.cs; ++w) s += peer_float(mine + row * stride + j, w);
-        else
-            s = mine[row * stride + j];
-        s *= scale;
+    for (int e = tid; e < (r_hi - r_lo) * (r / 4); e += kShrinkThreads) {  // four values of a row
+        const int row = r_lo + e / (r / 4), j = e % (r / 4) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q.cs > 1) {
+            for (int w = 0; w < q.cs; ++w) {
+                const float4 v = peer_float4(mine + row * stride + j, w);
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+        } else {
+            s = *reinterpret_cast<const float4 *>(mine + row * stride + j);
+        }
+        s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
         const size_t at = static_cast<size_t>(t.t0 + row) * r + j;
-        q.sums[at] = s;
-        if (q.V_copy) q.V_copy[at] = s;
-        mx = fmaxf(mx, fabsf(s));
-        if (q.V) mv = fmaxf(mv, fabsf(__ldg(q.V + at)));
+        *reinterpret_cast<float4 *>(q.sums + at) = s;
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w))));
+        if (q.V) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(q.V + at));
+            mv = fmaxf(mv, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        }
     }
     if (q.tile_adapter) {
         atomicMax(&smax[0], __float_as_uint(mx));  // of values that are not negative: the order does not matter
@@ -438,18 +444,39 @@ __global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __gr
     }
     const int ncol = min(kCols, q.cols[which] - col0), width = kCols / q.cs;
     const float scale = (which && p.scaling ? __ldg(p.scaling + a) : 1.f) * down;
-    for (int e = tid; e < r * width; e += kWgThreads) {
-        const int j = which ? e % r : e / width, cc = rank * width + (which ? e / r : e % width);
-        if (cc >= ncol) continue;
-        float s = 0.f;
-        if (q.cs > 1)
-            for (int k = 0; k < q.cs; ++k) s += peer_float(sums + j * OS + cc, k);
-        else
-            s = sums[j * OS + cc];
+    auto total = [&](int j, int cc) {  // four columns of the cluster's sums
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q.cs == 1) return *reinterpret_cast<const float4 *>(sums + j * OS + cc);
+        for (int k = 0; k < q.cs; ++k) {
+            const float4 v = peer_float4(sums + j * OS + cc, k);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        return s;
+    };
+    auto put = [&](size_t at, float s) {
         s *= scale;
-        const size_t at = which ? (static_cast<size_t>(a) * p.N + col0 + cc) * r + j : (static_cast<size_t>(a) * r + j) * p.K + col0 + cc;
         if (q.accumulate) s += load_elem(q.out[which], q.g_dtype, at);
         store_y_elem(q.out[which], q.g_dtype, at, s);
+    };
+    for (int e = tid; e < r * (width / 4); e += kWgThreads) {
+        // dA: neighbours take neighbouring columns; dB: neighbouring j of four columns
+        const int j = which ? e % r : e / (width / 4), cc = rank * width + (which ? e / r : e % (width / 4)) * 4;
+        if (cc >= ncol) continue;
+        const float4 s = total(j, cc);
+        const float v[4] = {s.x, s.y, s.z, s.w};
+        if (!which) {
+            const size_t at = (static_cast<size_t>(a) * r + j) * p.K + col0 + cc;  // a multiple of four, and so is ncol
+            if (!q.accumulate && q.g_dtype == kF32) {
+                *reinterpret_cast<float4 *>(static_cast<float *>(q.out[0]) + at) = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) put(at + i, v[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (cc + i < ncol) put((static_cast<size_t>(a) * p.N + col0 + cc + i) * r + j, v[i]);
+        }
     }
     if (q.cs > 1) {
         __syncwarp();
@@ -534,10 +561,10 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     q.cols[1] = p.N;
     for (int w = 0; w < 2; ++w) q.tiles[w] = (q.cols[w] + kCols - 1) / kCols;
     q.fault = fault_word();
-    // A CTA an SM, while each still has eight steps.
+    // Two CTAs an SM, while each still has four steps.
     const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * p.na;
     q.cs = 1;
-    while (q.cs < 8 && ctas * q.cs * 2 <= device_info().sm_count && p.T / p.na >= 16 * kStep * q.cs) q.cs *= 2;
+    while (q.cs < 8 && ctas * q.cs * 2 <= 2 * device_info().sm_count && p.T / p.na >= 8 * kStep * q.cs) q.cs *= 2;
     CUtensorMap maps[3];
     const cuuint32_t box[3] = {64, kStep, 1};
     for (int w = 0; w < 2; ++w) {

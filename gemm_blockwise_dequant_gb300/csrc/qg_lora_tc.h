@@ -8,7 +8,6 @@ namespace qg {
 struct ShrinkTc {
     LoraProblem p;
     float *sums;             // [T][rank]: V (unscaled) or G (scaled)
-    float *V_copy;           // a second place for them, or null
     const float *V;          // backward: the forward pass's V, for its largest values
     float *tile_max;         // [2][CTAs]: largest sum and largest V of a CTA's rows; or null
     int *tile_adapter;       // [CTAs] or null

@@ -34,17 +34,24 @@ constexpr int kWgChunk = 64;  // rows staged at a time
 // XT: type of the wide matrix; NATIVE: bf16 MMAs; MJ: 16-row groups of the rank
 template <int XT, bool NATIVE, int MJ>
 struct WgradKernel {
-    static constexpr int CPL = (XT == kF32 || MJ == 4) ? 4 : 8;  // columns of a lane
+    static constexpr int CPL = (XT == kF32 || MJ > 1) ? 4 : 8;   // columns of a lane
     static constexpr int WCOLS = 8 * CPL, COLS = 8 * WCOLS;      // of a warp, of a CTA
     static constexpr int RJ = 16 * MJ;
-    static constexpr int QS = NATIVE ? kWgChunk + 16 : kWgChunk + 16;  // row stride of the staged factor: banks of 8 (4) rows differ
-    static constexpr int QBYTES = RJ * QS * (NATIVE ? 2 : 4);          // one term
+    static constexpr int QBYTES = RJ * kWgChunk * (NATIVE ? 2 : 4);    // one term of the staged factor, [j][t]
     static constexpr int OS = COLS + 4;                                // row stride of the sums
     static constexpr int PB = CPL * (XT == kF32 ? 4 : 2);              // bytes of a lane's piece of a row: 16 or 8
-    static constexpr int STAGES = 3;
+    static constexpr int STAGES = XT == kF32 ? 2 : 3;
     static constexpr int WIDE_BYTES = 8 * STAGES * 8 * 32 * PB;        // the lanes' queues: 8 rows a step
     static constexpr int SMEM = (4 * QBYTES + WIDE_BYTES > RJ * OS * 4) ? 4 * QBYTES + WIDE_BYTES : RJ * OS * 4;
     static constexpr int QPT = kWgChunk * RJ / 256;                    // staged values of a thread
+
+    // Place of the staged value (j, t): the row's four-value pieces are permuted by
+    // j, so that neither the lanes that write 16 values j of one t nor those that
+    // read pieces of 4 to 8 rows j meet in a bank.
+    static __device__ __forceinline__ int place(int j, int t) {
+        const int f = NATIVE ? ((j & 3) << 2) | ((j >> 2) & 3) : ((j & 1) << 2) | ((j >> 1) & 3);
+        return j * kWgChunk + (((t >> 2) ^ f) << 2) + (t & 3);
+    }
 
     // Walks the 64-row chunks of the adapter's requests.
     struct Walk {
@@ -132,7 +139,7 @@ struct WgradKernel {
             unsigned char *hi = sm + 2 * b * QBYTES, *lo = hi + QBYTES;
 #pragma unroll
             for (int i = 0; i < QPT; ++i) {
-                const int e = tid + i * 256, at = (e % RJ) * QS + e / RJ;
+                const int e = tid + i * 256, at = place(e % RJ, e / RJ);
                 if constexpr (NATIVE) {
                     uint16_t h, l;
                     split16<kBF16>(stage[i], h, l);
@@ -205,7 +212,7 @@ struct WgradKernel {
                         for (int m = 0; m < MJ; ++m)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const int at = (m * 16 + h * 8 + g) * QS + tt;
+                                const int at = place(m * 16 + h * 8 + g, tt);
                                 fh[m][h] = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(hi) + at);
                                 fl[m][h] = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(lo) + at);
                             }
@@ -221,35 +228,42 @@ struct WgradKernel {
                             }
                         }
                     } else {
+                        // two columns' operands, split once, against every row group of the rank
 #pragma unroll
-                        for (int m = 0; m < MJ; ++m) {
-                            uint4 fh[2], fl[2];
+                        for (int i0 = 0; i0 < CPL; i0 += 2) {
+                            uint32_t v[2][4], vl[2][4];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int at = (m * 16 + h * 8 + g) * QS + tt;
-                                fh[h] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(hi) + at);
-                                fl[h] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(lo) + at);
-                            }
-#pragma unroll
-                            for (int i = 0; i < CPL; ++i) {
-                                uint32_t v[4], vl[4];
+                            for (int i = 0; i < 2; ++i)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     if constexpr (XT == kF32) {
-                                        split_tf32(__uint_as_float(x[s][e][i]), v[e], vl[e]);
+                                        split_tf32(__uint_as_float(x[s][e][i0 + i]), v[i][e], vl[i][e]);
                                     } else {
-                                        const uint32_t z = x[s][e][i >> 1];
-                                        v[e] = __float_as_uint(to_float<XT>(static_cast<uint16_t>((i & 1) ? z >> 16 : z & 0xFFFFu)));
+                                        const uint32_t z = x[s][e][i0 >> 1];
+                                        v[i][e] = __float_as_uint(to_float<XT>(static_cast<uint16_t>(i ? z >> 16 : z & 0xFFFFu)));
                                     }
                                 }
-                                if constexpr (XT == kF32) {
-                                    mma8(acc[m][i], fh[0].x, fh[1].x, fh[0].y, fh[1].y, vl[0], vl[1]);
-                                    mma8(acc[m][i], fh[0].z, fh[1].z, fh[0].w, fh[1].w, vl[2], vl[3]);
+#pragma unroll
+                            for (int m = 0; m < MJ; ++m) {
+                                uint4 fh[2], fl[2];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int at = place(m * 16 + h * 8 + g, tt);
+                                    fh[h] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(hi) + at);
+                                    fl[h] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(lo) + at);
                                 }
-                                mma8(acc[m][i], fl[0].x, fl[1].x, fl[0].y, fl[1].y, v[0], v[1]);
-                                mma8(acc[m][i], fl[0].z, fl[1].z, fl[0].w, fl[1].w, v[2], v[3]);
-                                mma8(acc[m][i], fh[0].x, fh[1].x, fh[0].y, fh[1].y, v[0], v[1]);
-                                mma8(acc[m][i], fh[0].z, fh[1].z, fh[0].w, fh[1].w, v[2], v[3]);
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    float (&d)[4] = acc[m][i0 + i];
+                                    if constexpr (XT == kF32) {
+                                        mma8(d, fh[0].x, fh[1].x, fh[0].y, fh[1].y, vl[i][0], vl[i][1]);
+                                        mma8(d, fh[0].z, fh[1].z, fh[0].w, fh[1].w, vl[i][2], vl[i][3]);
+                                    }
+                                    mma8(d, fl[0].x, fl[1].x, fl[0].y, fl[1].y, v[i][0], v[i][1]);
+                                    mma8(d, fl[0].z, fl[1].z, fl[0].w, fl[1].w, v[i][2], v[i][3]);
+                                    mma8(d, fh[0].x, fh[1].x, fh[0].y, fh[1].y, v[i][0], v[i][1]);
+                                    mma8(d, fh[0].z, fh[1].z, fh[0].w, fh[1].w, v[i][2], v[i][3]);
+                                }
                             }
                         }
                     }
@@ -297,7 +311,7 @@ struct WgradKernel {
 };
 
 template <int XT, bool NATIVE, int MJ>
-__global__ void __launch_bounds__(256, 2) lora_wgrad_kernel(const WgradArgs q) {
+__global__ void __launch_bounds__(256, MJ == 4 ? 1 : 2) lora_wgrad_kernel(const WgradArgs q) {
     WgradKernel<XT, NATIVE, MJ>::run(q);
 }
 

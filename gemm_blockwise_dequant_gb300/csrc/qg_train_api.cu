@@ -75,9 +75,9 @@ int dgrad_common(const void *dY, int dy_dtype, const uint8_t *W, const void *par
 
 extern "C" {
 
-size_t qg_lora_apply_workspace_bytes(int rows, int num_segments, int rank) {
-    if (rows <= 0 || num_segments < 0 || rank <= 0) return 0;
-    return qg::lora_apply_workspace_bytes(rows, num_segments, rank);
+size_t qg_lora_apply_workspace_bytes(int rows, int num_segments, int rank, int N, int K) {
+    if (rows <= 0 || num_segments < 0 || rank <= 0 || N <= 0 || K <= 0) return 0;
+    return qg::lora_apply_workspace_bytes(rows, num_segments, rank, N, K);
 }
 
 int qg_lora_apply(const void *X, int x_dtype, int64_t ldx, const int64_t *seg_offsets, const int32_t *seg_adapter,
@@ -98,7 +98,7 @@ int qg_lora_apply(const void *X, int x_dtype, int64_t ldx, const int64_t *seg_of
     if (!aligned(X, 16) || (ldx * esize(x_dtype)) % 16 || !aligned(A, 16) || !aligned(B, 16)) return QG_ERR_INVALID_ARG;
     if (!aligned(Y, esize(y_dtype)) || (Y_in && !aligned(Y_in, esize(y_in_dtype))) || !aligned(V_out, 16))
         return QG_ERR_INVALID_ARG;
-    st = check_workspace(workspace, workspace_bytes, qg::lora_apply_workspace_bytes(rows, num_segments, rank));
+    st = check_workspace(workspace, workspace_bytes, qg::lora_apply_workspace_bytes(rows, num_segments, rank, N, K));
     if (st != QG_OK) return st;
     qg::LoraApply q{};
     q.p = {seg_offsets, seg_adapter, num_segments, A, B, w_dtype, scaling, num_adapters, rank, rows, N, K, status_dev};

@@ -461,7 +461,7 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
  * Sums are fp32 (16-bit operands multiply exactly; with fp32 operands each
  * value is split in two TF32 terms, dropping less than 2^-21 of a product).
  * Deterministic.  workspace: at least qg_lora_apply_workspace_bytes(rows,
- * num_segments, rank) bytes, 16-byte aligned (NULL when that is 0).
+ * num_segments, rank, N, K) bytes, 16-byte aligned (NULL when that is 0).
  *
  * qg_lora_grad -- the backward pass, given dY, X and the V of the forward pass:
  *   G[t][j]  = scaling[a] * sum_n dY[t][n] * B[a][n][j]         (fp32)
@@ -478,7 +478,7 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
  *                adapter without rows.  accumulate = 1 adds to their contents.
  *   workspace    at least qg_lora_grad_workspace_bytes(...) bytes, 16-byte aligned
  */
-size_t qg_lora_apply_workspace_bytes(int rows, int num_segments, int rank);
+size_t qg_lora_apply_workspace_bytes(int rows, int num_segments, int rank, int N, int K);
 int qg_lora_apply(const void *X, int x_dtype, int64_t ldx, const int64_t *seg_offsets, const int32_t *seg_adapter,
                   int num_segments, const void *A, const void *B, int w_dtype, const float *scaling, int num_adapters,
                   int rank, const void *Y_in, int y_in_dtype, int64_t ldy_in, void *Y, int y_dtype, int64_t ldy,
