@@ -35,7 +35,7 @@ struct RowsArgs {
     int out_dtype;
     int64_t ld_out;
     float *sums;         // V_out / G or null, [T][rank]
-    float *tile_max;     // backward: [2][tiles] largest |G| and |V| of a tile's rows, and its adapter; or null
+    float *tile_max;     // backward: [2][tiles] largest finite |G| and |V| of a tile's rows, and its adapter; or null
     int *tile_adapter;
     const float *V;
     const float *given;  // the first product's sums where they are known, or null
@@ -89,18 +89,20 @@ struct RowsKernel {
     // The adapter's values of a lane's chunk.  Forward: A[a][j][k ..], the lane
     // column g of tile i is j = j0 + 8 i + g; w.v[i] is what tile i's MMAs take.
     // Backward: B[a][k + e][j], j = j0 + g NT + i, NT contiguous values of EL rows.
+    // Tiles i0 .. i0 + NH - 1 at a time.
+    static constexpr int NH = NT < 4 ? NT : 4;
     struct W1 {
-        uint32_t v[BWD ? EL : NT][BWD ? (WT == kF32 ? NT : NT / 2) : 4];
+        uint32_t v[BWD ? EL : NH][BWD ? (WT == kF32 ? NH : NH / 2) : 4];
     };
 
-    static __device__ __forceinline__ void load_w1(const RowsArgs &q, int a, int j0, int k, int g, W1 &w) {
+    static __device__ __forceinline__ void load_w1(const RowsArgs &q, int a, int j0, int i0, int k, int g, W1 &w) {
         const int r = q.p.r;
         if constexpr (!BWD) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
+            for (int i = 0; i < NH; ++i) {
                 w.v[i][0] = w.v[i][1] = w.v[i][2] = w.v[i][3] = 0;
-                if (j0 + 8 * i >= r || k >= q.c1) continue;  // the rank is a multiple of 8
-                const size_t at = (static_cast<size_t>(a) * r + j0 + 8 * i + g) * q.c1 + k;
+                if (j0 + 8 * (i0 + i) >= r || k >= q.c1) continue;  // the rank is a multiple of 8
+                const size_t at = (static_cast<size_t>(a) * r + j0 + 8 * (i0 + i) + g) * q.c1 + k;
                 if constexpr (WT == kF32 || NATIVE) {
                     const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(q.w1) + at * (NATIVE ? 2 : 4)));
                     w.v[i][0] = v.x, w.v[i][1] = v.y, w.v[i][2] = v.z, w.v[i][3] = v.w;
@@ -111,9 +113,9 @@ struct RowsKernel {
                 }
             }
         } else {
-            constexpr int WORDS = WT == kF32 ? NT : NT / 2;
+            constexpr int WORDS = WT == kF32 ? NH : NH / 2;
             const bool jin = j0 + g * NT < r;  // a multiple of 8: the NT values are in or out
-            const char *src = static_cast<const char *>(q.w1) + ((static_cast<size_t>(a) * q.c1 + k) * r + j0 + g * NT) * (WT == kF32 ? 4 : 2);
+            const char *src = static_cast<const char *>(q.w1) + ((static_cast<size_t>(a) * q.c1 + k) * r + j0 + g * NT + i0) * (WT == kF32 ? 4 : 2);
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
                 const bool in = jin && k + e < q.c1;
@@ -323,38 +325,50 @@ struct RowsKernel {
                         constexpr bool TOGETHER = NT <= 4;  // both chunks' adapter values, under the wait for the row
                         W1 wb[TOGETHER ? 2 : 1];
                         if (TOGETHER) {
-                            load_w1(q, t.adapter, j0, b * BLK + c * EL, g, wb[0]);
-                            load_w1(q, t.adapter, j0, b * BLK + CH + c * EL, g, wb[TOGETHER ? 1 : 0]);
+                            load_w1(q, t.adapter, j0, 0, b * BLK + c * EL, g, wb[0]);
+                            load_w1(q, t.adapter, j0, 0, b * BLK + CH + c * EL, g, wb[TOGETHER ? 1 : 0]);
                         }
                         queue_wait<STAGES - 1>();
                         const uint4 *x = queue + slot * PIECES * 32;
+                        float part_acc[MT][NT][4] = {};
 #pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            if (!TOGETHER) load_w1(q, t.adapter, j0, b * BLK + s * CH + c * EL, g, wb[0]);
-                            const W1 &w = wb[TOGETHER ? s : 0];
+                        for (int s = 0; s < 2; ++s)
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                const uint4 x0 = x[((s * MT + m) * 2) * 32], x1 = x[((s * MT + m) * 2 + 1) * 32];
-                                if constexpr (NATIVE) {
+                            for (int i0 = 0; i0 < NT; i0 += NH) {
+                                if (!TOGETHER) load_w1(q, t.adapter, j0, i0, b * BLK + s * CH + c * EL, g, wb[0]);
+                                const W1 &w = wb[TOGETHER ? s : 0];
 #pragma unroll
-                                    for (int i = 0; i < NT; ++i) {
-                                        mma16<XT>(acc[m][i], x0.x, x1.x, x0.y, x1.y, w1_word(w, i, 0), w1_word(w, i, 1));
-                                        mma16<XT>(acc[m][i], x0.z, x1.z, x0.w, x1.w, w1_word(w, i, 2), w1_word(w, i, 3));
-                                    }
-                                } else {
+                                for (int m = 0; m < MT; ++m) {
+                                    const uint4 x0 = x[((s * MT + m) * 2) * 32], x1 = x[((s * MT + m) * 2 + 1) * 32];
+                                    if constexpr (NATIVE) {
 #pragma unroll
-                                    for (int half = 0; half < 2; ++half) {
-                                        uint32_t hi[4], lo[4];
-                                        split_tf32(__uint_as_float(half ? x0.z : x0.x), hi[0], lo[0]);
-                                        split_tf32(__uint_as_float(half ? x1.z : x1.x), hi[1], lo[1]);
-                                        split_tf32(__uint_as_float(half ? x0.w : x0.y), hi[2], lo[2]);
-                                        split_tf32(__uint_as_float(half ? x1.w : x1.y), hi[3], lo[3]);
+                                        for (int i = 0; i < NH; ++i) {
+                                            mma16<XT>(part_acc[m][i0 + i], x0.x, x1.x, x0.y, x1.y, w1_word(w, i, 0), w1_word(w, i, 1));
+                                            mma16<XT>(part_acc[m][i0 + i], x0.z, x1.z, x0.w, x1.w, w1_word(w, i, 2), w1_word(w, i, 3));
+                                        }
+                                    } else {
 #pragma unroll
-                                        for (int i = 0; i < NT; ++i) mma_tf32_split(acc[m][i], hi, lo, w1_word(w, i, 2 * half), w1_word(w, i, 2 * half + 1));
+                                        for (int half = 0; half < 2; ++half) {
+                                            uint32_t hi[4], lo[4];
+                                            split_tf32(__uint_as_float(half ? x0.z : x0.x), hi[0], lo[0]);
+                                            split_tf32(__uint_as_float(half ? x1.z : x1.x), hi[1], lo[1]);
+                                            split_tf32(__uint_as_float(half ? x0.w : x0.y), hi[2], lo[2]);
+                                            split_tf32(__uint_as_float(half ? x1.w : x1.y), hi[3], lo[3]);
+#pragma unroll
+                                            for (int i = 0; i < NH; ++i)
+                                                mma_tf32_split(part_acc[m][i0 + i], hi, lo, w1_word(w, i, 2 * half), w1_word(w, i, 2 * half + 1));
+                                        }
                                     }
                                 }
                             }
-                        }
+                        // The MMAs add with truncation: a block's sums are added to the row's with
+                        // rounding, so the error does not grow with the row.
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[m][i][e] += part_acc[m][i][e];
                         slot = slot == STAGES - 1 ? 0 : slot + 1;
                     }
                     queue_wait<0>();
@@ -401,8 +415,8 @@ struct RowsKernel {
                     }
                     whole[e] = s;
                     if (maxima) {
-                        mx = fmaxf(mx, fabsf(s));
-                        if (j < r && row < t.rows) mv = fmaxf(mv, fabsf(__ldg(q.V + static_cast<size_t>(t.t0 + row) * r + j)));
+                        mx = fmaxf(mx, finite_abs(s));
+                        if (j < r && row < t.rows) mv = fmaxf(mv, finite_abs(__ldg(q.V + static_cast<size_t>(t.t0 + row) * r + j)));
                     }
                 }
                 if (maxima) {  // at the place of the partial sums, which have been read

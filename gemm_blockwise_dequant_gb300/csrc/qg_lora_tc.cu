@@ -37,6 +37,11 @@ constexpr int kInBytes = kTileRows * kStep * 2;
 constexpr int kBlock = kStep * 128;  // 64 rows of a 64-column block
 constexpr int kShrinkThreads = 192;  // TMA, MMA, four warps that read the sums back
 constexpr int kBars = 256;           // bytes of barriers and flags
+// The MMAs add to their accumulator with truncation (about 1.4e-8 of a sum each
+// time, measured), which would grow with the contraction: after this many steps
+// of four MMAs or more the accumulator is added, with rounding, to sums in
+// registers while the next steps go to a second one.
+constexpr int kDrainShrink = 8, kDrainWgrad = 4;
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
@@ -64,8 +69,9 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int stage_bytes = kInBytes + q.w_bytes;
     unsigned char *bars = sm + q.stages * stage_bytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + q.stages, *accf = empty + q.stages;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
+    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + q.stages;
+    uint64_t *accf = empty + q.stages, *drained = accf + 2;  // of two accumulators
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     unsigned *smax = tmem_slot + 2;  // largest sums and V of this CTA's rows, as bits
     const LoraProblem &p = q.p;
@@ -86,13 +92,16 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        mbar_init(accf, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&drained[i], 4);
+        }
         *abort_flag = 0;
         smax[0] = smax[1] = 0;
         mbar_fence_init();
     }
-    const uint32_t cols = pow2_cols(q.n);
-    if (warp == 1) tmem_alloc(tmem_slot, cols);
+    const uint32_t cols = pow2_cols(q.n);  // of one accumulator
+    if (warp == 1) tmem_alloc(tmem_slot, 2 * cols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -118,44 +127,64 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
         if (lane == 0) {
             const uint32_t idesc = idesc_f16(128, q.n, q.bf16) | (q.bwd ? 1u << 16 : 0u);
             for (int i = 0; i < ns; ++i) {
-                const int s = i % q.stages;
-                ok = mbar_wait(&full[s], (i / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
+                const int s = i % q.stages, blk = i / kDrainShrink, buf = blk & 1;
+                const bool fresh = i % kDrainShrink == 0;
+                ok = (!fresh || mbar_wait(&drained[buf], ((blk >> 1) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC)) &&
+                     mbar_wait(&full[s], (i / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t at = smem_u32(sm + s * stage_bytes);
                 const uint64_t ad = sdesc_k128(at), bd = q.bwd ? sdesc_mn(at + kInBytes) : sdesc_k128(at + kInBytes);
 #pragma unroll
-                for (int k = 0; k < kStep / 16; ++k) umma_f16(tmem, ad + 2 * k, bd + (q.bwd ? 128 : 2) * k, idesc, (i | k) != 0);
+                for (int k = 0; k < kStep / 16; ++k) umma_f16(tmem + buf * cols, ad + 2 * k, bd + (q.bwd ? 128 : 2) * k, idesc, !fresh || k > 0);
                 umma_commit(&empty[s]);
+                if (i % kDrainShrink == kDrainShrink - 1 || i == ns - 1) umma_commit(&accf[buf]);
             }
-            umma_commit(accf);
         }
-    } else {
-        ok = mbar_wait(accf, 0, abort_flag, q.fault, FAULT_WAIT_TC);
+    }
+    float sum[4][32];  // of this thread's row
+    if (warp >= 2) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+        for (int blk = 0; blk * kDrainShrink < ns; ++blk) {
+            const int buf = blk & 1;
+            ok = mbar_wait(&accf[buf], (blk >> 1) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c * 32 >= q.n) break;
+                uint32_t v[32];
+                tmem_ld32(tmem + buf * cols + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c * 32, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(v[i]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&drained[buf]);
+        }
     }
     __syncwarp();
     // The CTA's sums to shared memory (over the ring: every stage has been read), then the cluster's.
     float *mine = reinterpret_cast<float *>(sm);
     const int stride = q.n + 4;
+    tc_fence_before();
+    __syncthreads();
     if (warp >= 2) {
-        tc_fence_after();
-        const int sub = warp & 3;
-        for (int c = 0; c < q.n; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + c, v);
-            float4 *dst = reinterpret_cast<float4 *>(mine + (sub * 32 + lane) * stride + c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float4 *dst = reinterpret_cast<float4 *>(mine + ((warp & 3) * 32 + lane) * stride + c * 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c + 4 * i < q.n)
-                    dst[i] = ok && ns > 0 ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c * 32 + 4 * i < q.n) dst[i] = make_float4(sum[c][4 * i], sum[c][4 * i + 1], sum[c][4 * i + 2], sum[c][4 * i + 3]);
         }
-        tc_fence_before();
     }
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, cols);
+        tmem_dealloc(tmem, 2 * cols);
         __syncwarp();
     }
     if (q.cs > 1) {
@@ -179,10 +208,10 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
         s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
         const size_t at = static_cast<size_t>(t.t0 + row) * r + j;
         *reinterpret_cast<float4 *>(q.sums + at) = s;
-        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w))));
+        mx = fmaxf(mx, fmaxf(fmaxf(finite_abs(s.x), finite_abs(s.y)), fmaxf(finite_abs(s.z), finite_abs(s.w))));
         if (q.V) {
             const float4 v = __ldg(reinterpret_cast<const float4 *>(q.V + at));
-            mv = fmaxf(mv, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            mv = fmaxf(mv, fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w))));
         }
     }
     if (q.tile_adapter) {
@@ -214,7 +243,7 @@ __device__ __forceinline__ int fp16_exponent(unsigned largest) {
     return ef == 0 || ef == 255 ? 0 : min(max(14 - (ef - 127), -100), 100);
 }
 
-// The largest |value| of an adapter's G (which = 0) or V (1), from the shrink launch; every thread of the block calls it.
+// The largest finite |value| of an adapter's G (which = 0) or V (1), from the shrink launch; every thread of the block calls it.
 __device__ __forceinline__ unsigned largest_of(const float *tile_max, const int *tile_adapter, int parts, int which, int a, unsigned *smax) {
     float mx = 0.f;
     for (int i = threadIdx.x; i < parts; i += blockDim.x)
@@ -297,8 +326,9 @@ struct StepWalk {
     }
 };
 
-template <int TERMS, bool BF16>
-__global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap dy_map,
+// DRAIN: fp32 gradients.  One CTA an SM then, for two accumulators and the registers of the sums.
+template <int TERMS, bool BF16, bool DRAIN>
+__global__ void __launch_bounds__(kWgThreads, DRAIN ? 1 : 2) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap dy_map,
                                                                       const __grid_constant__ CUtensorMap thin_map, const WgradTc q) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -306,8 +336,9 @@ __global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __gr
     const int blocks = q.n > 64 ? 2 : 1;  // 64-column blocks of the thin operand
     const int term_bytes = blocks * kBlock, thin_bytes = TERMS * term_bytes, stage_bytes = kWideBytes + thin_bytes;
     unsigned char *bars = sm + q.stages * stage_bytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + q.stages, *masked = empty + q.stages, *accf = masked + q.stages;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
+    uint64_t *full = reinterpret_cast<uint64_t *>(bars), *empty = full + q.stages, *masked = empty + q.stages;
+    uint64_t *accf = masked + q.stages, *drained = accf + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     unsigned *smax = tmem_slot + 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -329,13 +360,16 @@ __global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __gr
             mbar_init(&empty[i], 1);
             mbar_init(&masked[i], 8);
         }
-        mbar_init(accf, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&drained[i], 8);
+        }
         *abort_flag = 0;
         *smax = 0;
         mbar_fence_init();
     }
     if (__syncthreads_or(bad)) return;  // the whole cluster
-    if (warp == 1) tmem_alloc(tmem_slot, kCols);
+    if (warp == 1) tmem_alloc(tmem_slot, (DRAIN ? 2 : 1) * kCols);
     float down = 1.f;
     if (!BF16) down = exp2i(-fp16_exponent(largest_of(q.tile_max, q.tile_adapter, q.parts, which, a, smax)));
     tc_fence_before();
@@ -369,8 +403,10 @@ __global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __gr
         const int thin_block = blocks == 2 ? kBlock : 0;  // up to rank 64 rows 64 .. 127 repeat the first ones, unread
         while (walk.next(p, a, q.cs, t0, rows)) {
             if (lane == 0) {
-                const int s = steps % q.stages;
-                ok = mbar_wait(&full[s], (steps / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC) &&
+                const int s = steps % q.stages, blk = DRAIN ? steps / kDrainWgrad : 0, buf = blk & 1;
+                const bool fresh = DRAIN ? steps % kDrainWgrad == 0 : steps == 0;
+                ok = (!DRAIN || !fresh || mbar_wait(&drained[buf], ((blk >> 1) & 1) ^ 1, abort_flag, q.fault, FAULT_WAIT_TC)) &&
+                     mbar_wait(&full[s], (steps / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC) &&
                      mbar_wait(&masked[s], (steps / q.stages) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
                 if (ok) {
                     tc_fence_after();
@@ -380,16 +416,43 @@ __global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __gr
                     for (int m = TERMS - 1; m >= 0; --m)
 #pragma unroll
                         for (int k = 0; k < kStep / 16; ++k)
-                            umma_f16(tmem, ad + m * (term_bytes >> 4) + 128 * k, bd + 128 * k, idesc, steps > 0 || k > 0 || m < TERMS - 1);
+                            umma_f16(tmem + buf * kCols, ad + m * (term_bytes >> 4) + 128 * k, bd + 128 * k, idesc, !fresh || k > 0 || m < TERMS - 1);
                     umma_commit(&empty[s]);
+                    if (DRAIN && steps % kDrainWgrad == kDrainWgrad - 1) umma_commit(&accf[buf]);
                 }
             }
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             ++steps;
         }
-        if (lane == 0) umma_commit(accf);
+        // what is left in the last accumulator
+        if (lane == 0 && (!DRAIN || steps % kDrainWgrad)) umma_commit(&accf[DRAIN ? (steps / kDrainWgrad) & 1 : 0]);
         __syncwarp();
-    } else {
+    }
+    float sum[DRAIN ? 4 : 1][32];  // DRAIN: value j = the lane's, 128 columns
+    if (warp >= 2) {
+        const int sub = warp & 3, half = (warp - 2) >> 2;
+#pragma unroll
+        for (int c = 0; c < (DRAIN ? 4 : 1); ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+        auto drain = [&](int blk) {
+            const int buf = blk & 1;
+            ok = mbar_wait(&accf[buf], (blk >> 1) & 1, abort_flag, q.fault, FAULT_WAIT_TC);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            tc_fence_after();
+            if (sub * 32 < r)
+#pragma unroll
+                for (int c = 0; c < (DRAIN ? 4 : 1); ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(tmem + buf * kCols + (static_cast<uint32_t>(sub * 32) << 16) + half * 128 + c * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(v[i]);
+                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&drained[buf]);
+            return true;
+        };
         // A request that ends inside a step: the rows behind it become zeros in both operands (either may hold a NaN).
         const int u = tid - 64;
         while (walk.next(p, a, q.cs, t0, rows)) {
@@ -407,8 +470,16 @@ __global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __gr
             }
             if (lane == 0) mbar_arrive(&masked[s]);
             ++steps;
+            // the accumulator before the one that the MMAs are at
+            if (DRAIN && steps % kDrainWgrad == 0 && steps > kDrainWgrad && !drain(steps / kDrainWgrad - 2)) break;
         }
-        ok = mbar_wait(accf, 0, abort_flag, q.fault, FAULT_WAIT_TC) && ok;
+        if constexpr (DRAIN) {
+            const int whole = steps / kDrainWgrad;
+            if (ok && whole > 0) ok = drain(whole - 1);
+            if (ok && steps % kDrainWgrad) ok = drain(whole);
+        } else {
+            ok = mbar_wait(accf, 0, abort_flag, q.fault, FAULT_WAIT_TC) && ok;
+        }
     }
     __syncwarp();
     // The CTA's sums [j][column] to shared memory (over the ring), then the cluster's, and out.
@@ -419,23 +490,25 @@ __global__ void __launch_bounds__(kWgThreads, 2) lora_wgrad_tc_kernel(const __gr
         tc_fence_after();
         const int sub = warp & 3, half = (warp - 2) >> 2;  // 32 values j; the half of the columns
         if (sub * 32 < r)
-#pragma unroll 1
-            for (int c = half * 128; c < half * 128 + 128; c += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + c, v);
-                if (sub * 32 + lane >= r) continue;
-                float4 *dst = reinterpret_cast<float4 *>(sums + (sub * 32 + lane) * OS + c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dst[i] = ok && steps > 0 ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                if constexpr (!DRAIN) tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + half * 128 + c * 32, v);
+                float4 *dst = reinterpret_cast<float4 *>(sums + (sub * 32 + lane) * OS + half * 128 + c * 32);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if constexpr (DRAIN) x = make_float4(sum[c][4 * i], sum[c][4 * i + 1], sum[c][4 * i + 2], sum[c][4 * i + 3]);
+                    else if (ok && steps > 0) x = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                    if (sub * 32 + lane < r) dst[i] = x;
+                }
             }
         tc_fence_before();
     }
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kCols);
+        tmem_dealloc(tmem, (DRAIN ? 2 : 1) * kCols);
         __syncwarp();
     }
     if (q.cs > 1) {
@@ -527,7 +600,7 @@ cudaError_t launch_shrink_tc(ShrinkTc q, const void *in, int64_t ld, const void 
 
 namespace {
 
-template <int TERMS, bool BF16>
+template <int TERMS, bool BF16, bool DRAIN>
 cudaError_t launch_wgrad_terms(WgradTc q, const TermsTc &c, const CUtensorMap *maps, cudaStream_t s) {
     const LoraProblem &p = q.p;
     cudaError_t e = launch_pdl(lora_terms_kernel<TERMS, BF16>, dim3(static_cast<unsigned>(shrink_tc_tiles(p.T, p.S)), 2), dim3(256), 0, s, c);
@@ -537,12 +610,12 @@ cudaError_t launch_wgrad_terms(WgradTc q, const TermsTc &c, const CUtensorMap *m
     constexpr int kOverhead = 1024 + kBars;
     q.stages = std::min(4, (227 * 1024 - kOverhead) / stage);
     const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * q.cs * p.na;
-    if (ctas > device_info().sm_count && 2 * stage + kOverhead <= 111 * 1024) q.stages = 2;
+    if (!DRAIN && ctas > device_info().sm_count && 2 * stage + kOverhead <= 111 * 1024) q.stages = 2;
     const int smem = 1024 + std::max(q.stages * stage, q.n * (kCols + 4) * 4) + kBars;
     static std::atomic<unsigned long long> done{0};
-    e = allow_smem(lora_wgrad_tc_kernel<TERMS, BF16>, done, 227 * 1024);
+    e = allow_smem(lora_wgrad_tc_kernel<TERMS, BF16, DRAIN>, done, 227 * 1024);
     if (e != cudaSuccess) return e;
-    return launch_cluster(lora_wgrad_tc_kernel<TERMS, BF16>, dim3(static_cast<unsigned>(q.tiles[0] + q.tiles[1]) * q.cs, p.na), dim3(kWgThreads), smem, s, q.cs,
+    return launch_cluster(lora_wgrad_tc_kernel<TERMS, BF16, DRAIN>, dim3(static_cast<unsigned>(q.tiles[0] + q.tiles[1]) * q.cs, p.na), dim3(kWgThreads), smem, s, q.cs,
                           maps[0], maps[1], maps[2], q);
 }
 
@@ -561,10 +634,10 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     q.cols[1] = p.N;
     for (int w = 0; w < 2; ++w) q.tiles[w] = (q.cols[w] + kCols - 1) / kCols;
     q.fault = fault_word();
-    // Two CTAs an SM, while each still has four steps.
+    // All CTAs resident at once (fp32 gradients: one an SM, else two), while each still has four steps.
     const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * p.na;
     q.cs = 1;
-    while (q.cs < 8 && ctas * q.cs * 2 <= 2 * device_info().sm_count && p.T / p.na >= 8 * kStep * q.cs) q.cs *= 2;
+    while (q.cs < 8 && ctas * q.cs * 2 <= (q.g_dtype == kF32 ? 1 : 2) * device_info().sm_count && p.T / p.na >= 8 * kStep * q.cs) q.cs *= 2;
     CUtensorMap maps[3];
     const cuuint32_t box[3] = {64, kStep, 1};
     for (int w = 0; w < 2; ++w) {
@@ -583,8 +656,9 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     c.tile_max = q.tile_max;
     c.tile_adapter = q.tile_adapter;
     c.parts = q.parts;
-    if (nt == 3) return launch_wgrad_terms<3, true>(q, c, maps, s);
-    return bf16 ? launch_wgrad_terms<2, true>(q, c, maps, s) : launch_wgrad_terms<2, false>(q, c, maps, s);
+    if (nt == 3) return launch_wgrad_terms<3, true, true>(q, c, maps, s);
+    if (bf16) return launch_wgrad_terms<2, true, false>(q, c, maps, s);
+    return q.g_dtype == kF32 ? launch_wgrad_terms<2, false, true>(q, c, maps, s) : launch_wgrad_terms<2, false, false>(q, c, maps, s);
 }
 
 }  // namespace qg

@@ -13,8 +13,8 @@ cudaError_t launch_one(WgradArgs q, cudaStream_t s) {
     const LoraProblem &p = q.p;
     for (int w = 0; w < 2; ++w) q.tiles[w] = (q.cols[w] + Kern::COLS - 1) / Kern::COLS;
     const int chunks = (p.r + Kern::RJ - 1) / Kern::RJ;
-    // As many CTAs as are resident at once (rank > 32: one an SM, else two), while each still has two row chunks.
-    const int slots = device_info().sm_count * (MJ == 4 ? 1 : 2);
+    // As many CTAs as are resident at once (rank > 16: one an SM, else two), while each still has two row chunks.
+    const int slots = device_info().sm_count * (MJ > 1 ? 1 : 2);
     const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * p.na * chunks;
     q.cs = 1;
     while (q.cs < 8 && ctas * q.cs * 2 <= slots && p.T / p.na > 2 * kWgChunk * q.cs) q.cs *= 2;

@@ -34,7 +34,7 @@ constexpr int kWgChunk = 64;  // rows staged at a time
 // XT: type of the wide matrix; NATIVE: bf16 MMAs; MJ: 16-row groups of the rank
 template <int XT, bool NATIVE, int MJ>
 struct WgradKernel {
-    static constexpr int CPL = (XT == kF32 || MJ > 1) ? 4 : 8;   // columns of a lane
+    static constexpr int CPL = NATIVE && MJ == 1 ? 8 : 4;            // columns of a lane
     static constexpr int WCOLS = 8 * CPL, COLS = 8 * WCOLS;      // of a warp, of a CTA
     static constexpr int RJ = 16 * MJ;
     static constexpr int QBYTES = RJ * kWgChunk * (NATIVE ? 2 : 4);    // one term of the staged factor, [j][t]
@@ -126,7 +126,9 @@ struct WgradKernel {
         }
         if (__syncthreads_or(bad)) return;  // the whole cluster
 
-        float acc[MJ][CPL][4] = {};
+        // The MMAs add into `acc` with truncation; a chunk's sums are then added to
+        // `total` with rounding, so the error does not grow with the rows.
+        float acc[MJ][CPL][4], total[MJ][CPL][4] = {};
         float stage[QPT];
         auto fetch = [&](int t0, int rows) {
 #pragma unroll
@@ -184,6 +186,12 @@ struct WgradKernel {
             more = advance(p, a, q.cs, w, t0, rows);
             if (more) fetch(t0, rows);
             const unsigned char *hi = sm + 2 * b * QBYTES, *lo = hi + QBYTES;
+#pragma unroll
+            for (int m = 0; m < MJ; ++m)
+#pragma unroll
+                for (int i = 0; i < CPL; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.f;
 #pragma unroll 1
             for (int st = 0; st < kWgChunk && st < cr; st += 32) {
                 ahead(slot == 0 ? STAGES - 1 : slot - 1);
@@ -269,6 +277,12 @@ struct WgradKernel {
                     }
                 }
             }
+#pragma unroll
+            for (int m = 0; m < MJ; ++m)
+#pragma unroll
+                for (int i = 0; i < CPL; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) total[m][i][e] += acc[m][i][e];
         }
         // ------------------------------------------------------------------ sums of the cluster, and out
         queue_wait<0>();
@@ -280,7 +294,7 @@ struct WgradKernel {
             for (int i = 0; i < CPL; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    sums[(m * 16 + (e >> 1) * 8 + g) * OS + warp * WCOLS + (2 * c + (e & 1)) * CPL + i] = acc[m][i][e];
+                    sums[(m * 16 + (e >> 1) * 8 + g) * OS + warp * WCOLS + (2 * c + (e & 1)) * CPL + i] = total[m][i][e];
         __syncthreads();
         if (q.cs > 1) {
             cluster_arrive();
@@ -311,7 +325,7 @@ struct WgradKernel {
 };
 
 template <int XT, bool NATIVE, int MJ>
-__global__ void __launch_bounds__(256, MJ == 4 ? 1 : 2) lora_wgrad_kernel(const WgradArgs q) {
+__global__ void __launch_bounds__(256, MJ > 1 ? 1 : 2) lora_wgrad_kernel(const WgradArgs q) {
     WgradKernel<XT, NATIVE, MJ>::run(q);
 }
 

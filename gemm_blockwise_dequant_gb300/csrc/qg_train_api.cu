@@ -14,7 +14,8 @@ int64_t esize(int d) { return d == QG_F32 ? 4 : 2; }
 
 // as the GEMM entry points: larger sizes are not implemented (32-bit row and column indexes)
 constexpr int kMaxRows = 1 << 20, kMaxN = 1 << 28, kMaxK = 1 << 24;
-constexpr int kMaxSegments = 1 << 20, kMaxAdapters = 65535, kMaxRank = 128;
+// Every CTA looks its rows up in the whole list of requests: more of them would take longer to find than to serve.
+constexpr int kMaxSegments = 1 << 16, kMaxAdapters = 65535, kMaxRank = 128;
 
 int finish(cudaError_t e) {
     if (e == cudaErrorNotSupported) return QG_ERR_UNSUPPORTED;

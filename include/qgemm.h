@@ -439,6 +439,7 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
  * compute nothing and set *status_dev to 1; an adapter id at or past
  * num_adapters counts as none and sets it too.  status_dev may be NULL and is
  * never cleared.  Rows at or past offs[num_segments] are left untouched.
+ * At most 65536 requests and 65535 adapters a call (QG_ERR_UNSUPPORTED).
  *
  * qg_lora_apply -- for every row t of a request with adapter a
  *   V[t][j] = sum_k X[t][k] * A[a][j][k]                        (fp32)

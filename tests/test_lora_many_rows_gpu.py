@@ -116,3 +116,45 @@ def test_offsets_that_break_the_rule_compute_nothing(qg):
                         dA, dB, status=status)
         assert int(status) == 1 and bool(dX.isnan().all()) and bool((dA == 7).all()) and bool((dB == 7).all())
     assert qg.qg_read_device_fault() == 0
+
+
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_more_rows_than_a_grid_dimension(qg, x):
+    c = lora_case([40000, 0, 25000, 5500], [0, 1, -1, 1], na=2, r=8, N=24, K=32, x=x, seed=29)
+    check_apply(qg, c, c["Yin"].to(DT[x]), DT[x])
+    check_grad(qg, c, forward_v(c), c["dXin"], torch.float32)
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_offsets_beyond_32_bits(qg, x):
+    """Rows 2^24 values apart: the last ones lie past 2^32 bytes and values."""
+    T, ld = 300, 1 << 24
+    big = torch.empty(T * ld, dtype=DT[x], device="cuda").view(T, ld)
+    c = lora_case([250, 50], [0, 1], na=2, r=16, N=40, K=64, x=x, seed=30)
+    for name, at in (("X", 0), ("dY", 128), ("dXin", 256)):
+        part = big[:, at:at + c[name].shape[1]]
+        part.copy_(c[name])
+        c[name] = part
+    check_apply(qg, c, None, DT[x])
+    V = forward_v(c)
+    dA, dB = torch.empty_like(c["A"]), torch.empty_like(c["B"])
+    dX = big[:, 512:576]
+    qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], c["dXin"], dX, dA, dB)
+    (wx, wa, wb), (mx, ma, mb) = grad64(c, V, c["dXin"])
+    check(dX, wx, mx)
+    check(dA, wa, ma)
+    check(dB, wb, mb)
+
+
+def test_an_infinity_does_not_scale_the_others(qg):
+    """fp16: one infinite value of V must not push the other columns' values, far beyond fp16's range, over it."""
+    c = lora_case([200], [0], na=1, r=8, N=32, K=64, x="f16", seed=31)
+    V = forward_v(c) * 2.0 ** 20
+    V[7, 3] = float("inf")
+    dA, dB = torch.empty(1, 8, 64, device="cuda"), torch.empty(1, 32, 8, device="cuda")
+    qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], None, None, dA, dB)
+    (_, wa, wb), (_, ma, mb) = grad64(c, V, None)
+    keep = [j for j in range(8) if j != 3]
+    check(dA, wa, ma)
+    check(dB[:, :, keep], wb[:, :, keep], mb[:, :, keep])
+    assert not bool(torch.isfinite(dB[:, :, 3]).any())
