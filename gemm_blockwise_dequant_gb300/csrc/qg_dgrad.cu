@@ -21,8 +21,10 @@
 //  * The codes and parameters go from global memory straight into registers,
 //    one step ahead; only dY needs the TMA.
 //  * fp32 dY: dY and the weight are each split in two fp16 terms and three of
-//    their four products are added in the same accumulator (TERMS = 2; the
-//    product of the second terms, 2^-22, is left out).  A row of dY is first
+//    their four products are added (TERMS = 2; the product of the second terms,
+//    2^-22, is left out).  The MMAs add with truncation (about 1.5e-8 of a sum each
+//    time, measured), so every kDrain steps the accumulator is added to fp32 sums,
+//    with rounding, while the MMAs go on in a second one.  A row of dY is first
 //    scaled by a power of two, and all weights by one that their largest
 //    parameters give, so that neither term leaves fp16's range.
 //  * Tiles that do not fill a wave are split along n and their fp32 pieces added
@@ -50,6 +52,7 @@ constexpr int kThreads = 64 + 32 * kDequantWarps;  // warp 0 TMA, warp 1 MMA, th
 constexpr int kABytes = kRows * kBK * 2;
 constexpr int kWBytes = kBK * kCols * 2;
 constexpr int kBlockBytes = kBK * 128;             // one 64-column block of the B operand
+constexpr int kDrain = 4;       // TERMS = 2: steps of one accumulator
 constexpr int kSmemFixed = 1024 + 512 + 2048;      // alignment, barriers, codebook table
 constexpr int kSmemBudget = 227 * 1024;
 
@@ -126,7 +129,7 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One arrival on the same barrier of CTA 0 of the cluster.
+// One arrival on the same barrier of CTA 0 of the cluster (a pair).
 __device__ __forceinline__ void arrive_leader(uint64_t *bar) {
     asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(
                      smem_u32(bar))
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
     constexpr int NA = a_slots(H, TERMS), NW = w_bufs(TERMS);
     constexpr int AT = H * TERMS * kABytes, WT = TERMS * kWBytes;  // of a step
     constexpr int BN = PAIR * kCols;
-    constexpr uint32_t TMEM_COLS = H * BN;
+    constexpr uint32_t TMEM_COLS = H * TERMS * BN;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *a_s = smem, *w_s = a_s + NA * AT;
@@ -333,11 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
     uint64_t *wfull = aempty + NA;   // weights of a step written (one arrival a warp)
     uint64_t *wempty = wfull + NW;   // their MMAs are done
     uint64_t *pfull = wempty + NW;   // (leader) the other CTA's dY and weights of a step are there
-    uint64_t *accf = pfull + NW;     // every MMA of the tile is done
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
+    uint64_t *accf = pfull + NW;     // every MMA of the tile (TERMS = 2: of one of two accumulators) is done
+    uint64_t *drained = accf + 2;    // (leader; TERMS = 2) every warp of the pair has taken an accumulator's sums
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *lut = reinterpret_cast<float *>(w_s + NW * WT + 512);  // 16 x 32 (codebook)
-    static_assert((2 * NA + 3 * NW + 1) * 8 + 8 <= 512, "barriers fit");
+    static_assert((2 * NA + 3 * NW + 4) * 8 + 8 <= 512, "barriers fit");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
@@ -366,7 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
             mbar_init(&wempty[i], 1);
             mbar_init(&pfull[i], 1);
         }
-        mbar_init(accf, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&drained[i], kDequantWarps * PAIR);
+        }
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -412,6 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
                     continue;
                 }
                 if (PAIR == 2) ok = mbar_wait_cluster(&pfull[b], (i / NW) & 1, abort_flag, p.fault, FAULT_WAIT_TC);
+                const int blk = TERMS == 2 ? i / kDrain : 0, buf = blk & 1;
+                const bool fresh = TERMS == 2 ? i % kDrain == 0 : i == 0;
+                if (TERMS == 2 && fresh) ok = ok && mbar_wait_cluster(&drained[buf], ((blk >> 1) & 1) ^ 1, abort_flag, p.fault, FAULT_WAIT_TC);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ad = sdesc_k128(smem_u32(a_s + s * AT));
@@ -419,18 +429,20 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
                 const uint64_t bd = sdesc_mn128(smem_u32(w_s + b * WT));
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k) {  // 16 n: 32 bytes along A's rows, two 8-row groups of B
-                    mma<PAIR>(tmem, ad + 2 * k, bd + 128 * k, idesc, (i | k) != 0);
+                    const uint32_t acc = tmem + buf * BN, add = !fresh || k > 0;
+                    mma<PAIR>(acc, ad + 2 * k, bd + 128 * k, idesc, add);
                     if constexpr (TERMS == 2) {
-                        mma<PAIR>(tmem, ad + 2 * k, bd + (kWBytes >> 4) + 128 * k, idesc, 1);
-                        mma<PAIR>(tmem, ad1 + 2 * k, bd + 128 * k, idesc, 1);
+                        mma<PAIR>(acc, ad + 2 * k, bd + (kWBytes >> 4) + 128 * k, idesc, 1);
+                        mma<PAIR>(acc, ad1 + 2 * k, bd + 128 * k, idesc, 1);
                     } else if (two) {
-                        mma<PAIR>(tmem + BN, ad1 + 2 * k, bd + 128 * k, idesc, (i | k) != 0);
+                        mma<PAIR>(tmem + BN, ad1 + 2 * k, bd + 128 * k, idesc, add);
                     }
                 }
                 commit<PAIR>(&aempty[s]);
                 commit<PAIR>(&wempty[b]);
+                if (TERMS == 2 && (i % kDrain == kDrain - 1 || i == ns - 1)) commit<PAIR>(&accf[buf]);
             }
-            if (rank == 0) commit<PAIR>(accf);
+            if (TERMS == 1 && rank == 0) commit<PAIR>(accf);
         }
     } else {
         // ---------------------------------------------------------------- dequant
@@ -477,11 +489,43 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
         };
         const float *lut_lane = lut + lane;
         const uint32_t zpu = __half_as_ushort(__float2half_rn(p.zpv)) * 0x10001u;
+        const int sub = warp & 3, cq = (warp - 2) >> 2;  // tensor-memory sub-partition; share of the columns
+        constexpr int CW = H * BN / (kDequantWarps / 4);
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+        float taken[TERMS == 2 ? CW : 1];  // TERMS = 2: the sums so far of this lane's row, CW columns
+        int blocks_taken = 0;
+        if constexpr (TERMS == 2)
+            for (int q = 0; q < CW; ++q) taken[q] = 0.f;
+        auto take = [&]() {
+            const int buf = blocks_taken & 1;
+            const bool here = mbar_wait(&accf[buf], (blocks_taken >> 1) & 1, abort_flag, p.fault, FAULT_WAIT_TC);
+            if (!__all_sync(0xffffffffu, here)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < CW; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(lane_addr + buf * BN + cq * CW + c, v);
+#pragma unroll
+                for (int q = 0; q < 32; ++q) taken[TERMS == 2 ? c + q : 0] += __uint_as_float(v[q]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR == 1) mbar_arrive(&drained[buf]);  // (its cluster is other CTAs of the tile)
+                else arrive_leader(&drained[buf]);
+            }
+            ++blocks_taken;
+            return true;
+        };
         float wscale = 1.f;
         if constexpr (TERMS == 2) wscale = exp2i(weight_exponent(p.maxima, WK == WK_CODEBOOK, BITS, zt, p.zpv));
         Task<BITS> next;
         load(group, next);
         for (int i = group; i < ns; i += kGroups) {
+            if constexpr (TERMS == 2) {
+                while (blocks_taken + 2 <= i / kDrain && ok) ok = take();  // the MMAs are at the other accumulator
+                if (!ok) break;
+            }
             Task<BITS> k = next;
             load(i + kGroups, next);
             const int b = i % NW;
@@ -546,15 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
             if (lane == 0) mbar_arrive(&wfull[b]);
         }
         // ---------------------------------------------------------------- epilogue
-        ok = mbar_wait(accf, 0, abort_flag, p.fault, FAULT_WAIT_TC);
+        if constexpr (TERMS == 2) {
+            while (blocks_taken * kDrain < ns && ok) ok = take();
+        } else {
+            ok = mbar_wait(accf, 0, abort_flag, p.fault, FAULT_WAIT_TC);
+        }
         tc_fence_after();
-        const int sub = warp & 3, cq = (warp - 2) >> 2;  // tensor-memory sub-partition; share of the columns
-        constexpr int CW = H * BN / (kDequantWarps / 4);
-        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
 #pragma unroll 1
         for (int cc = cq * CW; cc < (cq + 1) * CW; cc += 32) {
             uint32_t v[32];
-            tmem_ld32(lane_addr + cc, v);
+            if constexpr (TERMS == 1) tmem_ld32(lane_addr + cc, v);
             const int h = cc / BN, c0 = cc - h * BN;
             const int row = h * PAIR * kRows + rank * kRows + sub * 32 + lane, m = m0 + row, kc = k0 + c0;
             if (m >= p.M || kc >= p.K) continue;  // K is a multiple of 32: a column group is in or out
@@ -566,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
             if constexpr (TERMS == 2) {
                 const float rs = p.row_scale[m];
 #pragma unroll
-                for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * rs / wscale);
+                for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(taken[cc - cq * CW + q] * rs / wscale);
             }
             if (shared_tile) {
                 float4 *dst = reinterpret_cast<float4 *>(sums + row * SS + c0);
@@ -743,7 +788,7 @@ Plan make_plan(int dy_dtype, int M, int N, int K) {
         c.split_steps = (c.steps + sp - 1) / sp;
         c.splits = (c.steps + c.split_steps - 1) / c.split_steps;
     }
-    if (c.pair == 2 && c.splits > 1) c.partial_bytes = sizeof(float) * c.tail_tiles * c.splits * static_cast<size_t>(c.rows) * c.bn;
+    if (c.pair == 2 && c.splits > 1) c.partial_bytes = sizeof(float) * static_cast<size_t>(c.tail_tiles) * c.splits * static_cast<size_t>(c.rows) * c.bn;
     c.ld = (N + 7) / 8 * 8;
     if (c.ld != N || c.terms == 2) c.copy_bytes = (static_cast<size_t>(M) * c.ld * 2 + 255) / 256 * 256;
     c.front_bytes = c.terms * c.copy_bytes;

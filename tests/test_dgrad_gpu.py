@@ -123,6 +123,19 @@ def test_adjoint_of_the_forward_pass(qg, kind, zp):
     assert abs(float(left.sum() - right.sum())) <= 2.0 ** -18 * float((dY.double().abs() @ w.abs() * X.double().abs()).sum())
 
 
+@pytest.mark.parametrize("M", [40, 300])
+def test_long_sums(qg, M):
+    """Contractions of 8192 rows of the weight and more stay as exact as short ones."""
+    for N in (8192, 20000):
+        check(qg, M, N, 128, "u4", "tensor", x="f32", seed=20)
+        p, w = weight(N, 128, "nf4", "none", 64, 21)
+        dY = torch.randn(M, N, device="cuda")
+        dX = torch.empty(M, 128, device="cuda")
+        run(qg, p, dY, dX)
+        want = dY.double() @ w
+        assert float((dX.double() - want).norm()) <= 2e-6 * float(want.norm())  # 48 truncating additions of 1.5e-8, then fp32
+
+
 def test_special_values(qg):
     """Infinities and NaN of dY stay in their row; large and small rows keep their precision in fp32."""
     p, w = weight(64, 128, "u4", "tensor", 64, 12)
