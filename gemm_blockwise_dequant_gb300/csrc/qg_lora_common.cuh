@@ -1,9 +1,9 @@
 // qg_lora_common.cuh -- what the adapter kernels share: warp-level MMAs,
 // splitting of fp32 values into operand terms, and the tiles of the requests.
 //
-// Two kinds of products (mma.sync; both accumulate in fp32).  All of them wait
-// for memory, not for the tensor cores, and their operands come from global
-// memory straight into fragments: the order of a contraction is free as long
+// Two kinds of products (mma.sync; both accumulate in fp32).  Up to a rank of
+// about 32 they wait for memory and latency, not for the tensor cores, and their
+// operands come from global memory straight into fragments: the order of a contraction is free as long
 // as both operands share it, so a lane takes 16 contiguous bytes where the
 // fragment layout asks for scattered pairs.
 //  * NATIVE (16-bit activations and adapters of one type): m16n8k16.  An fp32

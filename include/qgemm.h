@@ -459,8 +459,9 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
  *                zeros); others QG_ERR_UNSUPPORTED
  *   K            a multiple of 8; X, A and B 16-byte aligned, ldx * the
  *                element size a multiple of 16.  N and the strides of Y are free.
- * Sums are fp32 (16-bit operands multiply exactly; with fp32 operands each
- * value is split in two TF32 terms, dropping less than 2^-21 of a product).
+ * Sums are fp32.  16-bit operands multiply exactly; an fp32 operand is split in
+ * two TF32 terms (22 bits), and V, for the second product with 16-bit adapters of
+ * 16-bit activations, in two terms of their type (bf16: 16 bits, fp16: 22).
  * Deterministic.  workspace: at least qg_lora_apply_workspace_bytes(rows,
  * num_segments, rank, N, K) bytes, 16-byte aligned (NULL when that is 0).
  *
@@ -500,7 +501,9 @@ int qg_lora_grad(const void *dY, int x_dtype, int64_t lddy, const void *X, int64
  *   dY   [M][N] contiguous, dy_dtype;  dX  [M][K] contiguous, dx_dtype; both
  *        16-byte aligned
  *   16-bit dY: the weight is rounded to dY's type before the product, as in
- *   the forward pass; fp32 accumulation, one rounding to dx_dtype.
+ *   the forward pass; fp32 dY: dY and the weight go in two scaled fp16 terms each
+ *   (22 bits).  fp32 accumulation, one rounding to dx_dtype.  3-bit codes run on
+ *   a plain fp32 kernel.
  *   workspace: at least qgemm_dgrad_workspace_bytes(dy_dtype, M, N, K, bits)
  *   bytes, 16-byte aligned (NULL when that is 0).
  * M == 0 or K == 0 is a no-op; N == 0 writes zeros.
