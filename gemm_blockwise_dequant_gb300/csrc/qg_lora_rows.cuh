@@ -240,13 +240,14 @@ struct RowsKernel {
     // them the warps' partial sums, later the operand fragments of the second
     // product and the queues of its base rows.
     static __host__ __device__ int rank_pad(int r) { return (r + UW - 1) / UW * UW; }
-    static __host__ __device__ int sums_bytes(int r) { return 2 * R * rank_pad(r) * 4 + R * 4; }
+    static __host__ __device__ int sums_bytes(int r) { return (GIVEN ? 1 : 2) * R * rank_pad(r) * 4 + R * 4; }
     static __host__ __device__ int frag_bytes(int r) { return (R / 16) * (rank_pad(r) / UW) * 2 * 512; }
     static constexpr int PART_BYTES = KG * R * PS * 4;
     static constexpr int IN_BYTES = 8 * STAGES * PIECES * 512;
     static constexpr int BW = NATIVE ? 1 : 2;       // 16-byte pieces of 8 base values in the activations' type
     static constexpr int BASE_PIECES = 2 * MT * BW;  // of a lane and group
-    static constexpr int BASE_BYTES = 8 * STAGES * BASE_PIECES * 512;
+    static constexpr bool PAIRS = GIVEN && BWD && NATIVE;         // 64 columns at a time (pair_groups)
+    static constexpr int BASE_BYTES = PAIRS ? 8 * 2 * 4 * MT * 512 : 8 * STAGES * BASE_PIECES * 512;
     static __host__ __device__ int queue_offset(int r) { return r > RC ? sums_bytes(r) : 0; }  // several passes: their sums stay
     static __host__ __device__ int smem_bytes(int r) {
         if (GIVEN) return sums_bytes(r) + frag_bytes(r) + BASE_BYTES;
@@ -259,7 +260,7 @@ struct RowsKernel {
         const LoraProblem &p = q.p;
         const int r = p.r, rp = rank_pad(r);
         float *mine = reinterpret_cast<float *>(sm);
-        float *whole = mine + R * rp;
+        float *whole = GIVEN ? mine : mine + R * rp;
         float *rscale = whole + R * rp;
         float *part = rscale + R;
         uint4 *frag = reinterpret_cast<uint4 *>(part);
@@ -491,7 +492,10 @@ struct RowsKernel {
             uint4 *queue = reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(frag) + frag_bytes(r)) + warp * (STAGES * BASE_PIECES * 32) + lane;
             int first = n_lo + kg;
             if (t.adapter >= 0 && q.out_vec && q.out_dtype == XT && (!q.base || q.base_dtype == XT) && units <= UM)
+            {
+                if constexpr (PAIRS) first = pair_groups(q, t, n_lo, n_hi, kg, row0, rg, g, c, lane, units, mul, frag, warp);
                 first = whole_groups(q, t, first, n_hi, row0, rg, g, c, lane, units, mul, frag, queue);
+            }
             // What is left: the columns that do not fill a group, other types, rows at odd addresses.
             // The base rows ahead of their sums, when they have the activations' type.
             const bool queued = q.base && q.out_vec && q.base_dtype == XT;
@@ -689,30 +693,119 @@ struct RowsKernel {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = acc[m][e >> 1][h * 2 + (e & 1)] * mul[m][h];
                     }
-                    if (!in[m][h]) continue;
-                    if constexpr (NATIVE) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if constexpr (XT == kF16) {
-                                const __half2 p = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
-                                v[e] = *reinterpret_cast<const uint32_t *>(&p);
-                            } else {
-                                const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
-                                v[e] = *reinterpret_cast<const uint32_t *>(&p);
-                            }
-                        }
-                        *reinterpret_cast<uint4 *>(o) = make_uint4(v[0], v[1], v[2], v[3]);
-                    } else {
-                        reinterpret_cast<float4 *>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
-                        reinterpret_cast<float4 *>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
-                    }
+                    if (in[m][h]) store_row(o, y);
                 }
             out += KG * 32 * XS;
             slot = slot == STAGES - 1 ? 0 : slot + 1;
         }
         queue_wait<0>();
         return b;
+    }
+
+    // The same over pairs of groups, in the backward pass: a lane takes 8 columns of
+    // each adapter row in one load and uses them all, and a row tile's fragments
+    // are read once for 64 columns.  Column (tile i, lane column q) is n0 + 8 q + i;
+    // a lane ends with 16 contiguous outputs.  Returns the first group left to this warp.
+    static __device__ __forceinline__ int pair_groups(const RowsArgs &q, const RowTile &t, int n_lo, int n_hi, int kg, int row0, int rg, int g, int c,
+                                                      int lane, int units, const float (&mul)[MT][2], const uint4 *frag, int warp) {
+        const int pairs = (min(n_hi, q.c2 / 32) - n_lo) / 2, r = q.p.r;
+        if (pairs <= 0) return n_lo + kg;
+        uint4 *queue = const_cast<uint4 *>(frag) + frag_bytes(r) / 16 + warp * (2 * 4 * MT * 32) + lane;
+        const size_t row = static_cast<size_t>(t.t0 + row0 + g);
+        const int col = (n_lo + 2 * kg) * 32;
+        const int64_t base_step = q.ld_base * 16, out_step = q.ld_out * 16;  // eight rows
+        const char *base = static_cast<const char *>(q.base) + (row * q.ld_base + col + c * 16) * 2;
+        char *out = static_cast<char *>(q.out) + (row * q.ld_out + col + c * 16) * 2;
+        const char *w2 = static_cast<const char *>(q.w2) + ((static_cast<size_t>(t.adapter) * r + c * EU) * q.c2 + col + g * 8) * 2;
+        const int64_t w_row = static_cast<int64_t>(q.c2) * 2;
+        bool in[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) in[m][h] = row0 + m * 16 + h * 8 + g < t.rows;
+        auto ahead = [&](int slot) {
+            if (q.base) {
+                const char *p = base;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h, p += base_step)
+#pragma unroll
+                        for (int o = 0; o < 2; ++o)
+                            queue_copy<16>(queue + (slot * 4 * MT + (m * 2 + h) * 2 + o) * 32, in[m][h] ? p + 16 * o : static_cast<const char *>(q.base), in[m][h]);
+                base += KG * 64 * 2;
+            }
+            queue_commit();
+        };
+        if (kg < pairs) ahead(0);
+        int slot = 0;
+        for (int b = kg; b < pairs; b += KG, slot ^= 1) {
+            if (b + KG < pairs) ahead(slot ^ 1);
+            else queue_commit();
+            float acc[MT][8][4] = {};
+            for (int u = 0; u < units; ++u) {
+                uint4 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = u * UW + c * EU < r ? __ldg(reinterpret_cast<const uint4 *>(w2 + (static_cast<int64_t>(u) * UW + e) * w_row)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int mt = rg * MT + m;
+                    const uint4 h = frag[((mt * units + u) * 2) * 32 + lane], l = frag[((mt * units + u) * 2 + 1) * 32 + lane];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
+                        const uint32_t b0 = __byte_perm(word(x[0], i >> 1), word(x[1], i >> 1), sel), b1 = __byte_perm(word(x[2], i >> 1), word(x[3], i >> 1), sel);
+                        mma16<XT>(acc[m][i], l.x, l.y, l.z, l.w, b0, b1);
+                        mma16<XT>(acc[m][i], h.x, h.y, h.z, h.w, b0, b1);
+                    }
+                }
+            }
+            w2 += KG * 64 * 2;
+            queue_wait<1>();
+            char *o = out;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h, o += out_step)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {  // columns 16 c + 8 part ..
+                        float y[8];
+                        if (q.base) {
+                            take_base(queue + (slot * 4 * MT + (m * 2 + h) * 2 + part) * 32, y);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = fmaf(acc[m][e][h * 2 + part], mul[m][h], y[e]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = acc[m][e][h * 2 + part] * mul[m][h];
+                        }
+                        if (in[m][h]) store_row(o + 16 * part, y);
+                    }
+            out += KG * 64 * 2;
+        }
+        queue_wait<0>();
+        return n_lo + 2 * pairs + kg;
+    }
+
+    // 8 values of the activations' type at a 16-byte boundary
+    static __device__ __forceinline__ void store_row(char *o, const float (&y)[8]) {
+        if constexpr (NATIVE) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (XT == kF16) {
+                    const __half2 p = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
+                    v[e] = *reinterpret_cast<const uint32_t *>(&p);
+                } else {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+                    v[e] = *reinterpret_cast<const uint32_t *>(&p);
+                }
+            }
+            *reinterpret_cast<uint4 *>(o) = make_uint4(v[0], v[1], v[2], v[3]);
+        } else {
+            reinterpret_cast<float4 *>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
+            reinterpret_cast<float4 *>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
+        }
     }
 
     // 8 base values of the activations' type from the lane's queue
