@@ -158,14 +158,21 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
     int parts = 0;
     int *tile_adapter = nullptr;
     float *tile_max = nullptr, *G = q.sums;
+    uint16_t *terms = nullptr;
+    const bool bf16 = a.x_dtype == kBF16;
     if (tc) {
         const int cs = two ? shrink_splits(a.p.T, a.p.S, a.p.N) : 1;
         parts = two ? shrink_tc_tiles(a.p.T, a.p.S) * cs : (a.p.T + kRowsTile - 1) / kRowsTile + a.p.S;
         tile_adapter = reinterpret_cast<int *>(static_cast<char *>(ws) + align256(static_cast<size_t>(a.p.T) * a.p.r * 4));
         tile_max = reinterpret_cast<float *>(tile_adapter + parts);
-        q.tile_adapter = tile_adapter;
-        q.tile_max = tile_max;
+        terms = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(tile_adapter) + align256(static_cast<size_t>(grad_parts(a.p.T, a.p.S)) * 12));
         q.V = a.V;
+        if (bf16) {
+            q.terms = {terms, wgrad_tc_terms(true, a.g_dtype), static_cast<size_t>(a.p.T) * a.p.r};
+        } else {
+            q.tile_adapter = tile_adapter;
+            q.tile_max = tile_max;
+        }
     }
     cudaError_t e = cudaSuccess;
     if (two) {
@@ -174,10 +181,11 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
         t.sums = G;
         t.V = a.V;
         t.bwd = 1;
-        t.bf16 = a.x_dtype == kBF16;
+        t.bf16 = bf16;
         t.cs = shrink_splits(a.p.T, a.p.S, a.p.N);
-        t.tile_adapter = tile_adapter;
-        t.tile_max = tile_max;
+        t.tile_adapter = q.tile_adapter;
+        t.tile_max = q.tile_max;
+        t.terms = q.terms;
         e = launch_shrink_tc(t, a.dY, a.lddy, a.p.B, s);
         q.given = G;
         q.sums = nullptr;
@@ -195,8 +203,7 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
         w.tile_max = tile_max;
         w.tile_adapter = tile_adapter;
         w.parts = parts;
-        uint16_t *terms = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(tile_adapter) + align256(static_cast<size_t>(grad_parts(a.p.T, a.p.S)) * 12));
-        e = launch_wgrad_tc(w, G, a.V, terms, a.X, a.ldx, a.dY, a.lddy, a.x_dtype == kBF16, s);
+        e = launch_wgrad_tc(w, G, a.V, terms, a.X, a.ldx, a.dY, a.lddy, bf16, s);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     WgradArgs w{};

@@ -134,6 +134,23 @@ __device__ __forceinline__ bool find_tile(const LoraProblem &p, int tile, int si
     return !bad;
 }
 
+// Where the 16-bit terms of G and V go: [G, V][terms][T][rank].
+struct TermsOut {
+    uint16_t *at;  // null: not wanted here
+    int terms;
+    size_t all;    // T * rank
+};
+
+// The bf16 terms of value `e` of G (which = 0) or V (1): 8 bits each; an infinity or NaN is its own first term.
+__device__ __forceinline__ void put_terms(const TermsOut &o, int which, size_t e, float x) {
+    for (int m = 0; m < o.terms; ++m) {
+        const uint16_t h = f2bf(x);
+        const float f = bf2f(h);
+        x = fabsf(f) < __int_as_float(0x7f800000) ? x - f : 0.f;
+        o.at[(static_cast<size_t>(which) * o.terms + m) * o.all + e] = h;
+    }
+}
+
 __device__ __forceinline__ float finite_abs(float x) {  // 0 for an infinity or NaN
     const float a = fabsf(x);
     return a < __int_as_float(0x7f800000) ? a : 0.f;

@@ -38,6 +38,7 @@ struct RowsArgs {
     float *tile_max;     // backward: [2][tiles] largest finite |G| and |V| of a tile's rows, and its adapter; or null
     int *tile_adapter;
     const float *V;
+    TermsOut terms;      // bf16, backward: the terms of G and V for dA and dB
     const float *given;  // the first product's sums where they are known, or null
     int cs;              // CTAs that share a tile: a cluster, unless the sums are given
     int in_vec, out_vec; // rows at 16-byte boundaries: vector accesses
@@ -412,7 +413,14 @@ struct RowsKernel {
                         else
                             s = mine[e];
                         if (BWD) s *= scale;
-                        if (q.sums && rank == 0 && row < t.rows) q.sums[static_cast<size_t>(t.t0 + row) * r + j] = s;
+                        if (q.sums && rank == 0 && row < t.rows) {
+                            const size_t at = static_cast<size_t>(t.t0 + row) * r + j;
+                            q.sums[at] = s;
+                            if (BWD && XT == kBF16 && q.terms.at) {
+                                put_terms(q.terms, 0, at, s);
+                                put_terms(q.terms, 1, at, __ldg(q.V + at));
+                            }
+                        }
                     }
                     whole[e] = s;
                     if (maxima) {

@@ -17,11 +17,12 @@
 //   wgrad     G or V, MN-major, 16-bit     X or dY, MN-major, 256 columns
 // (wgrad the other way round, the wide operand as A in two halves and N = the
 // rank, kept the tensor pipe busy for 116 cycles an MMA and was bound by it.)
-// The thin operand of wgrad is fp32.  A small kernel between the two splits G and
-// V once in two 16-bit terms (three for fp32 gradients of bf16 activations),
-// after scaling them, for fp16, by the power of two that the adapter's largest
-// value gives; done by every CTA of wgrad for itself, that work took longer than
-// its wide operand (125 us of 8192 x (4096 + 14336) bf16 at rank 64).
+// The thin operand of wgrad is fp32; it comes in two 16-bit terms (three for fp32
+// gradients of bf16 activations).  For bf16 whatever makes G writes them, of V
+// too; for fp16 a small kernel does, after scaling by the power of two that the
+// adapter's largest value gives.  Done by every CTA of wgrad for itself, that
+// work took longer than its wide operand (125 us of 8192 x (4096 + 14336) bf16 at
+// rank 64).
 #include <algorithm>
 #include <atomic>
 
@@ -208,8 +209,17 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
         s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
         const size_t at = static_cast<size_t>(t.t0 + row) * r + j;
         *reinterpret_cast<float4 *>(q.sums + at) = s;
+        if (q.terms.at) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(q.V + at));
+            const float g4[4] = {s.x, s.y, s.z, s.w}, v4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                put_terms(q.terms, 0, at + i, g4[i]);
+                put_terms(q.terms, 1, at + i, v4[i]);
+            }
+        }
         mx = fmaxf(mx, fmaxf(fmaxf(finite_abs(s.x), finite_abs(s.y)), fmaxf(finite_abs(s.z), finite_abs(s.w))));
-        if (q.V) {
+        if (q.tile_adapter) {
             const float4 v = __ldg(reinterpret_cast<const float4 *>(q.V + at));
             mv = fmaxf(mv, fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w))));
         }
@@ -253,8 +263,7 @@ __device__ __forceinline__ unsigned largest_of(const float *tile_max, const int 
     return *smax;
 }
 
-// G and V of a tile of rows as 16-bit terms [which][term][T][rank].
-template <int TERMS, bool BF16>
+// G and V of a tile of rows as two fp16 terms each, scaled for the tile's adapter.
 __global__ void __launch_bounds__(256) lora_terms_kernel(const TermsTc q) {
     __shared__ unsigned smax[2];
     const LoraProblem &p = q.p;
@@ -263,30 +272,20 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(const TermsTc q) {
     RowTile t;
     if (!find_tile(p, blockIdx.x, kTileRows, false, t) || t.rows == 0 || t.adapter < 0) return;
     const int which = blockIdx.y;
-    float up = 1.f;
-    if (!BF16) {
-        if (threadIdx.x == 0) smax[which] = 0;
-        __syncthreads();
-        up = exp2i(fp16_exponent(largest_of(q.tile_max, q.tile_adapter, q.parts, which, t.adapter, smax + which)));
-    }
+    if (threadIdx.x == 0) smax[which] = 0;
+    __syncthreads();
+    const float up = exp2i(fp16_exponent(largest_of(q.tile_max, q.tile_adapter, q.parts, which, t.adapter, smax + which)));
     const size_t all = static_cast<size_t>(p.T) * p.r, first = static_cast<size_t>(t.t0) * p.r;
     const float *src = q.skinny[which] + first;
-    uint16_t *dst = q.terms + which * TERMS * all + first;
+    uint16_t *dst = q.terms + which * 2 * all + first;
     for (int e = threadIdx.x * 4; e < t.rows * p.r; e += 1024) {
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + e));
-        float x[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
+        const float x[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
+        uint16_t hi[4], lo[4];
 #pragma unroll
-        for (int m = 0; m < TERMS; ++m) {
-            uint32_t w[2];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // the next 8 or 11 bits of each value; an infinity or NaN is its own first term
-                const uint16_t h = BF16 ? f2bf(x[k]) : f2h(x[k]);
-                const float f = BF16 ? bf2f(h) : h2f(h);
-                x[k] = fabsf(f) < __int_as_float(0x7f800000) ? x[k] - f : 0.f;
-                w[k >> 1] = (k & 1) ? w[k >> 1] | static_cast<uint32_t>(h) << 16 : h;
-            }
-            *reinterpret_cast<uint2 *>(dst + m * all + e) = make_uint2(w[0], w[1]);
-        }
+        for (int k = 0; k < 4; ++k) split16<kF16>(x[k], hi[k], lo[k]);
+        *reinterpret_cast<uint2 *>(dst + e) = make_uint2(pack2(hi[0], hi[1]), pack2(hi[2], hi[3]));
+        *reinterpret_cast<uint2 *>(dst + all + e) = make_uint2(pack2(lo[0], lo[1]), pack2(lo[2], lo[3]));
     }
 }
 
@@ -601,10 +600,8 @@ cudaError_t launch_shrink_tc(ShrinkTc q, const void *in, int64_t ld, const void 
 namespace {
 
 template <int TERMS, bool BF16, bool DRAIN>
-cudaError_t launch_wgrad_terms(WgradTc q, const TermsTc &c, const CUtensorMap *maps, cudaStream_t s) {
+cudaError_t launch_wgrad_terms(WgradTc q, const CUtensorMap *maps, cudaStream_t s) {
     const LoraProblem &p = q.p;
-    cudaError_t e = launch_pdl(lora_terms_kernel<TERMS, BF16>, dim3(static_cast<unsigned>(shrink_tc_tiles(p.T, p.S)), 2), dim3(256), 0, s, c);
-    if (e != cudaSuccess) return e;
     const int stage = kWideBytes + TERMS * (q.n > 64 ? 2 : 1) * kBlock;
     // More CTAs than SMs: two on an SM, with half the ring each, so that one's start and end run under the other's loads.
     constexpr int kOverhead = 1024 + kBars;
@@ -613,22 +610,22 @@ cudaError_t launch_wgrad_terms(WgradTc q, const TermsTc &c, const CUtensorMap *m
     if (!DRAIN && ctas > device_info().sm_count && 2 * stage + kOverhead <= 111 * 1024) q.stages = 2;
     const int smem = 1024 + std::max(q.stages * stage, q.n * (kCols + 4) * 4) + kBars;
     static std::atomic<unsigned long long> done{0};
-    e = allow_smem(lora_wgrad_tc_kernel<TERMS, BF16, DRAIN>, done, 227 * 1024);
+    const cudaError_t e = allow_smem(lora_wgrad_tc_kernel<TERMS, BF16, DRAIN>, done, 227 * 1024);
     if (e != cudaSuccess) return e;
     return launch_cluster(lora_wgrad_tc_kernel<TERMS, BF16, DRAIN>, dim3(static_cast<unsigned>(q.tiles[0] + q.tiles[1]) * q.cs, p.na), dim3(kWgThreads), smem, s, q.cs,
                           maps[0], maps[1], maps[2], q);
 }
 
-int terms_of(bool bf16, int g_dtype) { return bf16 && g_dtype == kF32 ? 3 : 2; }
-
 }  // namespace
+
+int wgrad_tc_terms(bool bf16, int g_dtype) { return bf16 && g_dtype == kF32 ? 3 : 2; }
 
 size_t wgrad_tc_terms_bytes(int T, int r) { return static_cast<size_t>(2) * 3 * T * r * 2; }
 
 cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t *terms, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16,
                             cudaStream_t s) {
     const LoraProblem &p = q.p;
-    const int nt = terms_of(bf16, q.g_dtype);
+    const int nt = wgrad_tc_terms(bf16, q.g_dtype);
     q.n = thin_cols(p.r);
     q.cols[0] = p.K;
     q.cols[1] = p.N;
@@ -648,6 +645,7 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.r), static_cast<cuuint64_t>(p.T), static_cast<cuuint64_t>(2 * nt)};
     const cuuint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
     if (!make_map(maps[2], bf16, terms, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (bf16) return nt == 3 ? launch_wgrad_terms<3, true, true>(q, maps, s) : launch_wgrad_terms<2, true, false>(q, maps, s);
     TermsTc c{};
     c.p = p;
     c.skinny[0] = G;
@@ -656,9 +654,9 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     c.tile_max = q.tile_max;
     c.tile_adapter = q.tile_adapter;
     c.parts = q.parts;
-    if (nt == 3) return launch_wgrad_terms<3, true, true>(q, c, maps, s);
-    if (bf16) return launch_wgrad_terms<2, true, false>(q, c, maps, s);
-    return q.g_dtype == kF32 ? launch_wgrad_terms<2, false, true>(q, c, maps, s) : launch_wgrad_terms<2, false, false>(q, c, maps, s);
+    const cudaError_t e = launch_pdl(lora_terms_kernel, dim3(static_cast<unsigned>(shrink_tc_tiles(p.T, p.S)), 2), dim3(256), 0, s, c);
+    if (e != cudaSuccess) return e;
+    return q.g_dtype == kF32 ? launch_wgrad_terms<2, false, true>(q, maps, s) : launch_wgrad_terms<2, false, false>(q, maps, s);
 }
 
 }  // namespace qg

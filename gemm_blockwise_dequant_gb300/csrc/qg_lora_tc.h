@@ -11,6 +11,7 @@ struct ShrinkTc {
     const float *V;          // backward: the forward pass's V, for its largest values
     float *tile_max;         // [2][CTAs]: largest sum and largest V of a CTA's rows; or null
     int *tile_adapter;       // [CTAs] or null
+    TermsOut terms;          // bf16, backward: the terms of G and V
     int bwd, bf16, cs;
     int n, steps, stages, w_bytes;  // filled in by the launch
     unsigned *fault;
@@ -40,6 +41,8 @@ bool lora_tc_available();
 int shrink_tc_tiles(int T, int S);
 cudaError_t launch_shrink_tc(ShrinkTc q, const void *in, int64_t ld, const void *w, cudaStream_t s);
 size_t wgrad_tc_terms_bytes(int T, int r);  // room for the 16-bit terms of G and V
+int wgrad_tc_terms(bool bf16, int g_dtype); // how many each
+// bf16: the terms are there; fp16: they are made from G and V with the tiles' largest values.
 cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t *terms, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16,
                             cudaStream_t s);
 
