@@ -41,14 +41,17 @@ bool rows16(const void *p, int64_t ld, int dtype) {  // rows at 16-byte boundari
 // while each has at least 256 values of a row to contract: 64 requests of one row
 // at 4096 -> 14336, rank 16, take 37.2 / 23.8 / 15.9 / 20.6 us with 1 / 2 / 4 / 8
 // CTAs a tile, one row 36 / 21.6 / 13.9 / 9.9 / 8.2 (16).  Clusters of 16 are few
-// at a time (256 rows: 15.2 us with them, 9.3 with 8).
-RowsPlan make_plan(int T, int S, int c1) {
+// at a time (256 rows: 15.2 us with them, 9.3 with 8).  In the backward pass of
+// 16-bit rows clusters of 8 pay only while a CTA has an SM to itself: 512 rows with
+// dA and dB take 24.7 us with 4 and 27.9 with 8 (fp32: 51.0 and 43.2; forward 11.3
+// and 10.5).
+RowsPlan make_plan(int T, int S, int c1, bool bwd16) {
     RowsPlan plan{};
     const int sms = device_info().sm_count;
     plan.tiles = (T + kRowsTile - 1) / kRowsTile + S;  // the most that any offsets can need
     const int real = std::max(T / kRowsTile, std::min(S, T));
     plan.cs = 1;
-    while (plan.cs < 16 && real * plan.cs * 2 <= (plan.cs < 8 ? 2 * sms : sms) && c1 >= 512 * plan.cs) plan.cs *= 2;
+    while (plan.cs < 16 && real * plan.cs * 2 <= (plan.cs < (bwd16 ? 4 : 8) ? 2 * sms : sms) && c1 >= 512 * plan.cs) plan.cs *= 2;
     return plan;
 }
 
@@ -79,7 +82,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 cudaError_t rows(const RowsArgs &args, int x_dtype, bool bwd, cudaStream_t s) {
     RowsArgs q = args;
-    const RowsPlan plan = q.given ? expand_plan(q.p.T, q.p.S, q.c2) : make_plan(q.p.T, q.p.S, std::max(q.c1, q.c2));
+    const RowsPlan plan = q.given ? expand_plan(q.p.T, q.p.S, q.c2) : make_plan(q.p.T, q.p.S, std::max(q.c1, q.c2), bwd && x_dtype != kF32);
     q.cs = plan.cs;
     if (x_dtype == kBF16) return launch_rows<kBF16, kBF16>(q, bwd, plan, s);
     if (x_dtype == kF16) return launch_rows<kF16, kF16>(q, bwd, plan, s);

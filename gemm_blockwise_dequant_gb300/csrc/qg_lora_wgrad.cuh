@@ -40,7 +40,7 @@ struct WgradKernel {
     static constexpr int QBYTES = RJ * kWgChunk * (NATIVE ? 2 : 4);    // one term of the staged factor, [j][t]
     static constexpr int OS = COLS + 4;                                // row stride of the sums
     static constexpr int PB = CPL * (XT == kF32 ? 4 : 2);              // bytes of a lane's piece of a row: 16 or 8
-    static constexpr int STAGES = XT == kF32 ? 2 : 3;
+    static constexpr int STAGES = XT == kF32 && MJ == 1 ? 2 : 3;       // two CTAs an SM at rank 16
     static constexpr int WIDE_BYTES = 8 * STAGES * 8 * 32 * PB;        // the lanes' queues: 8 rows a step
     static constexpr int SMEM = (4 * QBYTES + WIDE_BYTES > RJ * OS * 4) ? 4 * QBYTES + WIDE_BYTES : RJ * OS * 4;
     static constexpr int QPT = kWgChunk * RJ / 256;                    // staged values of a thread
