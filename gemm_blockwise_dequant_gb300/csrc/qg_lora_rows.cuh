@@ -606,8 +606,12 @@ struct RowsKernel {
                               : (static_cast<size_t>(t.adapter) * q.c2 + first * 32 + (g >> 1) * 8 + (g & 1)) * r + c * EU) * WS;
         const int64_t w_row = static_cast<int64_t>(BWD ? q.c2 : 2 * r) * WS, w_unit = static_cast<int64_t>(BWD ? static_cast<int64_t>(UW) * q.c2 : UW) * WS;
         const int w_group = KG * 32 * (BWD ? 1 : r) * WS;
-        uint32_t w[UM][4][2];
-        auto load = [&](const char *p) {
+        // The adapter's values come DEPTH groups of this warp ahead of their use (one
+        // 16-row tile takes 1 KB of them a group at rank 16: 64 requests of one row
+        // took 15.2 us with one group ahead).
+        constexpr int DEPTH = MT > 1 || UM > 2 ? 1 : UM == 2 ? 2 : 4;
+        uint32_t ring[DEPTH][UM][4][2];
+        auto load = [&](const char *p, uint32_t (&w)[UM][4][2]) {
 #pragma unroll
             for (int u = 0; u < UM; ++u) {
                 const bool jin = u * UW + c * EU < r;
@@ -673,38 +677,48 @@ struct RowsKernel {
             if (loaded < end) ahead(i);
             else queue_commit();
         }
-        constexpr bool EARLY = UM <= 4;  // the next group's adapter values while this one's rows are written
-        if (EARLY) load(w2);
+        constexpr bool EARLY = UM <= 4;  // else a group's values are loaded where they are used
+        if (EARLY) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d)
+                if (first + d * KG < end) load(w2 + d * w_group, ring[d]);
+        }
         int slot = 0, b = first;
-        for (; b < end; b += KG, loaded += KG) {
-            if (loaded < end) ahead(slot == 0 ? STAGES - 1 : slot - 1);
-            else queue_commit();
-            if (!EARLY) load(w2);
-            float acc[MT][4][4] = {};
+        while (b < end) {
 #pragma unroll
-            for (int u = 0; u < UM; ++u)
-                if (u < units) multiply(acc, frag, u, units, rg, lane, w[u]);
-            w2 += w_group;
-            if (EARLY && b + KG < end) load(w2);
-            queue_wait<STAGES - 1>();
-            char *o = out;
+            for (int d = 0; d < DEPTH; ++d) {
+                if (b >= end) break;
+                if (loaded < end) ahead(slot == 0 ? STAGES - 1 : slot - 1);
+                else queue_commit();
+                uint32_t (&w)[UM][4][2] = ring[d];
+                if (!EARLY) load(w2, w);
+                float acc[MT][4][4] = {};
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int u = 0; u < UM; ++u)
+                    if (u < units) multiply(acc, frag, u, units, rg, lane, w[u]);
+                if (EARLY && b + DEPTH * KG < end) load(w2 + DEPTH * w_group, w);
+                w2 += w_group;
+                queue_wait<STAGES - 1>();
+                char *o = out;
 #pragma unroll
-                for (int h = 0; h < 2; ++h, o += out_step) {
-                    float y[8];
-                    if (q.base) {
-                        take_base(queue + (slot * BASE_PIECES + (m * 2 + h) * BW) * 32, y);
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = fmaf(acc[m][e >> 1][h * 2 + (e & 1)], mul[m][h], y[e]);
-                    } else {
+                    for (int h = 0; h < 2; ++h, o += out_step) {
+                        float y[8];
+                        if (q.base) {
+                            take_base(queue + (slot * BASE_PIECES + (m * 2 + h) * BW) * 32, y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = acc[m][e >> 1][h * 2 + (e & 1)] * mul[m][h];
+                            for (int e = 0; e < 8; ++e) y[e] = fmaf(acc[m][e >> 1][h * 2 + (e & 1)], mul[m][h], y[e]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = acc[m][e >> 1][h * 2 + (e & 1)] * mul[m][h];
+                        }
+                        if (in[m][h]) store_row(o, y);
                     }
-                    if (in[m][h]) store_row(o, y);
-                }
-            out += KG * 32 * XS;
-            slot = slot == STAGES - 1 ? 0 : slot + 1;
+                out += KG * 32 * XS;
+                slot = slot == STAGES - 1 ? 0 : slot + 1;
+                b += KG, loaded += KG;
+            }
         }
         queue_wait<0>();
         return b;
