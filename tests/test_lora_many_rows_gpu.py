@@ -158,3 +158,20 @@ def test_an_infinity_does_not_scale_the_others(qg):
     check(dA, wa, ma)
     check(dB[:, :, keep], wb[:, :, keep], mb[:, :, keep])
     assert not bool(torch.isfinite(dB[:, :, 3]).any())
+
+
+@pytest.mark.parametrize("lens,r,N,K", [([1000, 30, 470], 64, 6001, 4096), ([33, 1, 300], 24, 523, 512), ([1] * 40, 8, 262, 1024)])
+@pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
+def test_outputs_of_odd_widths(qg, x, lens, r, N, K):
+    """Rows that begin at no 16-byte boundary: every type of base and output, in place, and rows without an adapter."""
+    c = lora_case(lens, [(i % 3) - 1 for i in range(len(lens))], na=2, r=r, N=N, K=K, x=x, seed=25, extra=3)
+    for y in {DT[x], torch.float32}:
+        for base in (None, c["Yin"], c["Yin"].to(y)):
+            check_apply(qg, c, base, y)
+    out = c["Yin"].to(DT[x])
+    keep = out.clone()
+    qg.qg_lora_apply(c["X"], c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], out, out)
+    wy, _, mag = apply64(c, keep)
+    n = c["off_host"][-1]
+    check(out[:n], wy[:n], mag[:n])
+    assert torch.equal(out[n:], keep[n:])
