@@ -33,9 +33,10 @@ bool two_launches(int T, int N, int K, int r) {
 
 size_t esize(int d) { return d == kF32 ? 4 : 2; }
 
-bool rows16(const void *p, int64_t ld, int dtype) {  // rows at 16-byte boundaries
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * static_cast<int64_t>(esize(dtype))) % 16 == 0;
+bool rows_at(unsigned bytes, const void *p, int64_t ld, int dtype) {  // all rows at such boundaries
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * static_cast<int64_t>(esize(dtype))) % bytes == 0;
 }
+bool rows16(const void *p, int64_t ld, int dtype) { return rows_at(16, p, ld, dtype); }
 
 // The cluster of a tile is as wide as leaves all CTAs resident at once, two an SM,
 // while each has at least 256 values of a row to contract: 64 requests of one row
@@ -112,6 +113,7 @@ cudaError_t lora_apply(const LoraApply &a, void *ws, cudaStream_t s) {
     q.ld_out = a.ldy;
     q.sums = a.V;
     q.in_vec = rows16(a.X, a.ldx, a.x_dtype);
+    q.in_words = rows_at(4, a.X, a.ldx, a.x_dtype);
     q.out_vec = rows16(a.Y, a.ldy, a.y_dtype) && (!a.Yin || rows16(a.Yin, a.ldyin, a.yin_dtype));
     if (two_launches(a.p.T, a.p.N, a.p.K, a.p.r) && tensor_cores(a.p, a.x_dtype, q.in_vec)) {
         ShrinkTc t{};
@@ -155,6 +157,7 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
     q.ld_out = a.lddx;
     q.sums = static_cast<float *>(ws);
     q.in_vec = rows16(a.dY, a.lddy, a.x_dtype);
+    q.in_words = rows_at(4, a.dY, a.lddy, a.x_dtype);
     q.out_vec = 1;
     const bool tc = a.p.T >= kTcGradRows && tensor_cores(a.p, a.x_dtype, q.in_vec),
                two = tc && two_launches(a.p.T, a.p.N, a.p.K, a.p.r);
@@ -219,6 +222,8 @@ cudaError_t lora_grad(const LoraGrad &a, void *ws, cudaStream_t s) {
     w.cols[1] = a.p.N;
     w.vec[0] = 1;
     w.vec[1] = q.in_vec;
+    w.words[0] = 1;
+    w.words[1] = q.in_words;
     w.skinny[0] = static_cast<const float *>(ws);
     w.skinny[1] = a.V;
     w.out[0] = a.dA;

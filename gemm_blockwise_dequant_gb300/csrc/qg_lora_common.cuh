@@ -167,6 +167,14 @@ __device__ __forceinline__ void queue_copy(void *dst, const void *src, bool in) 
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n), "n"(BYTES) : "memory");
 }
+// 16 bytes of a row (the values from k on, vw to a word) as four words; from value `end` on zeros.
+__device__ __forceinline__ void copy_words(void *dst, const char *row, int k, int vw, int end) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool in = k + e * vw < end;
+        queue_copy<4>(static_cast<char *>(dst) + 4 * e, row + (in ? static_cast<size_t>(k + e * vw) * (4 / vw) : 0), in);
+    }
+}
 __device__ __forceinline__ void queue_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void queue_wait() {

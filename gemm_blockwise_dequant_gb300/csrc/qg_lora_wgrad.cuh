@@ -23,7 +23,8 @@ struct WgradArgs {
     const void *wide[2];     // X, dY
     int64_t ld[2];
     int cols[2], tiles[2];   // K, N and their column tiles
-    int vec[2];
+    int vec[2];              // rows at 16-byte boundaries
+    int words[2];            // at 4-byte boundaries
     const float *skinny[2];  // G, V
     void *out[2];            // dA, dB
     int g_dtype, accumulate, cs;
@@ -96,6 +97,15 @@ struct WgradKernel {
         if (!in || col >= cols || (q.vec[which] && col + CPL <= cols)) {
             in = in && col < cols;
             queue_copy<PB>(dst, static_cast<const char *>(q.wide[which]) + (in ? at * (XT == kF32 ? 4 : 2) : 0), in);
+            return;
+        }
+        if (q.words[which] && (XT == kF32 || col + CPL <= cols || !(cols & 1))) {  // no word holds a value from past the end
+            constexpr int VW = XT == kF32 ? 1 : 2;
+#pragma unroll
+            for (int i = 0; i < CPL; i += VW) {
+                const bool win = col + i < cols;
+                queue_copy<4>(dst + i * (4 / VW), static_cast<const char *>(q.wide[which]) + (win ? (at + i) * (4 / VW) : 0), win);
+            }
             return;
         }
 #pragma unroll

@@ -175,3 +175,15 @@ def test_outputs_of_odd_widths(qg, x, lens, r, N, K):
     n = c["off_host"][-1]
     check(out[:n], wy[:n], mag[:n])
     assert torch.equal(out[n:], keep[n:])
+
+
+@pytest.mark.parametrize("lens,N,K,pad", [([300, 0, 211], 1001, 264, 0), ([300, 0, 211], 1002, 264, 0), ([40, 3], 331, 520, 1),
+                                          ([200, 9], 330, 520, 2), ([17], 6, 8, 0)])
+@pytest.mark.parametrize("x,r", [("bf16", 16), ("f16", 40), ("f32", 16), ("f32", 64)])
+def test_gradients_of_odd_widths(qg, x, r, lens, N, K, pad):
+    """Rows of dY that begin at 2-byte and 4-byte boundaries, with odd and even widths."""
+    c = lora_case(lens, [1, 0, 1][:len(lens)], na=2, r=r, N=N, K=K, x=x, seed=26, extra=2)
+    if pad:
+        c["dY"] = torch.nn.functional.pad(c["dY"], (0, pad), value=float("nan"))[:, :N]
+    for g in {DT[x], torch.float32}:
+        check_grad(qg, c, forward_v(c), c["dXin"], g)
