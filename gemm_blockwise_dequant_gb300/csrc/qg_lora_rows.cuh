@@ -254,7 +254,14 @@ struct RowsKernel {
     static constexpr int BW = NATIVE ? 1 : 2;       // 16-byte pieces of 8 base values in the activations' type
     static constexpr int BASE_PIECES = 2 * MT * BW;  // of a lane and group
     static constexpr bool PAIRS = GIVEN && BWD && NATIVE;         // 64 columns at a time (pair_groups)
-    static constexpr int BASE_BYTES = PAIRS ? 8 * 2 * 4 * MT * 512 : 8 * STAGES * BASE_PIECES * 512;
+    // Each of the 8 warps keeps its base rows in a region of its own, whichever loop it is at: warps go from one
+    // loop to the next without waiting for each other.
+    static constexpr int PAIR_PIECES = 4 * MT;      // of a lane and pair of groups, two stages
+    static constexpr int QUEUE_PIECES = PAIRS && 2 * PAIR_PIECES > STAGES * BASE_PIECES ? 2 * PAIR_PIECES : STAGES * BASE_PIECES;
+    static constexpr int BASE_BYTES = 8 * QUEUE_PIECES * 512;
+    static __device__ __forceinline__ uint4 *base_queue(uint4 *frag, int r, int warp, int lane) {
+        return frag + frag_bytes(r) / 16 + warp * (QUEUE_PIECES * 32) + lane;
+    }
     static __host__ __device__ int queue_offset(int r) { return r > RC ? sums_bytes(r) : 0; }  // several passes: their sums stay
     static __host__ __device__ int smem_bytes(int r) {
         if (GIVEN) return sums_bytes(r) + frag_bytes(r) + BASE_BYTES;
@@ -503,11 +510,11 @@ struct RowsKernel {
                     mul[m][h] = BWD ? 1.f : scale;
                     if (XT == kF16 && t.adapter >= 0) mul[m][h] *= rscale[row0 + m * 16 + h * 8 + g];
                 }
-            uint4 *queue = reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(frag) + frag_bytes(r)) + warp * (STAGES * BASE_PIECES * 32) + lane;
+            uint4 *queue = base_queue(frag, r, warp, lane);
             int first = n_lo + kg;
             if (t.adapter >= 0 && q.out_vec && q.out_dtype == XT && (!q.base || q.base_dtype == XT) && units <= UM)
             {
-                if constexpr (PAIRS) first = pair_groups(q, t, n_lo, n_hi, kg, row0, rg, g, c, lane, units, mul, frag, warp);
+                if constexpr (PAIRS) first = pair_groups(q, t, n_lo, n_hi, kg, row0, rg, g, c, lane, units, mul, frag, queue);
                 first = whole_groups(q, t, first, n_hi, row0, rg, g, c, lane, units, mul, frag, queue);
             }
             if constexpr (!BWD)
@@ -737,10 +744,9 @@ struct RowsKernel {
     // are read once for 64 columns.  Column (tile i, lane column q) is n0 + 8 q + i;
     // a lane ends with 16 contiguous outputs.  Returns the first group left to this warp.
     static __device__ __forceinline__ int pair_groups(const RowsArgs &q, const RowTile &t, int n_lo, int n_hi, int kg, int row0, int rg, int g, int c,
-                                                      int lane, int units, const float (&mul)[MT][2], const uint4 *frag, int warp) {
+                                                      int lane, int units, const float (&mul)[MT][2], const uint4 *frag, uint4 *queue) {
         const int pairs = (min(n_hi, q.c2 / 32) - n_lo) / 2, r = q.p.r;
         if (pairs <= 0) return n_lo + kg;
-        uint4 *queue = const_cast<uint4 *>(frag) + frag_bytes(r) / 16 + warp * (2 * 4 * MT * 32) + lane;
         const size_t row = static_cast<size_t>(t.t0 + row0 + g);
         const int col = (n_lo + 2 * kg) * 32;
         const int64_t base_step = q.ld_base * 16, out_step = q.ld_out * 16;  // eight rows
@@ -762,7 +768,7 @@ struct RowsKernel {
                     for (int h = 0; h < 2; ++h, p += base_step)
 #pragma unroll
                         for (int o = 0; o < 2; ++o)
-                            queue_copy<16>(queue + (slot * 4 * MT + (m * 2 + h) * 2 + o) * 32, in[m][h] ? p + 16 * o : static_cast<const char *>(q.base), in[m][h]);
+                            queue_copy<16>(queue + (slot * PAIR_PIECES + (m * 2 + h) * 2 + o) * 32, in[m][h] ? p + 16 * o : static_cast<const char *>(q.base), in[m][h]);
                 base += KG * 64 * 2;
             }
             queue_commit();
@@ -802,7 +808,7 @@ struct RowsKernel {
                     for (int part = 0; part < 2; ++part) {  // columns 16 c + 8 part ..
                         float y[8];
                         if (q.base) {
-                            take_base(queue + (slot * 4 * MT + (m * 2 + h) * 2 + part) * 32, y);
+                            take_base(queue + (slot * PAIR_PIECES + (m * 2 + h) * 2 + part) * 32, y);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) y[e] = fmaf(acc[m][e][h * 2 + part], mul[m][h], y[e]);
                         } else {
@@ -825,7 +831,7 @@ struct RowsKernel {
     static __device__ __forceinline__ int odd_groups(const RowsArgs &q, const RowTile &t, int first, int n_hi, int row0, int rg, int g, int c, int lane,
                                                      int units, const float (&mul)[MT][2], const uint4 *frag, float *stage) {
         constexpr int LS = 36;  // row stride: no bank conflicts either way
-        static_assert(MT * 16 * LS * 4 <= STAGES * BASE_PIECES * 512, "the stage lies in the warp's queue");
+        static_assert(MT * 16 * LS * 4 <= QUEUE_PIECES * 512, "the stage lies in the warp's queue");
         const int rows = t.rows - row0;
         const auto base_at = [&](int n) { return static_cast<size_t>(t.t0 + row0) * q.ld_base + n; };
         // four rows at a time, so that a tile of one row does not pay for sixteen
