@@ -1,0 +1,24 @@
+"""qg_lora_apply and qg_lora_grad at the ends of their ranges: no adapters, no outputs, single rows of odd strides, and sums over
+very many rows of one sign."""
+import pytest
+import torch
+
+from lora_util import DT, check, grad64, lora_case, scale_of
+from test_lora_gpu import check_apply, check_grad, forward_v, qg  # noqa: F401  (qg: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [1, 40, 2048])
+@pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
+def test_no_adapters_at_all(qg, x, T):
+    """Without an adapter there is nothing to add: Y is Y_in, V is zero and dX is dX_in, whatever the number of rows."""
+    c = lora_case([T // 2, T - T // 2], [-1, -1], na=1, r=64, N=8192, K=4096, x=x, seed=61)
+    c["A"], c["B"], c["scaling"] = c["A"][:0], c["B"][:0], None
+    base = c["Yin"].to(DT[x])
+    Y, V = torch.empty_like(base), torch.full((T, 64), float("nan"), device="cuda")
+    qg.qg_lora_apply(c["X"], c["offsets"], c["ids"], c["A"], c["B"], None, base, Y, V=V)
+    assert torch.equal(Y, base) and not V.any()
+    dX = torch.empty_like(c["dXin"])
+    qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], None, c["dXin"], dX, torch.empty_like(c["A"]), torch.empty_like(c["B"]))
+    assert torch.equal(dX, c["dXin"])
