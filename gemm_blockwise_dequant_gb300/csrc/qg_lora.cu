@@ -67,9 +67,9 @@ RowsPlan expand_plan(int T, int S, int c2) {
 }
 
 // 16-bit activations at 16-byte boundaries, not cut into small requests, and adapters
-// to read (the copies of a tensor without any cannot be set up; the row kernel needs none).
+// with outputs to read (copies of an empty tensor cannot be set up; the row kernel needs none).
 bool tensor_cores(const LoraProblem &p, int x_dtype, bool aligned) {
-    return x_dtype != kF32 && aligned && p.T / 128 >= p.S && p.na > 0 && lora_tc_available();
+    return x_dtype != kF32 && aligned && p.T / 128 >= p.S && p.na > 0 && p.N > 0 && lora_tc_available();
 }
 
 // CTAs that share a tile's contraction: enough for two an SM, of eight steps or more.

@@ -117,7 +117,7 @@ int qg_lora_apply(const void *X, int x_dtype, int64_t ldx, const int64_t *seg_of
 }
 
 size_t qg_lora_grad_workspace_bytes(int rows, int num_segments, int num_adapters, int rank, int N, int K) {
-    if (rows <= 0 || num_segments < 0 || num_adapters < 0 || rank <= 0 || N <= 0 || K <= 0) return 0;
+    if (rows <= 0 || num_segments < 0 || num_adapters < 0 || rank <= 0 || N < 0 || K <= 0) return 0;
     return qg::lora_grad_workspace_bytes(rows, num_segments, num_adapters, rank, N, K);
 }
 
@@ -133,17 +133,18 @@ int qg_lora_grad(const void *dY, int x_dtype, int64_t lddy, const void *X, int64
     if (!valid_dtype(g_dtype) || (accumulate != 0 && accumulate != 1)) return QG_ERR_INVALID_ARG;
     if (g_dtype != w_dtype && g_dtype != QG_F32) return QG_ERR_UNSUPPORTED;
     if (lddy < N || ldx < K || (dX && lddx < K) || (dX_in && !dX)) return QG_ERR_INVALID_ARG;
-    if (num_adapters > 0 && (!A || !B || !dA || !dB)) return QG_ERR_INVALID_ARG;
+    if (num_adapters > 0 && (!A || !dA || (N > 0 && (!B || !dB)))) return QG_ERR_INVALID_ARG;
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(dA, 16) || !aligned(dB, 16)) return QG_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (rows == 0 || N == 0 || num_segments == 0) {  // no row of any adapter: the gradients are zeros
+    if (rows == 0 || num_segments == 0) {  // no row of any adapter: the gradients are zeros
         if (accumulate || num_adapters == 0) return QG_OK;
         const size_t per = static_cast<size_t>(num_adapters) * rank * esize(g_dtype);
         if (cudaMemsetAsync(dA, 0, per * K, s) != cudaSuccess) return QG_ERR_CUDA;
         if (N > 0 && cudaMemsetAsync(dB, 0, per * N, s) != cudaSuccess) return QG_ERR_CUDA;
         return QG_OK;
     }
-    if (!dY || !X || !V || !aligned(dY, esize(x_dtype)) || !aligned(X, 16) || !aligned(V, 16)) return QG_ERR_INVALID_ARG;
+    // N == 0 goes on: its sums are empty, and dX is dX_in
+    if ((N > 0 && !dY) || !X || !V || !aligned(dY, esize(x_dtype)) || !aligned(X, 16) || !aligned(V, 16)) return QG_ERR_INVALID_ARG;
     if ((ldx * esize(x_dtype)) % 16 || (dX && (lddx * esize(x_dtype)) % 16)) return QG_ERR_INVALID_ARG;
     if (!aligned(dX, 16) || !aligned(dX_in, 16)) return QG_ERR_INVALID_ARG;
     st = check_workspace(workspace, workspace_bytes,

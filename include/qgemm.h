@@ -464,6 +464,7 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
  * 16-bit activations, in two terms of their type (bf16: 16 bits, fp16: 22).
  * Deterministic.  workspace: at least qg_lora_apply_workspace_bytes(rows,
  * num_segments, rank, N, K) bytes, 16-byte aligned (NULL when that is 0).
+ * rows == 0, N == 0 or num_segments == 0 is a no-op: V_out is not written either.
  *
  * qg_lora_grad -- the backward pass, given dY, X and the V of the forward pass:
  *   G[t][j]  = scaling[a] * sum_n dY[t][n] * B[a][n][j]         (fp32)
@@ -479,6 +480,9 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
  *   dA, dB       shapes of A and B; g_dtype: w_dtype or QG_F32; zero for an
  *                adapter without rows.  accumulate = 1 adds to their contents.
  *   workspace    at least qg_lora_grad_workspace_bytes(...) bytes, 16-byte aligned
+ * rows == 0 or num_segments == 0: dA and dB are zeros (or what they held), dX is
+ * not written.  N == 0: empty sums, so dX is dX_in and dA is zero; dY, B and dB
+ * may be NULL.
  */
 size_t qg_lora_apply_workspace_bytes(int rows, int num_segments, int rank, int N, int K);
 int qg_lora_apply(const void *X, int x_dtype, int64_t ldx, const int64_t *seg_offsets, const int32_t *seg_adapter,

@@ -22,3 +22,21 @@ def test_no_adapters_at_all(qg, x, T):
     dX = torch.empty_like(c["dXin"])
     qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], None, c["dXin"], dX, torch.empty_like(c["A"]), torch.empty_like(c["B"]))
     assert torch.equal(dX, c["dXin"])
+
+
+@pytest.mark.parametrize("T", [1, 40, 2048])
+@pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
+def test_gradient_of_no_outputs(qg, x, T):
+    """N = 0: the sums over outputs are empty, so dX is dX_in and dA is zero."""
+    c = lora_case([T], [0], na=2, r=64, N=0, K=32768, x=x, seed=62, extra=3)
+    V = torch.ones(T + 3, 64, device="cuda")
+    dX = torch.full_like(c["dXin"], float("nan"))
+    dA = torch.full(c["A"].shape, 5.0, device="cuda")
+    dB = torch.empty(c["B"].shape, device="cuda")
+    call = lambda base, out, **kw: qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], base, out, dA, dB, **kw)
+    call(None, None, accumulate=True)
+    assert bool((dA == 5).all())
+    call(c["dXin"], dX)
+    assert torch.equal(dX[:T], c["dXin"][:T]) and bool(dX[T:].isnan().all()) and not dA.any()
+    call(None, dX)
+    assert not dX[:T].any() and bool(dX[T:].isnan().all())
