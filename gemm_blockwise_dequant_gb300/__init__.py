@@ -422,7 +422,7 @@ def _rows2d(t, rows, cols, what):
     ld, step = t.stride() if t.dim() == 2 else (0, 0)
     if t.shape != (rows, cols) or (step != 1 and cols > 1):
         raise ValueError("%s: a tensor of %d rows of %d contiguous values is wanted" % (what, rows, cols))
-    return ld if rows > 1 or ld >= cols else cols  # the stride of a single row says nothing
+    return ld if rows > 1 else cols  # the stride of a single row says nothing
 
 
 def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter):

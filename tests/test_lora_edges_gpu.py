@@ -40,3 +40,21 @@ def test_gradient_of_no_outputs(qg, x, T):
     assert torch.equal(dX[:T], c["dXin"][:T]) and bool(dX[T:].isnan().all()) and not dA.any()
     call(None, dX)
     assert not dX[:T].any() and bool(dX[T:].isnan().all())
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
+def test_a_single_row_has_no_stride(qg, x):
+    """One row out of a matrix whose rows begin at odd places: what lies behind it is never read."""
+    c = lora_case([1], [1], na=2, r=16, N=72, K=64, x=x, seed=63)
+    odd = lambda t: torch.cat([t, torch.full((1, 5), float("nan"), dtype=t.dtype, device="cuda")], 1).repeat(3, 1)[:1, :t.shape[1]]
+    for name in ("X", "dY", "dXin"):
+        c[name] = odd(c[name])
+    assert c["X"].stride(0) == 69
+    check_apply(qg, c, odd(c["Yin"].to(DT[x])), DT[x])
+    V = forward_v(c)
+    (wx, wa, wb), (mx, ma, mb) = grad64(c, V, c["dXin"])
+    dX, dA, dB = torch.empty(1, 64, dtype=DT[x], device="cuda"), torch.empty_like(c["A"]), torch.empty_like(c["B"])
+    qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], c["dXin"], dX, dA, dB)
+    check(dX, wx, mx)
+    check(dA, wa, ma)
+    check(dB, wb, mb)
