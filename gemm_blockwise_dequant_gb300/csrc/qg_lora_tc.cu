@@ -325,7 +325,8 @@ struct StepWalk {
     }
 };
 
-// DRAIN: fp32 gradients.  One CTA an SM then, for two accumulators and the registers of the sums.
+// DRAIN: fp32 gradients, and 16-bit ones of very many rows (drained_wgrad).  One CTA an SM then, for two accumulators
+// and the registers of the sums.
 template <int TERMS, bool BF16, bool DRAIN>
 __global__ void __launch_bounds__(kWgThreads, DRAIN ? 1 : 2) lora_wgrad_tc_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap dy_map,
                                                                       const __grid_constant__ CUtensorMap thin_map, const WgradTc q) {
@@ -620,6 +621,13 @@ cudaError_t launch_wgrad_terms(WgradTc q, const CUtensorMap *maps, cudaStream_t 
 
 int wgrad_tc_terms(bool bf16, int g_dtype) { return bf16 && g_dtype == kF32 ? 3 : 2; }
 
+// Where dA and dB leave the truncating accumulator every few steps: fp32 gradients always; 16-bit ones, rounded
+// at the end, only where the bias would near that rounding.  Two terms are an MMA for every 8 rows, 1.5e-8 of the
+// sum each: 6e-5 at 32768 rows of one accumulator and 4.9e-4 at 262144, an eighth of fp16's and bf16's unit
+// roundoff.  (2^20 rows of one sign: 1.8e-3 without.)  It costs the second CTA of an SM: 203 against 225 us for
+// 16384 x (4096 + 14336) fp16 at rank 64, 550 against 729 for 131072 x (1024 + 4096) bf16.
+static bool drained_wgrad(bool bf16, int g_dtype, int rows) { return g_dtype == kF32 || rows > (bf16 ? 262144 : 32768); }
+
 size_t wgrad_tc_terms_bytes(int T, int r) { return static_cast<size_t>(2) * 3 * T * r * 2; }
 
 cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t *terms, const void *x, int64_t ldx, const void *dy, int64_t lddy, bool bf16,
@@ -631,10 +639,16 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     q.cols[1] = p.N;
     for (int w = 0; w < 2; ++w) q.tiles[w] = (q.cols[w] + kCols - 1) / kCols;
     q.fault = fault_word();
-    // All CTAs resident at once (fp32 gradients: one an SM, else two), while each still has four steps.
+    // All CTAs resident at once (drained: one an SM, else two), while each still has four steps.
     const int64_t ctas = static_cast<int64_t>(q.tiles[0] + q.tiles[1]) * p.na;
-    q.cs = 1;
-    while (q.cs < 8 && ctas * q.cs * 2 <= (q.g_dtype == kF32 ? 1 : 2) * device_info().sm_count && p.T / p.na >= 8 * kStep * q.cs) q.cs *= 2;
+    const auto cluster = [&](int per_sm) {
+        int cs = 1;
+        while (cs < 8 && ctas * cs * 2 <= per_sm * device_info().sm_count && p.T / p.na >= 8 * kStep * cs) cs *= 2;
+        return cs;
+    };
+    q.cs = cluster(2);
+    const bool drain = drained_wgrad(bf16, q.g_dtype, p.T / q.cs);
+    if (drain) q.cs = cluster(1);
     CUtensorMap maps[3];
     const cuuint32_t box[3] = {64, kStep, 1};
     for (int w = 0; w < 2; ++w) {
@@ -645,7 +659,9 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.r), static_cast<cuuint64_t>(p.T), static_cast<cuuint64_t>(2 * nt)};
     const cuuint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
     if (!make_map(maps[2], bf16, terms, 3, dims, strides, box)) return cudaErrorInvalidValue;
-    if (bf16) return nt == 3 ? launch_wgrad_terms<3, true, true>(q, maps, s) : launch_wgrad_terms<2, true, false>(q, maps, s);
+    if (bf16)
+        return nt == 3 ? launch_wgrad_terms<3, true, true>(q, maps, s)
+               : drain ? launch_wgrad_terms<2, true, true>(q, maps, s) : launch_wgrad_terms<2, true, false>(q, maps, s);
     TermsTc c{};
     c.p = p;
     c.skinny[0] = G;
@@ -656,7 +672,7 @@ cudaError_t launch_wgrad_tc(WgradTc q, const float *G, const float *V, uint16_t 
     c.parts = q.parts;
     const cudaError_t e = launch_pdl(lora_terms_kernel, dim3(static_cast<unsigned>(shrink_tc_tiles(p.T, p.S)), 2), dim3(256), 0, s, c);
     if (e != cudaSuccess) return e;
-    return q.g_dtype == kF32 ? launch_wgrad_terms<2, false, true>(q, maps, s) : launch_wgrad_terms<2, false, false>(q, maps, s);
+    return drain ? launch_wgrad_terms<2, false, true>(q, maps, s) : launch_wgrad_terms<2, false, false>(q, maps, s);
 }
 
 }  // namespace qg

@@ -58,3 +58,27 @@ def test_a_single_row_has_no_stride(qg, x):
     check(dX, wx, mx)
     check(dA, wa, ma)
     check(dB, wb, mb)
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_many_rows_of_one_sign(qg, x):
+    """2^20 rows whose products all have one sign, 16-bit gradients: random signs would hide an accumulator that rounds one way."""
+    T, na, r, n = 1 << 20, 64, 8, 512
+    g = torch.Generator(device="cuda").manual_seed(64)
+    pos = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).abs()
+    c = dict(T=T, N=n, K=n, r=r, na=na, lens=[T], ids_host=[5], off_host=[0, T], x=DT[x], w=DT[x])
+    c["X"], c["dY"] = pos(T, n).to(DT[x]), pos(T, n).to(DT[x])
+    c["A"], c["B"] = pos(na, r, n).to(DT[x]), pos(na, n, r, std=0.1).to(DT[x])
+    c["scaling"] = torch.full((na,), 2.0 ** -15, device="cuda")
+    c["offsets"], c["ids"] = torch.tensor([0, T], device="cuda"), torch.tensor([5], dtype=torch.int32, device="cuda")
+    V = pos(T, r)
+    dA, dB = torch.empty_like(c["A"]), torch.empty_like(c["B"])
+    qg.qg_lora_grad(c["dY"], c["X"], V, c["offsets"], c["ids"], c["A"], c["B"], c["scaling"], None, None, dA, dB)
+    s, dy = scale_of(c, 5), c["dY"].double()
+    wa = (s * (dy @ c["B"][5].double())).t() @ c["X"].double()
+    wb = s * (dy.t() @ V.double())
+    check(dA[5], wa, wa)
+    check(dB[5], wb, wb)
+    for d in (dA, dB):
+        d[5] = 0
+        assert not d.any()
