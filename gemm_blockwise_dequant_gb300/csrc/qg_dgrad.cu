@@ -68,7 +68,7 @@ struct DgradArgs {
     float *partial;
     int M, N, K, nb, lbs, steps, mt;
     int full_tiles, splits, split_steps;  // as TcArgs: whole tiles first, then the others split along n
-    const float *row_scale;  // TERMS = 2: what a row's sums are multiplied by, and the parameters' maxima
+    const float *row_scale;  // TERMS = 2: the power of two that undoes a row's scale, and the parameters' maxima
     const float *maxima;
     unsigned *fault;
 };
@@ -192,10 +192,10 @@ constexpr int smem_bytes(int h, int terms) {
 // ------------------------------------------------------------------ fp32 dY: scales and terms
 constexpr int kMaxBlocks = 64;  // CTAs that look for the parameters' maxima
 
-// 2^e that brings `largest` to [2^14, 2^15); 1 for 0, infinity and NaN.
+// 2^e that brings `largest` to [2^14, 2^15), or as near as 2^126 does; 1 for infinity and NaN.
 __device__ __forceinline__ int scale_exponent(float largest) {
     const int ef = static_cast<int>((__float_as_uint(largest) >> 23) & 0xFFu);
-    return ef == 0 || ef == 255 ? 0 : min(max(14 - (ef - 127), -100), 100);
+    return ef == 255 ? 0 : min(14 - (ef - 127), 126);
 }
 
 // CTAs 0 .. M-1 split a row of dY; the others find the largest |scale| (absmax) and |zero point|.
@@ -609,9 +609,12 @@ __global__ void __launch_bounds__(kThreads, 1) dgrad_kernel(const __grid_constan
                 for (int q = 0; q < 32; ++q) v[q] = 0;
             }
             if constexpr (TERMS == 2) {
-                const float rs = p.row_scale[m];
+                // The row's and the weights' powers of two are undone together, in two equal steps: one of them alone
+                // may leave fp32's range where the result does not.
+                const int e = static_cast<int>(__float_as_uint(p.row_scale[m]) >> 23) - static_cast<int>(__float_as_uint(wscale) >> 23);
+                const float half = exp2i(e / 2), rest = exp2i(e - e / 2);
 #pragma unroll
-                for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(taken[cc - cq * CW + q] * rs / wscale);
+                for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(taken[cc - cq * CW + q] * half * rest);
             }
             if (shared_tile) {
                 float4 *dst = reinterpret_cast<float4 *>(sums + row * SS + c0);
