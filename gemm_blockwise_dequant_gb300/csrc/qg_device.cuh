@@ -152,6 +152,12 @@ __device__ __forceinline__ float bf2f(uint16_t b) { return __uint_as_float(stati
 __device__ __forceinline__ uint16_t f2h(float f) { return __half_as_ushort(__float2half_rn(f)); }
 __device__ __forceinline__ uint16_t f2bf(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
+// |x|, but 0 for an infinity or NaN: for largest values that scales are taken from.
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a < __int_as_float(0x7f800000) ? a : 0.f;
+}
+
 // 2^e as a float for integer e in [-127, 127] (exact).
 __device__ __forceinline__ float exp2i(int e) {
     return e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : __uint_as_float(0x00400000u);

@@ -192,13 +192,13 @@ constexpr int smem_bytes(int h, int terms) {
 // ------------------------------------------------------------------ fp32 dY: scales and terms
 constexpr int kMaxBlocks = 64;  // CTAs that look for the parameters' maxima
 
-// 2^e that brings `largest` to [2^14, 2^15), or as near as 2^126 does; 1 for infinity and NaN.
+// 2^e that brings `largest` to [2^14, 2^15), or as near as 2^126 does.
 __device__ __forceinline__ int scale_exponent(float largest) {
-    const int ef = static_cast<int>((__float_as_uint(largest) >> 23) & 0xFFu);
-    return ef == 255 ? 0 : min(14 - (ef - 127), 126);
+    return min(14 - (static_cast<int>((__float_as_uint(largest) >> 23) & 0xFFu) - 127), 126);
 }
 
-// CTAs 0 .. M-1 split a row of dY; the others find the largest |scale| (absmax) and |zero point|.
+// CTAs 0 .. M-1 split a row of dY; the others find the largest |scale| (absmax) and |zero point|.  Of finite
+// values: one that is not must not decide the scale of the others.
 __global__ void __launch_bounds__(256) split_dy_kernel(const GemmProblem p, int ld, __half *__restrict__ hi, __half *__restrict__ lo,
                                                        float *__restrict__ row_scale, float *__restrict__ maxima) {
     __shared__ float red[2][8];
@@ -209,17 +209,17 @@ __global__ void __launch_bounds__(256) split_dy_kernel(const GemmProblem p, int 
     const float *dy = static_cast<const float *>(p.A) + static_cast<size_t>(blockIdx.x) * p.N;
     const bool row = static_cast<int>(blockIdx.x) < p.M;
     if (row) {
-        for (int n = tid; n < p.N; n += 256) mx = fmaxf(mx, fabsf(dy[n]));
+        for (int n = tid; n < p.N; n += 256) mx = fmaxf(mx, finite_abs(dy[n]));
     } else {
         const size_t total = static_cast<size_t>(p.N) * (p.K / p.bs);
         const size_t first = static_cast<size_t>(blockIdx.x - p.M) * 256 + tid, stride = kMaxBlocks * 256;
         if (p.kind == WK_CODEBOOK) {
-            for (size_t i = first; i < total; i += stride) mx = fmaxf(mx, fabsf(__ldg(p.absmax + i)));
-            if (tid < 16) mz = fabsf(__ldg(p.codebook + tid));
+            for (size_t i = first; i < total; i += stride) mx = fmaxf(mx, finite_abs(__ldg(p.absmax + i)));
+            if (tid < 16) mz = finite_abs(__ldg(p.codebook + tid));
         } else {
-            for (size_t i = first; i < total; i += stride) mx = fmaxf(mx, fabsf(h2f(__ldg(reinterpret_cast<const unsigned short *>(p.scales) + i))));
+            for (size_t i = first; i < total; i += stride) mx = fmaxf(mx, finite_abs(h2f(__ldg(reinterpret_cast<const unsigned short *>(p.scales) + i))));
             if (p.zp_mode == ZP_TENSOR)
-                for (size_t i = first; i < total; i += stride) mz = fmaxf(mz, fabsf(h2f(__ldg(reinterpret_cast<const unsigned short *>(p.zp) + i))));
+                for (size_t i = first; i < total; i += stride) mz = fmaxf(mz, finite_abs(h2f(__ldg(reinterpret_cast<const unsigned short *>(p.zp) + i))));
         }
     }
     for (int o = 16; o >= 1; o >>= 1) {

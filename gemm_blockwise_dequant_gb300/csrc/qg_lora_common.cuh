@@ -151,11 +151,6 @@ __device__ __forceinline__ void put_terms(const TermsOut &o, int which, size_t e
     }
 }
 
-__device__ __forceinline__ float finite_abs(float x) {  // 0 for an infinity or NaN
-    const float a = fabsf(x);
-    return a < __int_as_float(0x7f800000) ? a : 0.f;
-}
-
 // A lane's queue in shared memory.  A lane copies ahead exactly the bytes that it
 // will read itself, so nothing but its own cp.async groups has to be waited for,
 // and the loads in flight do not occupy registers.  What lies outside is written as zeros.
