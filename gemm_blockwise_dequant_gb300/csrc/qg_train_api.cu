@@ -191,6 +191,7 @@ int qgemm_nbits_uniform_zp_dgrad(const void *dY, int dy_dtype, const uint8_t *W,
                                  float uniform_zp, void *dX, int dx_dtype, int M, int N, int K, int bits,
                                  int block_size, void *workspace, size_t workspace_bytes, qg_stream_t stream) {
     (void)cudaGetLastError();
+    if (!(uniform_zp >= -65504.f && uniform_zp <= 65504.f)) return QG_ERR_INVALID_ARG;  // not a finite fp16 value
     qg::GemmProblem p{};
     p.kind = qg::WK_NBITS;
     p.scales = scales_f16;
