@@ -507,18 +507,24 @@ def qgemm_dgrad_workspace_bytes(dy_dtype: int, M: int, N: int, K: int, bits: int
     return lib().qgemm_dgrad_workspace_bytes(dy_dtype, M, N, K, bits)
 
 
-def _dgrad_sizes(dY, W, params, dX, bits, block_size):
-    M, N = dY.shape
-    K = dX.shape[1]
-    if not dY.is_contiguous() or not dX.is_contiguous() or dX.shape[0] != M or W.shape != (N, K * bits // 8) \
-            or params.shape[0] != N or (block_size > 0 and params.shape[1] != K // block_size):
+def _dgrad_sizes(dY, W, params, table, dX, bits, block_size, codebook=False):
+    """M, N, K; table: the zero points [N, K/block_size] or None, or the codebook [16]."""
+    torch = _torch()
+    (M, N), (mx, K), (nw, wb), (np, nb) = dY.shape, dX.shape, W.shape, params.shape
+    if mx != M or nw != N or np != N or wb != K * bits // 8 or (block_size > 0 and nb != K // block_size) or not dY.is_contiguous() \
+            or not dX.is_contiguous() or not W.is_contiguous() or not params.is_contiguous():
         raise ValueError("dY [M, N], W [N, K*bits/8], parameters [N, K/block_size] and dX [M, K], contiguous, are wanted")
+    wanted = torch.float32 if codebook else torch.float16
+    if W.dtype != torch.uint8 or params.dtype != wanted:
+        raise ValueError("W in uint8 and %s are wanted" % ("absmax in float32" if codebook else "scales in float16"))
+    if table is not None and (table.dtype != wanted or not table.is_contiguous() or (table.numel() != 16 if codebook else table.shape != (N, nb))):
+        raise ValueError("the codebook [16] in float32, or zero points in the scales' shape and type, contiguous, are wanted")
     return M, N, K
 
 
 def qgemm_nbits_dgrad(dY, W, scales, zero_points, dX, *, bits, block_size, workspace=None, stream=None, raw=False):
     """dX[M,K] = dY[M,N] . dequant(W)[N,K]: the gradient of the activations through the frozen weight of qgemm_nbits."""
-    M, N, K = _dgrad_sizes(dY, W, scales, dX, bits, block_size)
+    M, N, K = _dgrad_sizes(dY, W, scales, zero_points, dX, bits, block_size)
     L = lib()
     need = L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits) if workspace is None else 0
     st, wp, wb, _ = _stream_and_workspace(need, workspace, dY, stream)
@@ -529,7 +535,7 @@ def qgemm_nbits_dgrad(dY, W, scales, zero_points, dX, *, bits, block_size, works
 
 def qgemm_nbits_uniform_zp_dgrad(dY, W, scales, uniform_zp, dX, *, bits, block_size, workspace=None, stream=None, raw=False):
     """As qgemm_nbits_dgrad with every zero point equal to the scalar uniform_zp."""
-    M, N, K = _dgrad_sizes(dY, W, scales, dX, bits, block_size)
+    M, N, K = _dgrad_sizes(dY, W, scales, None, dX, bits, block_size)
     L = lib()
     need = L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, bits) if workspace is None else 0
     st, wp, wb, _ = _stream_and_workspace(need, workspace, dY, stream)
@@ -540,7 +546,7 @@ def qgemm_nbits_uniform_zp_dgrad(dY, W, scales, uniform_zp, dX, *, bits, block_s
 
 def qgemm_codebook4_dgrad(dY, W, codebook, absmax, dX, *, block_size, workspace=None, stream=None, raw=False):
     """dX = dY . (codebook[q] * absmax): the gradient of the activations through the frozen weight of qgemm_codebook4."""
-    M, N, K = _dgrad_sizes(dY, W, absmax, dX, 4, block_size)
+    M, N, K = _dgrad_sizes(dY, W, absmax, codebook, dX, 4, block_size, codebook=True)
     L = lib()
     need = L.qgemm_dgrad_workspace_bytes(_dtype_code(dY), M, N, K, 4) if workspace is None else 0
     st, wp, wb, _ = _stream_and_workspace(need, workspace, dY, stream)

@@ -20,3 +20,40 @@ def test_uniform_zero_points_as_in_the_forward_pass(qg, zp, sizes):
 def test_uniform_zero_points_at_the_ends(qg):
     for zp in (65504.0, -65504.0, 7.5):
         assert qg.lib().qgemm_nbits_uniform_zp_dgrad(P, qg.QG_F16, P, P, zp, P, qg.QG_F16, 0, 32, 64, 4, 32, None, 0, None) == qg.QG_OK
+
+
+def test_activation_gradient_operands(qg):
+    """Types, shapes and order of every operand: the library takes addresses, so nothing else would notice."""
+    import torch
+
+    M, N, K, bs = 4, 32, 128, 64
+    half, single = dict(dtype=torch.float16), dict(dtype=torch.float32)
+    good = dict(dY=torch.zeros(M, N), W=torch.zeros(N, K // 2, dtype=torch.uint8), scales=torch.zeros(N, K // bs, **half),
+                zp=torch.zeros(N, K // bs, **half), absmax=torch.zeros(N, K // bs, **single), codebook=torch.zeros(16, **single), dX=torch.zeros(M, K))
+    strided = lambda t: torch.zeros(t.shape[0], 2 * t.shape[1], dtype=t.dtype)[:, ::2]
+
+    def nbits(**o):
+        g = dict(good, **o)
+        qg.qgemm_nbits_dgrad(g["dY"], g["W"], g["scales"], g["zp"], g["dX"], bits=4, block_size=bs)
+
+    def uniform(**o):
+        g = dict(good, **o)
+        qg.qgemm_nbits_uniform_zp_dgrad(g["dY"], g["W"], g["scales"], 8.0, g["dX"], bits=4, block_size=bs)
+
+    def codebook(**o):
+        g = dict(good, **o)
+        qg.qgemm_codebook4_dgrad(g["dY"], g["W"], g["codebook"], g["absmax"], g["dX"], block_size=bs)
+
+    common = [dict(W=good["W"].int()), dict(W=strided(good["W"])), dict(W=good["W"][:-1]), dict(dY=strided(good["dY"])), dict(dX=strided(good["dX"]))]
+    for o in common + [dict(scales=good["scales"].float()), dict(scales=strided(good["scales"])), dict(scales=good["scales"].flatten()[:N]),
+                       dict(scales=good["scales"].bfloat16())]:
+        for f in (nbits, uniform):
+            with pytest.raises(ValueError):
+                f(**o)
+    for o in (dict(zp=good["zp"].float()), dict(zp=good["zp"].to(torch.uint8)), dict(zp=good["zp"][:, :1]), dict(zp=good["zp"][:-1]), dict(zp=strided(good["zp"]))):
+        with pytest.raises(ValueError):
+            nbits(**o)
+    for o in common + [dict(absmax=good["absmax"].half()), dict(absmax=strided(good["absmax"])), dict(codebook=torch.zeros(15)),
+                       dict(codebook=torch.zeros(16, **half)), dict(codebook=torch.zeros(32)[::2])]:
+        with pytest.raises(ValueError):
+            codebook(**o)
