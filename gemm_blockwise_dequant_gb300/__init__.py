@@ -575,6 +575,8 @@ class QGGradList:
             raise ValueError("outs: one for each gradient is wanted")
         host = (_GradTensor * max(1, len(grads)))()
         for h, g, o in zip(host, grads, outs):
+            if not g.is_cuda or not o.is_cuda:
+                raise ValueError("gradients and outs: tensors of a GPU are wanted")
             if not g.is_contiguous() or not o.is_contiguous() or g.numel() != o.numel() or g.dtype != o.dtype:
                 raise ValueError("gradients and outs: contiguous tensors of one size and type are wanted")
             h.grad, h.out, h.numel, h.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g)
@@ -596,6 +598,8 @@ def qg_clip_grad_norm(grads, max_norm, norm, *, eps=1e-6, workspace=None, stream
     grads: a QGGradList, or a sequence of tensors (clipped in place; the list is then laid out in every call);
     norm: a float32 device tensor of one value.
     """
+    if norm.dtype != _torch().float32 or norm.numel() != 1 or not norm.is_cuda:
+        raise ValueError("norm: one float32 value of a GPU is wanted")
     if not isinstance(grads, QGGradList):
         grads = QGGradList(grads)
     st, wp, wb, _ = _stream_and_workspace(0, grads.workspace if workspace is None else workspace, grads.table, stream)

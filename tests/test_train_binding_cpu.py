@@ -57,3 +57,15 @@ def test_activation_gradient_operands(qg):
                        dict(codebook=torch.zeros(16, **half)), dict(codebook=torch.zeros(32)[::2])]:
         with pytest.raises(ValueError):
             codebook(**o)
+
+
+def test_clipping_operands(qg):
+    """The norm is written as one float32 value, and the list's addresses are followed on the device."""
+    import torch
+
+    empty = qg.QGGradList.__new__(qg.QGGradList)  # refused before anything of it is used
+    for norm in (torch.zeros(1, dtype=torch.float16), torch.zeros(1, dtype=torch.float64), torch.zeros(0), torch.zeros(2), torch.zeros(1)):
+        with pytest.raises(ValueError, match="norm"):
+            qg.qg_clip_grad_norm(empty, 1.0, norm)
+    with pytest.raises(ValueError, match="GPU"):
+        qg.QGGradList([torch.zeros(4)])
