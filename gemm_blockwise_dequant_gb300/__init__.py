@@ -425,8 +425,10 @@ def _rows2d(t, rows, cols, what):
     return ld if rows > 1 else cols  # the stride of a single row says nothing
 
 
-def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter):
+def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter, status):
     torch = _torch()
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status: an int32 is wanted")
     na, r, K = A.shape
     N = B.shape[1]
     if B.shape != (na, N, r) or A.dtype != B.dtype or not A.is_contiguous() or not B.is_contiguous():
@@ -454,7 +456,7 @@ def qg_lora_apply(X, seg_offsets, seg_adapter, A, B, scaling, Y_in, Y, *, V=None
     Y: [T, N]; V: [T, rank] float32 that receives X A^T for qg_lora_grad, or None; status: a device int32 or None.
     X, Y_in and Y may be column slices (rows apart, values contiguous).
     """
-    na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter)
+    na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter, status)
     T = X.shape[0]
     ldx, ldy = _rows2d(X, T, K, "X"), _rows2d(Y, T, N, "Y")
     yin = (None, 0, 0) if Y_in is None else (Y_in.data_ptr(), _dtype_code(Y_in), _rows2d(Y_in, T, N, "Y_in"))
@@ -481,7 +483,7 @@ def qg_lora_grad(dY, X, V, seg_offsets, seg_adapter, A, B, scaling, dX_in, dX, d
     (dX_in None for zeros or dX itself; dX None when no gradient of X is wanted); dA and dB: shapes of A and B, in
     their type or float32, zero for adapters without rows (accumulate: added to what they hold).
     """
-    na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter)
+    na, r, K, N, S = _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter, status)
     T = X.shape[0]
     xt = X.dtype
     if dY.dtype != xt or V.shape != (T, r) or V.dtype != _torch().float32 or not V.is_contiguous():

@@ -69,3 +69,17 @@ def test_clipping_operands(qg):
             qg.qg_clip_grad_norm(empty, 1.0, norm)
     with pytest.raises(ValueError, match="GPU"):
         qg.QGGradList([torch.zeros(4)])
+
+
+@pytest.mark.parametrize("status", ["uint8", "int64", "none"])
+def test_adapter_status(qg, status):
+    """The status is written as an int32."""
+    import torch
+
+    status = torch.zeros(0, dtype=torch.int32) if status == "none" else torch.zeros(1, dtype=getattr(torch, status))
+    X, Y, A, B, V = torch.zeros(4, 64), torch.zeros(4, 32), torch.zeros(1, 8, 64), torch.zeros(1, 32, 8), torch.zeros(4, 8)
+    off, ids = torch.tensor([0, 4]), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="status"):
+        qg.qg_lora_apply(X, off, ids, A, B, None, None, Y, status=status)
+    with pytest.raises(ValueError, match="status"):
+        qg.qg_lora_grad(Y, X, V, off, ids, A, B, None, None, None, torch.zeros_like(A), torch.zeros_like(B), status=status)
