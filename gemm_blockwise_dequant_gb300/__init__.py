@@ -162,6 +162,16 @@ def _check(status, where):
     return status
 
 
+def _empty_for(nbytes, device, stream):
+    """Scratch memory for one call on `stream` (None: the current one).  Memory of the stream's own: what it held before
+    is done with, and whoever gets it next comes later, in that stream's order -- no other stream's."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _workspace(need, workspace, device):
     """(workspace, its size in bytes): the caller's, else a new one of need()
     bytes (None when the call needs none); the library checks the size."""
@@ -404,16 +414,13 @@ def _addr(t):
 
 
 def _stream_and_workspace(need, workspace, t, stream):
-    """(raw stream, workspace address, its bytes, the workspace): on `stream`, or on the device's current one.
-    A workspace made here is not given away again before the work on `stream` that uses it is done."""
+    """(raw stream, workspace address, its bytes, the workspace): on `stream`, or on the device's current one."""
     raw = _torch()._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
     if workspace is not None:
         return raw, workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if not need:
         return raw, None, 0, None
-    workspace = _torch().empty(need, dtype=_torch().uint8, device=t.device)
-    if stream is not None:
-        workspace.record_stream(stream)
+    workspace = _empty_for(need, t.device, stream)
     return raw, workspace.data_ptr(), need, workspace
 
 

@@ -83,3 +83,61 @@ def test_adapter_status(qg, status):
         qg.qg_lora_apply(X, off, ids, A, B, None, None, Y, status=status)
     with pytest.raises(ValueError, match="status"):
         qg.qg_lora_grad(Y, X, V, off, ids, A, B, None, None, None, torch.zeros_like(A), torch.zeros_like(B), status=status)
+
+
+class FakeTorch:
+    """Stands in for torch where a call looks for scratch memory: records the stream that each piece is made on."""
+
+    uint8 = "uint8"
+
+    class Piece:
+        def __init__(self, nbytes, stream):
+            self.nbytes, self.stream = nbytes, stream
+
+        def data_ptr(self):
+            return P
+
+        def record_stream(self, stream):
+            pass
+
+    class Stream:
+        cuda_stream = 7
+
+    def __init__(self):
+        fake = self
+        self.now, self.made = "current", []
+
+        class Within:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                self.before, fake.now = fake.now, self.stream
+
+            def __exit__(self, *e):
+                fake.now = self.before
+
+        self.cuda = type("cuda", (), dict(stream=Within))
+        self._C = type("_C", (), dict(_cuda_getCurrentRawStream=staticmethod(lambda device: 3)))
+
+    def empty(self, nbytes, dtype, device):
+        self.made.append(self.Piece(nbytes, self.now))
+        return self.made[-1]
+
+
+class FakeTensor:
+    device = "cuda:0"
+
+    def get_device(self):
+        return 0
+
+
+def test_scratch_memory_belongs_to_the_stream_of_the_call(qg, monkeypatch):
+    """Memory of another stream's pool may still be in use there by an earlier call, and goes back there too early."""
+    fake, s = FakeTorch(), FakeTorch.Stream()
+    monkeypatch.setattr(qg, "_TORCH", fake)
+    raw, at, size, piece = qg._stream_and_workspace(64, None, FakeTensor(), s)
+    assert (raw, at, size, piece.stream, fake.now) == (7, P, 64, s, "current")
+    raw, at, size, piece = qg._stream_and_workspace(64, None, FakeTensor(), None)
+    assert (raw, at, size, piece.stream) == (3, P, 64, "current")
+    assert qg._stream_and_workspace(0, None, FakeTensor(), s)[1:] == (None, 0, None) and len(fake.made) == 2
