@@ -172,7 +172,7 @@ def _empty_for(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _workspace(need, workspace, device):
+def _workspace(need, workspace, device, stream):
     """(workspace, its size in bytes): the caller's, else a new one of need()
     bytes (None when the call needs none); the library checks the size."""
     if workspace is not None:
@@ -180,7 +180,7 @@ def _workspace(need, workspace, device):
     nbytes = need()
     if nbytes == 0:
         return None, 0
-    return _torch().empty(nbytes, dtype=_torch().uint8, device=device), nbytes
+    return _empty_for(nbytes, device, stream), nbytes
 
 
 def qgemm_workspace_bytes(a_dtype: int, M: int, N: int, K: int, bits: int, block_size: int) -> int:
@@ -195,7 +195,7 @@ def qgemm_nbits(A, W, scales, zero_points, Y, *, bits, block_size, workspace=Non
     """
     M, K = A.shape
     N = W.shape[0]
-    ws, wsb = _workspace(lambda: qgemm_workspace_bytes(_dtype_code(A), M, N, K, bits, block_size), workspace, A.device)
+    ws, wsb = _workspace(lambda: qgemm_workspace_bytes(_dtype_code(A), M, N, K, bits, block_size), workspace, A.device, stream)
     s = lib().qgemm_nbits(_ptr(A), _dtype_code(A), _ptr(W), _ptr(scales), _ptr(zero_points), _ptr(Y),
                           _dtype_code(Y), M, N, K, bits, block_size, _ptr(ws), wsb, _stream(stream))
     return s if raw else _check(s, "qgemm_nbits")
@@ -206,7 +206,7 @@ def qgemm_nbits_uniform_zp(A, W, scales, uniform_zp, Y, *, bits, block_size, wor
     """As qgemm_nbits with every zero point equal to the scalar uniform_zp."""
     M, K = A.shape
     N = W.shape[0]
-    ws, wsb = _workspace(lambda: qgemm_workspace_bytes(_dtype_code(A), M, N, K, bits, block_size), workspace, A.device)
+    ws, wsb = _workspace(lambda: qgemm_workspace_bytes(_dtype_code(A), M, N, K, bits, block_size), workspace, A.device, stream)
     s = lib().qgemm_nbits_uniform_zp(_ptr(A), _dtype_code(A), _ptr(W), _ptr(scales), float(uniform_zp), _ptr(Y),
                                      _dtype_code(Y), M, N, K, bits, block_size, _ptr(ws), wsb, _stream(stream))
     return s if raw else _check(s, "qgemm_nbits_uniform_zp")
@@ -216,7 +216,7 @@ def qgemm_codebook4(A, W, codebook, absmax, Y, *, block_size, workspace=None, st
     """Y = A . (codebook[q] * absmax)^T; codebook [16] float32, absmax [N, K/block_size] float32."""
     M, K = A.shape
     N = W.shape[0]
-    ws, wsb = _workspace(lambda: qgemm_workspace_bytes(_dtype_code(A), M, N, K, 4, block_size), workspace, A.device)
+    ws, wsb = _workspace(lambda: qgemm_workspace_bytes(_dtype_code(A), M, N, K, 4, block_size), workspace, A.device, stream)
     s = lib().qgemm_codebook4(_ptr(A), _dtype_code(A), _ptr(W), _ptr(codebook), _ptr(absmax), _ptr(Y),
                               _dtype_code(Y), M, N, K, block_size, _ptr(ws), wsb, _stream(stream))
     return s if raw else _check(s, "qgemm_codebook4")
@@ -233,7 +233,7 @@ def qmoe_decode_fused(x, expert_ids, expert_weights, *, num_experts, fc1_w, fc1_
     hidden = x.shape[-1]
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
-    ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device)
+    ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device, stream)
     s = lib().qmoe_decode_fused(_ptr(x), _ptr(expert_ids), _ptr(expert_weights), k, num_experts, _ptr(fc1_w),
                                 _ptr(fc1_scales), _ptr(fc1_zp), _ptr(fc1_bias), _ptr(fc2_w), _ptr(fc2_scales),
                                 _ptr(fc2_zp), _ptr(fc2_bias), hidden, inter, bits, block_size,
@@ -248,7 +248,7 @@ def qmoe_decode_fused_dp4a(x, expert_ids, expert_weights, *, num_experts, fc1_w,
     hidden = x.shape[-1]
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
-    ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device)
+    ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device, stream)
     s = lib().qmoe_decode_fused_dp4a(_ptr(x), _ptr(expert_ids), _ptr(expert_weights), k, num_experts, _ptr(fc1_w),
                                      _ptr(fc1_scales), _ptr(fc1_zp), _ptr(fc1_bias), _ptr(fc2_w), _ptr(fc2_scales),
                                      _ptr(fc2_zp), _ptr(fc2_bias), hidden, inter, bits, block_size,
@@ -273,9 +273,8 @@ def qmoe_decode_fused_noalloc(x, expert_ids, expert_weights, *, num_experts, fc1
 
 def qg_fp16_uniform_value(t, workspace=None, stream=None):
     """(is_uniform, value) for an fp16 tensor (bitwise equality of all elements)."""
-    torch = _torch()
     if workspace is None:
-        workspace = torch.empty(16, dtype=torch.uint8, device=t.device)
+        workspace = _empty_for(16, t.device, stream)
     u = ctypes.c_int(0)
     v = ctypes.c_float(0.0)
     _check(lib().qg_fp16_uniform_value(_ptr(t), t.numel(), ctypes.byref(u), ctypes.byref(v), _ptr(workspace),
@@ -315,7 +314,7 @@ def qgemm_codebook4_nested(A, W, codebook, absmax_q, absmax_table, absmax2, absm
     M, K = A.shape
     N = W.shape[0]
     ws, wsb = _workspace(lambda: qgemm_codebook4_nested_workspace_bytes(_dtype_code(A), M, N, K, block_size), workspace,
-                         A.device)
+                         A.device, stream)
     s = lib().qgemm_codebook4_nested(_ptr(A), _dtype_code(A), _ptr(W), _ptr(codebook), _ptr(absmax_q),
                                      _ptr(absmax_table), _ptr(absmax2), float(absmax_offset), nested_block, _ptr(Y),
                                      _dtype_code(Y), M, N, K, block_size, _ptr(ws), wsb, _stream(stream))
@@ -334,7 +333,7 @@ def qgemm_nbits_packed_zp(A, W, scales, zero_points_packed, Y, *, bits, block_si
     M, K = A.shape
     N = W.shape[0]
     ws, wsb = _workspace(lambda: qgemm_nbits_packed_zp_workspace_bytes(_dtype_code(A), M, N, K, bits, block_size),
-                         workspace, A.device)
+                         workspace, A.device, stream)
     s = lib().qgemm_nbits_packed_zp(_ptr(A), _dtype_code(A), _ptr(W), _ptr(scales), _ptr(zero_points_packed),
                                     _ptr(Y), _dtype_code(Y), M, N, K, bits, block_size, _ptr(ws), wsb,
                                     _stream(stream))
@@ -365,7 +364,7 @@ def qmoe_ragged_mm(X, offsets, W, scales, zero_points, Y, *, bits, block_size, w
     E, N = W.shape[0], W.shape[1]
     K = X.shape[1]
     ws, wsb = _workspace(lambda: lib().qmoe_ragged_mm_workspace_bytes(_dtype_code(X), p, E, N, K, bits, block_size),
-                         workspace, X.device)
+                         workspace, X.device, stream)
     s = lib().qmoe_ragged_mm(_ptr(X), _dtype_code(X), p, E, _ptr(W), _ptr(scales), _ptr(zero_points), _ptr(Y),
                              _dtype_code(Y), N, K, bits, block_size, _ptr(ws), wsb, _stream(stream))
     return s if raw else _check(s, "qmoe_ragged_mm")
@@ -384,7 +383,7 @@ def qmoe_ragged_mm_device_offsets(X, offsets_dev, W, scales, zero_points, Y, *, 
     """
     E, N = W.shape[0], W.shape[1]
     max_rows, K = X.shape
-    ws, wsb = _workspace(lambda: lib().qmoe_ragged_mm_device_offsets_workspace_bytes(E), workspace, X.device)
+    ws, wsb = _workspace(lambda: lib().qmoe_ragged_mm_device_offsets_workspace_bytes(E), workspace, X.device, stream)
     s = lib().qmoe_ragged_mm_device_offsets(_ptr(X), _dtype_code(X), _ptr(offsets_dev), E, max_rows, _ptr(W),
                                             _ptr(scales), _ptr(zero_points), _ptr(Y), _dtype_code(Y), N, K, bits,
                                             block_size, _ptr(ws), wsb, _ptr(status), _stream(stream))

@@ -141,3 +141,12 @@ def test_scratch_memory_belongs_to_the_stream_of_the_call(qg, monkeypatch):
     raw, at, size, piece = qg._stream_and_workspace(64, None, FakeTensor(), None)
     assert (raw, at, size, piece.stream) == (3, P, 64, "current")
     assert qg._stream_and_workspace(0, None, FakeTensor(), s)[1:] == (None, 0, None) and len(fake.made) == 2
+
+
+def test_scratch_memory_of_the_other_calls(qg, monkeypatch):
+    fake, s = FakeTorch(), FakeTorch.Stream()
+    monkeypatch.setattr(qg, "_TORCH", fake)
+    for stream in (s, None):
+        piece, size = qg._workspace(lambda: 128, None, "cuda:0", stream)
+        assert size == 128 and piece.stream == (stream or "current") and fake.now == "current"
+    assert qg._workspace(lambda: 0, None, "cuda:0", s) == (None, 0) and len(fake.made) == 2
