@@ -26,7 +26,7 @@ __all__ = [
     "qgemm_codebook4_nested", "qgemm_codebook4_nested_workspace_bytes", "qmoe_ragged_mm",
     "qmoe_ragged_mm_workspace_bytes", "qg_gather_block_quantized", "QG_WF_U2", "QG_WF_U4", "QG_WF_U8", "QG_WF_E4M3",
     "qgemm_nbits_packed_zp", "qgemm_nbits_packed_zp_workspace_bytes", "qg_test_bounded_wait",
-    "qg_test_gemv_plan", "qmoe_ragged_mm_device_offsets", "qmoe_ragged_mm_device_offsets_workspace_bytes",
+    "qg_test_gemv_plan", "qg_test_cluster_limit", "qmoe_ragged_mm_device_offsets", "qmoe_ragged_mm_device_offsets_workspace_bytes",
     "qg_lora_apply", "qg_lora_apply_workspace_bytes", "qg_lora_grad", "qg_lora_grad_workspace_bytes",
     "qgemm_nbits_dgrad", "qgemm_nbits_uniform_zp_dgrad", "qgemm_codebook4_dgrad", "qgemm_dgrad_workspace_bytes",
     "QGGradList", "qg_clip_grad_norm", "qg_clip_grad_norm_workspace_bytes",
@@ -100,6 +100,7 @@ _SIGS = {
     "qg_read_device_fault": ([_P], _I),
     "qg_test_bounded_wait": ([_I, ctypes.c_uint, _P, _P], _I),
     "qg_test_gemv_plan": ([_I, _I, _I, _I, _I, _P], _I),
+    "qg_test_cluster_limit": ([_I], _I),
     "qg_status_string": ([_I], ctypes.c_char_p),
 }
 
@@ -644,6 +645,15 @@ def qg_test_gemv_plan(M: int, N: int, K: int, a_dtype: int = QG_F32, zp_mode: in
         return None
     _check(s, "qg_test_gemv_plan")
     return dict(zip(("rows_per_tile", "warps", "ctas", "stages"), list(out)))
+
+
+def qg_test_cluster_limit(widest: int) -> int:
+    """Test hook (include/qgemm_testing.h): the widest cluster of the adapter and activation-gradient launches of few
+    rows (1, 2, 4, 8 or 16) from now on; returns the limit before."""
+    before = lib().qg_test_cluster_limit(int(widest))
+    if before == 0:
+        raise ValueError("a power of two up to 16 is wanted")
+    return before
 
 
 def qg_status_string(status: int) -> str:

@@ -54,6 +54,36 @@ const DeviceInfo &device_info() {
     return g_info[slot];
 }
 
+std::atomic<int> g_cluster_limit{16};
+
+int fitting_cluster(const void *kern, ClusterFit &seen, int want, int threads, int smem) {
+    want = std::min(want, g_cluster_limit.load(std::memory_order_relaxed));
+    if (want <= 8) return want;
+    const int slot = device_slot();
+    const unsigned long long bit = slot < 0 ? 0 : 1ull << slot;
+    if (!(seen.known.load(std::memory_order_acquire) & bit)) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(want));
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(want);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            n = 0;
+            (void)cudaGetLastError();
+        }
+        if (n > 0) seen.fits.fetch_or(bit, std::memory_order_relaxed);
+        seen.known.fetch_or(bit, std::memory_order_release);
+        return n > 0 ? want : 8;
+    }
+    return seen.fits.load(std::memory_order_relaxed) & bit ? want : 8;
+}
+
 unsigned *fault_word() {
     const int slot = device_slot();
     if (slot < 0 || !g_fault_ready[slot].load(std::memory_order_acquire)) {

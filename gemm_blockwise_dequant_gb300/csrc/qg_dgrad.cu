@@ -803,7 +803,7 @@ Plan make_plan(int dy_dtype, int M, int N, int K) {
 bool tensor_cores(int bits) { return bits != 3 && encode_fn() != nullptr; }
 
 template <int WK, int BITS, bool BF16, int PAIR, int H, int TERMS = 1>
-cudaError_t launch(const CUtensorMap *maps, const DgradArgs &a, int tiles, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap *maps, DgradArgs a, int tiles, cudaStream_t s) {
     auto kern = dgrad_kernel<WK, BITS, BF16, PAIR, H, TERMS>;
     static std::atomic<unsigned long long> configured{0};
     const int slot = device_slot();
@@ -816,6 +816,15 @@ cudaError_t launch(const CUtensorMap *maps, const DgradArgs &a, int tiles, cudaS
             if (e16 != cudaSuccess) return e16;
         }
         configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    if (PAIR == 1) {  // fewer CTAs a tile where so many cannot be a cluster
+        static ClusterFit fit;
+        const int splits = fitting_cluster(reinterpret_cast<const void *>(kern), fit, a.splits, kThreads, smem_bytes(H, TERMS));
+        if (splits != a.splits) {
+            tiles = tiles / a.splits * splits;
+            a.splits = splits;
+            a.split_steps = (a.steps + splits - 1) / splits;
+        }
     }
     return launch_cluster(kern, dim3(tiles * PAIR), dim3(kThreads), smem_bytes(H, TERMS), s, PAIR == 1 ? a.splits : PAIR, maps[0], maps[1], a);
 }

@@ -2,6 +2,7 @@
 // units (not part of the public ABI; see include/qgemm.h for that).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -46,6 +47,14 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+// How wide a cluster of up to `want` CTAs of `kern` may be.  More than 8 are not portable: where no group of SMs
+// open to this process has room for them such a launch fails, so it takes 8.  Looked up once per device and kernel.
+struct ClusterFit {
+    std::atomic<unsigned long long> known{0}, fits{0};  // a bit for each device
+};
+int fitting_cluster(const void *kern, ClusterFit &seen, int want, int threads, int smem);
+extern std::atomic<int> g_cluster_limit;  // the widest one for all of them (16; a test lowers it)
 
 // ZP_PACKED: bits-wide unsigned zero points packed along each row, rows padded
 // to whole bytes (the SIMT kernel reads them as staged; no other kernel does).

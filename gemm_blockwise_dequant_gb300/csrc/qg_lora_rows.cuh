@@ -1009,12 +1009,16 @@ __global__ void __launch_bounds__(256, 2) lora_rows_kernel(const RowsArgs q) {
 }
 
 template <int XT, int WT, bool BWD, int MT, int RG, int NT, bool GIVEN>
-cudaError_t launch_rows_one(const RowsArgs &q, const RowsPlan &plan, cudaStream_t s) {
+cudaError_t launch_rows_one(RowsArgs q, const RowsPlan &plan, cudaStream_t s) {
     auto kern = lora_rows_kernel<XT, WT, BWD, MT, RG, NT, GIVEN>;
     const int smem = RowsKernel<XT, WT, BWD, MT, RG, NT, GIVEN>::smem_bytes(q.p.r);
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = allow_smem(kern, done, RowsKernel<XT, WT, BWD, MT, RG, NT, GIVEN>::smem_bytes(kMaxRank), true);
     if (e != cudaSuccess) return e;
+    if constexpr (!GIVEN) {
+        static ClusterFit fit;
+        q.cs = fitting_cluster(reinterpret_cast<const void *>(kern), fit, q.cs, 256, RowsKernel<XT, WT, BWD, MT, RG, NT, GIVEN>::smem_bytes(kMaxRank));
+    }
     return launch_cluster(kern, dim3(static_cast<unsigned>(plan.tiles) * q.cs), dim3(256), smem, s, GIVEN ? 1 : q.cs, q);
 }
 

@@ -1,4 +1,4 @@
-// qg_testing.cu -- a hook for the failure-detection test (include/qgemm_testing.h).
+// qg_testing.cu -- hooks for the tests (include/qgemm_testing.h).
 //
 // Every pipeline wait of the library's kernels goes through mbar_wait
 // (qg_device.cuh): bounded by %globaltimer, it gives up, records a bit in the
@@ -49,4 +49,9 @@ extern "C" int qg_test_bounded_wait(int fill, unsigned int limit_us, int *out_de
 extern "C" int qg_test_gemv_plan(int M, int N, int K, int a_dtype, int zp_mode, int *out) {
     if (!out || M < 1 || N < 1 || K < 1) return QG_ERR_INVALID_ARG;
     return qg::mma_gemv_plan(M, N, K, a_dtype, zp_mode, out) ? QG_OK : QG_ERR_UNSUPPORTED;
+}
+
+extern "C" int qg_test_cluster_limit(int widest) {
+    if (widest < 1 || widest > 16 || (widest & (widest - 1))) return 0;
+    return qg::g_cluster_limit.exchange(widest, std::memory_order_relaxed);
 }

@@ -39,6 +39,15 @@
  * Returns QG_OK, QG_ERR_INVALID_ARG (null out, M, N or K not positive) or
  * QG_ERR_UNSUPPORTED (the request does not take this GEMV: other paths serve it).
  */
+/*
+ * qg_test_cluster_limit -- the widest thread-block cluster that the adapter and
+ * activation-gradient launches of few rows may take from now on, in this process:
+ * 16 unless a test lowers it to see the launches of a device (or a part of one) on
+ * which no cluster of 16 fits.
+ *
+ *   widest    1, 2, 4, 8 or 16
+ * Returns the limit before, or 0 (and changes nothing) for any other value.
+ */
 #ifndef QGEMM_TESTING_H
 #define QGEMM_TESTING_H
 
@@ -50,6 +59,7 @@ extern "C" {
 
 int qg_test_bounded_wait(int fill, unsigned int limit_us, int *out_dev, qg_stream_t stream);
 int qg_test_gemv_plan(int M, int N, int K, int a_dtype, int zp_mode, int *out);
+int qg_test_cluster_limit(int widest);
 
 #ifdef __cplusplus
 }
