@@ -480,6 +480,11 @@ int qg_gather_block_quantized(const int64_t *indices, int64_t n_indices, const u
  *   dA, dB       shapes of A and B; g_dtype: w_dtype or QG_F32; zero for an
  *                adapter without rows.  accumulate = 1 adds to their contents.
  *   workspace    at least qg_lora_grad_workspace_bytes(...) bytes, 16-byte aligned
+ * Sums are fp32 with operands as above; G and V enter dA and dB in two bf16 terms (16
+ * bits) for bf16 gradients, else in 22 bits or more.
+ * Infinities and NaN (both passes): a result is infinite or NaN where one that is enters
+ * its sum, and no other result is; as operands go in two terms, a sum that an infinity
+ * makes infinite may come out as NaN.
  * rows == 0 or num_segments == 0: dA and dB are zeros (or what they held), dX is
  * not written.  N == 0: empty sums, so dX is dX_in and dA is zero; dY, B and dB
  * may be NULL.
@@ -508,6 +513,10 @@ int qg_lora_grad(const void *dY, int x_dtype, int64_t lddy, const void *X, int64
  *   the forward pass; fp32 dY: dY and the weight go in two scaled fp16 terms each
  *   (22 bits).  fp32 accumulation, one rounding to dx_dtype.  3-bit codes run on
  *   a plain fp32 kernel.
+ *   An infinite or NaN dY reaches the whole of its row, an infinite or NaN parameter the
+ *   columns of its block, and nothing else; with fp32 dY, whose terms are multiplied one
+ *   by one, an infinity comes out as NaN.  A uniform_zp that is no finite fp16 value is
+ *   QG_ERR_INVALID_ARG, as in qgemm_nbits_uniform_zp.
  *   workspace: at least qgemm_dgrad_workspace_bytes(dy_dtype, M, N, K, bits)
  *   bytes, 16-byte aligned (NULL when that is 0).
  * M == 0 or K == 0 is a no-op; N == 0 writes zeros.
