@@ -30,12 +30,15 @@ __all__ = [
     "qg_lora_apply", "qg_lora_apply_workspace_bytes", "qg_lora_grad", "qg_lora_grad_workspace_bytes",
     "qgemm_nbits_dgrad", "qgemm_nbits_uniform_zp_dgrad", "qgemm_codebook4_dgrad", "qgemm_dgrad_workspace_bytes",
     "QGGradList", "qg_clip_grad_norm", "qg_clip_grad_norm_workspace_bytes",
+    "QGAdamWList", "qg_adamw_step", "qg_adamw_step_workspace_bytes", "QG_STATE_F32", "QG_STATE_E4M3", "QG_STATE_BLOCK",
+    "qg_token_logprobs", "qg_token_logprobs_grad",
 ]
 
 QG_OK, QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_CUDA, QG_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3, 4
 QG_F32, QG_F16, QG_BF16 = 0, 1, 2
 QG_QMOE_NOALLOC_SCRATCH_BYTES = 1 << 20
 QG_WF_U2, QG_WF_U4, QG_WF_U8, QG_WF_E4M3 = 0, 1, 2, 3
+QG_STATE_F32, QG_STATE_E4M3, QG_STATE_BLOCK = 0, 1, 256
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libqgemm.so")
@@ -58,7 +61,7 @@ def _status_name(s):
             4: "QG_ERR_WORKSPACE_TOO_SMALL"}.get(s, "status %d" % s)
 
 
-_P, _I, _SZ, _F, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64
+_P, _I, _SZ, _F, _L, _D = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64, ctypes.c_double
 _SIGS = {
     "qgemm_nbits": ([_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P], _I),
     "qgemm_nbits_uniform_zp": ([_P, _I, _P, _P, _F, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P], _I),
@@ -97,6 +100,11 @@ _SIGS = {
     "qg_grad_list_init": ([_P, _I, _P], _I),
     "qg_clip_grad_norm_workspace_bytes": ([_L], _SZ),
     "qg_clip_grad_norm": ([_P, _I, _L, _F, _F, _P, _P, _SZ, _P], _I),
+    "qg_adamw_list_init": ([_P, _I, _P], _I),
+    "qg_adamw_step_workspace_bytes": ([_L], _SZ),
+    "qg_adamw_step": ([_P, _I, _L, _D, _P, _D, _D, _D, _L, _P, _F, _F, _P, _P, _SZ, _P], _I),
+    "qg_token_logprobs": ([_P, _I, _L, _P, _I, _I, _F, _P, _P, _P, _I, _P, _P, _P, _P], _I),
+    "qg_token_logprobs_grad": ([_P, _I, _L, _P, _P, _P, _P, _P, _F, _P, _L, _I, _I, _P], _I),
     "qg_read_device_fault": ([_P], _I),
     "qg_test_bounded_wait": ([_I, ctypes.c_uint, _P, _P], _I),
     "qg_test_gemv_plan": ([_I, _I, _I, _I, _I, _P], _I),
@@ -618,6 +626,185 @@ def qg_clip_grad_norm(grads, max_norm, norm, *, eps=1e-6, workspace=None, stream
     s = lib().qg_clip_grad_norm(_addr(grads.table), grads.count, grads.chunks, float(max_norm), float(eps), _addr(norm), wp,
                                 wb, st)
     return s if raw else _check(s, "qg_clip_grad_norm")
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", _P), ("grad", _P), ("master", _P), ("exp_avg", _P), ("exp_avg_sq", _P), ("exp_avg_scale", _P),
+                ("exp_avg_sq_scale", _P), ("numel", _L), ("first_chunk", _L), ("weight_decay", _F), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32)]
+
+
+class QGAdamWList:
+    """The tensors of an optimizer step, for qg_adamw_step: made once, used every step.
+
+    params and grads: one gradient of its size for each parameter, float32/float16/bfloat16 each.  master: float32 copies of
+    the parameters, or None (a sequence may hold None for some).  weight_decay: a number, or one for each tensor.
+
+    States: with exp_avg None they are made here, all zero, as `state` says ("f32", or "e4m3": 8 bits and a scale for
+    every QG_STATE_BLOCK values; or one of the two for each tensor).  Else the caller's: exp_avg in float32 with
+    exp_avg_sq, or in float8_e4m3fn with exp_avg_rms (the root of the second moment) and the float32 scales of both.
+    They are attributes of those names afterwards, for saving: lists with None where a tensor has none.
+
+    It holds the tensors, their addresses on the device and a workspace, so it is for buffers that stay where they are
+    from step to step, and for one step at a time.
+    """
+
+    def __init__(self, params, grads, *, master=None, weight_decay=0.0, state="f32", exp_avg=None, exp_avg_sq=None, exp_avg_scale=None,
+                 exp_avg_rms=None, exp_avg_rms_scale=None):
+        torch = _torch()
+        params = list(params)
+        n = len(params)
+        each = lambda v, what: [None] * n if v is None else _as_many(list(v), n, what)
+        grads, master = _as_many(list(grads), n, "grads"), each(master, "master")
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else _as_many([float(d) for d in weight_decay], n, "weight_decay")
+        if exp_avg is None:
+            if not (exp_avg_sq is None and exp_avg_scale is None and exp_avg_rms is None and exp_avg_rms_scale is None):
+                raise ValueError("states: exp_avg is wanted with them")
+            kinds = [state] * n if isinstance(state, str) else _as_many(list(state), n, "state")
+            if any(k not in ("f32", "e4m3") for k in kinds):
+                raise ValueError("state: f32 or e4m3 is wanted")
+            zeros = lambda p, k, dtype, per=1: None if k else torch.zeros(-(-p.numel() // per), dtype=dtype, device=p.device)
+            eight = [k == "e4m3" for k in kinds]
+            exp_avg = [zeros(p, False, torch.float8_e4m3fn if k else torch.float32) for p, k in zip(params, eight)]
+            exp_avg_sq = [zeros(p, k, torch.float32) for p, k in zip(params, eight)]
+            exp_avg_rms = [zeros(p, not k, torch.float8_e4m3fn) for p, k in zip(params, eight)]
+            exp_avg_scale, exp_avg_rms_scale = ([zeros(p, not k, torch.float32, QG_STATE_BLOCK) for p, k in zip(params, eight)] for _ in range(2))
+        exp_avg = _as_many(list(exp_avg), n, "exp_avg")
+        exp_avg_sq, exp_avg_rms = each(exp_avg_sq, "exp_avg_sq"), each(exp_avg_rms, "exp_avg_rms")
+        exp_avg_scale, exp_avg_rms_scale = each(exp_avg_scale, "exp_avg_scale"), each(exp_avg_rms_scale, "exp_avg_rms_scale")
+        host = (_AdamWTensor * max(1, n))()
+        for i, (h, p) in enumerate(zip(host, params)):
+            m = exp_avg[i]
+            eight = m is not None and m.dtype == torch.float8_e4m3fn
+            second = exp_avg_rms[i] if eight else exp_avg_sq[i]
+            blocks = -(-p.numel() // QG_STATE_BLOCK)
+            wanted = [(grads[i], None, p.numel()), (m, torch.float8_e4m3fn if eight else torch.float32, p.numel()),
+                      (second, torch.float8_e4m3fn if eight else torch.float32, p.numel())]
+            if eight:
+                wanted += [(exp_avg_scale[i], torch.float32, blocks), (exp_avg_rms_scale[i], torch.float32, blocks)]
+            if master[i] is not None:
+                wanted.append((master[i], torch.float32, p.numel()))
+            for t, dtype, numel in [(p, None, p.numel())] + wanted:
+                if t is None or not t.is_cuda or t.device != params[0].device:
+                    raise ValueError("parameters, gradients and states: tensors of one GPU are wanted")
+                if not t.is_contiguous() or t.numel() != numel or (dtype is not None and t.dtype != dtype):
+                    raise ValueError("gradients, states and master copies: contiguous tensors of the parameter's size are wanted (states in "
+                                     "float32, or in float8_e4m3fn with float32 scales)")
+            h.param, h.grad, h.master, h.exp_avg, h.exp_avg_sq = p.data_ptr(), grads[i].data_ptr(), _addr(master[i]), m.data_ptr(), second.data_ptr()
+            h.exp_avg_scale, h.exp_avg_sq_scale = (_addr(exp_avg_scale[i]), _addr(exp_avg_rms_scale[i])) if eight else (None, None)
+            h.numel, h.weight_decay, h.param_dtype, h.grad_dtype = p.numel(), decay[i], _dtype_code(p), _dtype_code(grads[i])
+            h.state = QG_STATE_E4M3 if eight else QG_STATE_F32
+        chunks = ctypes.c_int64(0)
+        _check(lib().qg_adamw_list_init(host, n, ctypes.byref(chunks)), "qg_adamw_list_init")
+        self.params, self.grads, self.master, self.count, self.chunks = params, grads, master, n, chunks.value
+        self.exp_avg, self.exp_avg_sq, self.exp_avg_scale = exp_avg, exp_avg_sq, exp_avg_scale
+        self.exp_avg_rms, self.exp_avg_rms_scale = exp_avg_rms, exp_avg_rms_scale
+        device = params[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        self.table = torch.frombuffer(bytearray(host), dtype=torch.uint8).to(device)
+        self.workspace = torch.empty(lib().qg_adamw_step_workspace_bytes(self.chunks), dtype=torch.uint8, device=device)
+
+
+def _as_many(v, n, what):
+    if len(v) != n:
+        raise ValueError("%s: one for each parameter is wanted" % what)
+    return v
+
+
+def qg_adamw_step_workspace_bytes(chunks: int) -> int:
+    return lib().qg_adamw_step_workspace_bytes(chunks)
+
+
+def _device_scalar(t, dtype, what):
+    if t.dtype != dtype or t.numel() != 1 or not t.is_cuda:
+        raise ValueError("%s: one %s value of a GPU is wanted" % (what, str(dtype).replace("torch.", "")))
+    return t.data_ptr()
+
+
+def qg_adamw_step(tensors, *, lr, step, betas=(0.9, 0.999), eps=1e-8, max_norm=None, norm_eps=1e-6, norm=None, workspace=None, stream=None,
+                  raw=False):
+    """One AdamW step over the parameters of a QGAdamWList, in place.
+
+    lr: a number or a float32 device tensor of one value; step: 1 for the first one, a number or an int64 device tensor
+    of one value (a captured call reads both anew).  max_norm: the gradients enter scaled by min(1, max_norm / (their
+    2-norm + norm_eps)), None for no clipping; norm: a float32 device tensor of one value that receives the 2-norm (with
+    max_norm), or None.  A norm that is infinite or NaN leaves every tensor as it was.
+    """
+    torch = _torch()
+    if not isinstance(tensors, QGAdamWList):
+        raise ValueError("tensors: a QGAdamWList is wanted")
+    lr_dev = _device_scalar(lr, torch.float32, "lr") if isinstance(lr, torch.Tensor) else None
+    step_dev = _device_scalar(step, torch.int64, "step") if isinstance(step, torch.Tensor) else None
+    norm_dev = None if norm is None else _device_scalar(norm, torch.float32, "norm")
+    if max_norm is not None and not max_norm >= 0:
+        raise ValueError("max_norm: a number that is not negative, or None, is wanted")
+    st, wp, wb, _ = _stream_and_workspace(0, tensors.workspace if workspace is None else workspace, tensors.table, stream)
+    if stream is not None:
+        tensors.table.record_stream(stream)
+        tensors.workspace.record_stream(stream)
+    s = lib().qg_adamw_step(tensors.table.data_ptr(), tensors.count, tensors.chunks, 0.0 if lr_dev else float(lr), lr_dev, betas[0], betas[1],
+                            eps, 1 if step_dev else int(step), step_dev, -1.0 if max_norm is None else float(max_norm), float(norm_eps),
+                            norm_dev, wp, wb, st)
+    return s if raw else _check(s, "qg_adamw_step")
+
+
+# ---------------------------------------------------------------- log probabilities of tokens
+def _logits_args(X, targets):
+    """rows, vocab, the distance between rows, and the tokens' address."""
+    if X.dim() != 2:
+        raise ValueError("X: logits [rows, vocab] are wanted")
+    T, V = X.shape
+    if targets is not None and (targets.dtype != _torch().int64 or targets.shape != (T,) or not targets.is_contiguous()):
+        raise ValueError("targets: [rows] int64 is wanted")
+    return T, V, _rows2d(X, T, V, "X"), _addr(targets)
+
+
+def _per_row(t, T, what):
+    if t is None:
+        return None
+    if t.dtype != _torch().float32 or t.shape != (T,) or not t.is_contiguous():
+        raise ValueError("%s: [rows] float32 is wanted" % what)
+    return t.data_ptr()
+
+
+def qg_token_logprobs(X, targets, logprob, *, entropy=None, lse=None, top_ids=None, top_logprobs=None, inv_temperature=1.0, status=None,
+                      stream=None, raw=False):
+    """logprob[t] = log softmax(X[t] * inv_temperature)[targets[t]], with the entropy and log-sum-exp of each row and the
+    most probable tokens.
+
+    X: [T, V] float32/float16/bfloat16 logits (rows may lie apart); targets: [T] int64 or None (a negative one: none given
+    there, logprob 0); logprob, entropy, lse: [T] float32 or None; top_ids [T, k] int64 and top_logprobs [T, k] float32
+    (k up to 64): the k largest logits of each row, the lower index first among equals; status: a device int32 set to 1 by
+    a target at or past V, or None.
+    """
+    T, V, ldx, tp = _logits_args(X, targets)
+    torch = _torch()
+    k = 0
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs: both or none are wanted")
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != T or top_ids.dtype != torch.int64 or top_logprobs.shape != top_ids.shape \
+                or top_logprobs.dtype != torch.float32 or not top_ids.is_contiguous() or not top_logprobs.is_contiguous():
+            raise ValueError("top_ids [rows, k] int64 and top_logprobs [rows, k] float32 are wanted")
+        k = top_ids.shape[1]
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status: an int32 is wanted")
+    st = torch._C._cuda_getCurrentRawStream(X.get_device()) if stream is None else stream.cuda_stream
+    s = lib().qg_token_logprobs(X.data_ptr(), _dtype_code(X), ldx, tp, T, V, inv_temperature, _per_row(logprob, T, "logprob"),
+                                _per_row(entropy, T, "entropy"), _per_row(lse, T, "lse"), k, _addr(top_ids), _addr(top_logprobs), _addr(status), st)
+    return s if raw else _check(s, "qg_token_logprobs")
+
+
+def qg_token_logprobs_grad(X, targets, lse, d_logprob, dX, *, entropy=None, d_entropy=None, inv_temperature=1.0, stream=None, raw=False):
+    """The gradient of the logits from d_logprob [T] and d_entropy [T] (None: zeros) of qg_token_logprobs, with its lse and
+    (beside d_entropy) entropy; dX: [T, V] in X's type, or X itself."""
+    T, V, ldx, tp = _logits_args(X, targets)
+    lddx = _rows2d(dX, T, V, "dX")
+    if dX.dtype != X.dtype:
+        raise ValueError("dX: X's type is wanted")
+    st = _torch()._C._cuda_getCurrentRawStream(X.get_device()) if stream is None else stream.cuda_stream
+    s = lib().qg_token_logprobs_grad(X.data_ptr(), _dtype_code(X), ldx, tp, _per_row(lse, T, "lse"), _per_row(entropy, T, "entropy"),
+                                     _per_row(d_logprob, T, "d_logprob"), _per_row(d_entropy, T, "d_entropy"), inv_temperature, dX.data_ptr(), lddx, T, V, st)
+    return s if raw else _check(s, "qg_token_logprobs_grad")
 
 
 def qg_read_device_fault() -> int:

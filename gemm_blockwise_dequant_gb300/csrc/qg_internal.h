@@ -228,6 +228,50 @@ size_t clip_workspace_bytes(int64_t chunks);
 cudaError_t clip_grad_norm(const void *list, int count, int64_t chunks, float max_norm, float eps, float *norm, void *ws,
                            cudaStream_t s);
 
+// One AdamW step over a list of tensors (qg_adamw.cu); the list is include/qgemm.h's qg_adamw_tensor.
+int64_t adamw_chunks(int64_t numel);
+size_t adamw_workspace_bytes(int64_t chunks);
+struct AdamwStep {
+    const void *list;
+    int count;
+    int64_t chunks;
+    double lr, beta1, beta2, eps;
+    const float *lr_dev;     // or null
+    int64_t step;
+    const int64_t *step_dev; // or null
+    bool clip;
+    float max_norm, norm_eps;
+    float *norm;             // or null
+};
+cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s);
+
+// Log probabilities of given tokens and their gradient (validated requests; qg_logprobs.cu).
+struct TokenLogprobs {
+    const void *X;
+    int x_dtype;
+    int64_t ldx;
+    const int64_t *target;   // or null
+    int T, V, top;
+    float inv_t;
+    float *logprob, *entropy, *lse;  // or null
+    int64_t *top_ids;
+    float *top_logprobs;
+    int *status;
+};
+cudaError_t token_logprobs(const TokenLogprobs &q, cudaStream_t s);
+struct TokenLogprobsGrad {
+    const void *X;
+    int x_dtype;
+    int64_t ldx;
+    const int64_t *target;
+    const float *lse, *entropy, *d_logprob, *d_entropy;  // d_entropy null: entropy is not read
+    void *dX;
+    int64_t lddx;
+    int T, V;
+    float inv_t;
+};
+cudaError_t token_logprobs_grad(const TokenLogprobsGrad &q, cudaStream_t s);
+
 // Utility kernels.
 cudaError_t launch_dequant(const GemmProblem &p, float *out, cudaStream_t s);
 cudaError_t launch_uniform_check(const uint16_t *t, size_t n, unsigned *ws, cudaStream_t s);

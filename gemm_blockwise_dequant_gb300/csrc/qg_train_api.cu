@@ -2,6 +2,7 @@
 // (include/qgemm.h): argument checks and dispatch.  Everything is refused or
 // accepted on the host before anything is enqueued.
 #include <climits>
+#include <cmath>
 
 #include "../../include/qgemm.h"
 #include "qg_internal.h"
@@ -244,6 +245,50 @@ int qg_clip_grad_norm(const qg_grad_tensor *tensors_dev, int count, int64_t chun
     if (st != QG_OK) return st;
     return finish(qg::clip_grad_norm(tensors_dev, count, chunks, max_norm, eps, norm_dev, workspace,
                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qg_adamw_list_init(qg_adamw_tensor *tensors_host, int count, int64_t *chunks) {
+    if (count < 0 || !chunks || (count > 0 && !tensors_host)) return QG_ERR_INVALID_ARG;
+    int64_t at = 0;
+    for (int i = 0; i < count; ++i) {
+        qg_adamw_tensor &t = tensors_host[i];
+        if (t.numel < 0 || !valid_dtype(t.param_dtype) || !valid_dtype(t.grad_dtype)) return QG_ERR_INVALID_ARG;
+        if (t.state != QG_STATE_F32 && t.state != QG_STATE_E4M3) return QG_ERR_INVALID_ARG;
+        if (!(t.weight_decay >= 0.f && t.weight_decay < INFINITY)) return QG_ERR_INVALID_ARG;  // NaN too
+        if (t.numel > 0 && (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq)) return QG_ERR_INVALID_ARG;
+        if (!aligned(t.param, esize(t.param_dtype)) || !aligned(t.grad, esize(t.grad_dtype)) || !aligned(t.master, 4)) return QG_ERR_INVALID_ARG;
+        if (t.state == QG_STATE_F32) {
+            if (!aligned(t.exp_avg, 4) || !aligned(t.exp_avg_sq, 4)) return QG_ERR_INVALID_ARG;
+        } else if ((t.numel > 0 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) || !aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4)) {
+            return QG_ERR_INVALID_ARG;
+        }
+        t.first_chunk = at;
+        at += qg::adamw_chunks(t.numel);
+        if (at > INT_MAX) return QG_ERR_UNSUPPORTED;
+    }
+    *chunks = at;
+    return QG_OK;
+}
+
+size_t qg_adamw_step_workspace_bytes(int64_t chunks) { return qg::adamw_workspace_bytes(chunks < 0 ? 0 : chunks); }
+
+int qg_adamw_step(const qg_adamw_tensor *tensors_dev, int count, int64_t chunks, double lr, const float *lr_dev, double beta1,
+                  double beta2, double eps, int64_t step, const int64_t *step_dev, float max_norm, float norm_eps,
+                  float *norm_dev, void *workspace, size_t workspace_bytes, qg_stream_t stream) {
+    (void)cudaGetLastError();
+    if (count < 0 || chunks < 0 || chunks > INT_MAX || (count == 0 && chunks > 0)) return QG_ERR_INVALID_ARG;
+    if (count > 0 && (!tensors_dev || !aligned(tensors_dev, 8))) return QG_ERR_INVALID_ARG;
+    if (!lr_dev && !(lr >= 0.0 && lr < INFINITY)) return QG_ERR_INVALID_ARG;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0 && eps < INFINITY)) return QG_ERR_INVALID_ARG;
+    if ((!step_dev && step < 1) || !aligned(lr_dev, 4) || !aligned(step_dev, 8) || !aligned(norm_dev, 4)) return QG_ERR_INVALID_ARG;
+    const bool clip = !(max_norm < 0.f);
+    if (max_norm != max_norm || (clip && !(norm_eps >= 0.f))) return QG_ERR_INVALID_ARG;
+    if (clip) {
+        const int st = check_workspace(workspace, workspace_bytes, qg::adamw_workspace_bytes(chunks));
+        if (st != QG_OK) return st;
+    }
+    const qg::AdamwStep q{tensors_dev, count, chunks, lr, beta1, beta2, eps, lr_dev, step, step_dev, clip, max_norm, norm_eps, norm_dev};
+    return finish(qg::adamw_step(q, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

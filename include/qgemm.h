@@ -567,6 +567,91 @@ int qg_clip_grad_norm(const qg_grad_tensor *tensors_dev, int count, int64_t chun
                       float *norm_dev, void *workspace, size_t workspace_bytes, qg_stream_t stream);
 
 /*
+ * qg_adamw_step -- one AdamW step over a list of tensors, in place (an addition of this library, like what follows):
+ *   c  = min(1, max_norm / (norm + norm_eps)),  norm = sqrt( sum over every tensor and value of grad^2 );  g' = c * grad
+ *   m' = beta1 m + (1 - beta1) g',   v' = beta2 v + (1 - beta2) g'^2
+ *   p' = p (1 - lr weight_decay) - lr (m' / (1 - beta1^step)) / (sqrt(v' / (1 - beta2^step)) + eps)
+ * computed in fp32.  p is the fp32 master copy where a tensor has one (param then receives it rounded), else param.
+ *
+ * States (state of a tensor), m in exp_avg and the second moment in exp_avg_sq:
+ *   QG_STATE_F32    m and v in fp32; the scales are not used
+ *   QG_STATE_E4M3   e4m3 codes of m and of u = sqrt(v), value = code * scale with one fp32 scale for every
+ *                   QG_STATE_BLOCK values of the tensor (the last block may be shorter): exp_avg_scale and
+ *                   exp_avg_sq_scale, [ceil(numel / QG_STATE_BLOCK)].  A step stores round(x / scale), scale = the
+ *                   block's largest magnitude / 448 (a block below 1e-30 is stored as zeros with scale 0), u above
+ *                   zero never as zero; p' uses m' and v' before that rounding.  All zeros is the state to begin with.
+ * A block of a QG_STATE_E4M3 state that an infinity or NaN enters holds NaN from then on; values outside the block keep theirs.
+ *
+ *   tensors     the list in DEVICE memory, laid out by qg_adamw_list_init from a host array (it holds addresses).
+ *               Its buffers may not overlap.
+ *   count       tensors in the list;  chunks  what qg_adamw_list_init returned
+ *   lr          or, where lr_dev is not NULL, one fp32 in device memory
+ *   step        1 for the first step; or, where step_dev is not NULL, one int64 in device memory (below 1: 1), so
+ *               that a captured call serves every step.  Both are read when the kernels run, neither is changed.
+ *   max_norm    the clipping bound; negative: no clipping (norm_dev is not written).  With clipping, a norm that is
+ *               infinite or NaN leaves every tensor as it was.
+ *   norm_dev    fp32, device: the norm before clipping, or NULL
+ *   workspace   at least qg_adamw_step_workspace_bytes(chunks) bytes, 16-byte aligned (with clipping; else NULL will do)
+ * Sums of the norm as in qg_clip_grad_norm.  Deterministic.
+ *
+ * qg_adamw_list_init -- checks a host array and fills in first_chunk; *chunks receives the number of chunks.  Pointers
+ * have their type's alignment (any address for codes); numel may be 0, with NULL pointers.  Host only.
+ */
+enum { QG_STATE_F32 = 0, QG_STATE_E4M3 = 1 };
+#define QG_STATE_BLOCK 256
+typedef struct {
+    void *param;
+    const void *grad;
+    float *master;           /* or NULL */
+    void *exp_avg, *exp_avg_sq;
+    float *exp_avg_scale, *exp_avg_sq_scale; /* QG_STATE_E4M3 */
+    int64_t numel;
+    int64_t first_chunk;     /* filled in by qg_adamw_list_init */
+    float weight_decay;
+    int32_t param_dtype, grad_dtype; /* QG_F32, QG_F16 or QG_BF16, each */
+    int32_t state;
+} qg_adamw_tensor;
+int qg_adamw_list_init(qg_adamw_tensor *tensors_host, int count, int64_t *chunks);
+size_t qg_adamw_step_workspace_bytes(int64_t chunks);
+int qg_adamw_step(const qg_adamw_tensor *tensors_dev, int count, int64_t chunks, double lr, const float *lr_dev, double beta1,
+                  double beta2, double eps, int64_t step, const int64_t *step_dev, float max_norm, float norm_eps,
+                  float *norm_dev, void *workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/*
+ * qg_token_logprobs -- log probabilities of given tokens, from the logits that the last projection of a model wrote:
+ *   z = X[t] * inv_temperature,  lse[t] = log sum_v exp(z_v),  logprob[t] = z[targets[t]] - lse[t]
+ *   entropy[t] = - sum_v p_v log p_v,  p_v = exp(z_v - lse[t])  (a term with p_v = 0 is 0)
+ *   top_ids[t][j], top_logprobs[t][j]: the top_k most probable tokens and their log probabilities, the largest logit
+ *   first, the lower index first among equals
+ *
+ *   X            [rows] rows of vocab values, ldx values apart; x_dtype; any alignment of its type
+ *   targets      [rows] int64 (device), or NULL (none).  Negative: no token is given, logprob 0.  At or past vocab:
+ *                the same, and *status_dev is set to 1 (it may be NULL and is never cleared).
+ *   inv_temperature  finite, above 0
+ *   logprob, entropy, lse  [rows] fp32, each may be NULL
+ *   top_k        0 .. 64 and at most vocab (0: top_ids and top_logprobs may be NULL)
+ *   top_ids      [rows][top_k] int64;  top_logprobs  [rows][top_k] fp32
+ * Logits of -inf have probability 0.  A row with nothing above -inf: lse and the log probabilities are -inf, the
+ * entropy 0.  A row with +inf or NaN among its logits: NaN throughout; its top_ids are in the order of the logits all
+ * the same, NaN above +inf.  Sums in fp32.  Deterministic.  No workspace.
+ *
+ * qg_token_logprobs_grad -- the gradient of the logits:
+ *   dX[t][v] = inv_temperature * ( d_logprob[t] ([v = targets[t]] - p_v) - d_entropy[t] p_v (log p_v + entropy[t]) )
+ * with the first term left out of rows without a given token (also: a token at or past vocab).
+ *   lse, entropy, inv_temperature  as the forward pass left or had them (entropy: only beside d_entropy)
+ *   d_logprob    [rows] fp32;  d_entropy  [rows] fp32 or NULL (zeros)
+ *   dX           [rows] rows of vocab values, lddx apart, x_dtype; may be X itself (with lddx = ldx)
+ * A row whose two gradients are 0, or whose lse is -inf, gets zeros, whatever its logits.
+ * rows == 0 is a no-op in both; vocab 1 .. 2^28.
+ */
+int qg_token_logprobs(const void *X, int x_dtype, int64_t ldx, const int64_t *targets, int rows, int vocab,
+                      float inv_temperature, float *logprob, float *entropy, float *lse, int top_k, int64_t *top_ids,
+                      float *top_logprobs, int *status_dev, qg_stream_t stream);
+int qg_token_logprobs_grad(const void *X, int x_dtype, int64_t ldx, const int64_t *targets, const float *lse,
+                           const float *entropy, const float *d_logprob, const float *d_entropy, float inv_temperature,
+                           void *dX, int64_t lddx, int rows, int vocab, qg_stream_t stream);
+
+/*
  * qg_read_device_fault -- every wait inside the library's kernels is
  * bounded; a wait that gives up records a bit in a device-side fault word
  * instead of hanging.  This call synchronises the current device, returns
