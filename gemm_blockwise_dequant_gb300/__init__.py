@@ -31,7 +31,7 @@ __all__ = [
     "qgemm_nbits_dgrad", "qgemm_nbits_uniform_zp_dgrad", "qgemm_codebook4_dgrad", "qgemm_dgrad_workspace_bytes",
     "QGGradList", "qg_clip_grad_norm", "qg_clip_grad_norm_workspace_bytes",
     "QGAdamWList", "qg_adamw_step", "qg_adamw_step_workspace_bytes", "QG_STATE_F32", "QG_STATE_E4M3", "QG_STATE_BLOCK",
-    "qg_token_logprobs", "qg_token_logprobs_grad",
+    "qg_token_logprobs", "qg_token_logprobs_grad", "qmoe_route_topk", "qmoe_tokens_fused", "qmoe_tokens_workspace_bytes",
 ]
 
 QG_OK, QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_CUDA, QG_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3, 4
@@ -105,6 +105,9 @@ _SIGS = {
     "qg_adamw_step": ([_P, _I, _L, _D, _P, _D, _D, _D, _L, _P, _F, _F, _P, _P, _SZ, _P], _I),
     "qg_token_logprobs": ([_P, _I, _L, _P, _I, _I, _F, _P, _P, _P, _I, _P, _P, _P, _P], _I),
     "qg_token_logprobs_grad": ([_P, _I, _L, _P, _P, _P, _P, _P, _F, _P, _L, _I, _I, _P], _I),
+    "qmoe_route_topk": ([_P, _I, _L, _I, _I, _I, _I, _P, _P, _P], _I),
+    "qmoe_tokens_workspace_bytes": ([_I, _I, _I, _I], _SZ),
+    "qmoe_tokens_fused": ([_P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _SZ, _P], _I),
     "qg_read_device_fault": ([_P], _I),
     "qg_test_bounded_wait": ([_I, ctypes.c_uint, _P, _P], _I),
     "qg_test_gemv_plan": ([_I, _I, _I, _I, _I, _P], _I),
@@ -805,6 +808,74 @@ def qg_token_logprobs_grad(X, targets, lse, d_logprob, dX, *, entropy=None, d_en
     s = lib().qg_token_logprobs_grad(X.data_ptr(), _dtype_code(X), ldx, tp, _per_row(lse, T, "lse"), _per_row(entropy, T, "entropy"),
                                      _per_row(d_logprob, T, "d_logprob"), _per_row(d_entropy, T, "d_entropy"), inv_temperature, dX.data_ptr(), lddx, T, V, st)
     return s if raw else _check(s, "qg_token_logprobs_grad")
+
+
+# ---------------------------------------------------------------- mixture of experts over a few tokens
+def qmoe_route_topk(logits, expert_ids, expert_weights, *, renormalize=True, stream=None, raw=False):
+    """The k experts of each token with the largest router logits (the lower index first among equals), and their softmax
+    weights over the k (renormalize) or over all experts.
+
+    logits: [T, E] float32/float16/bfloat16 (rows may lie apart); expert_ids: [T, k] int32; expert_weights: [T, k] float32.
+    """
+    torch = _torch()
+    if logits.dim() != 2:
+        raise ValueError("logits: [tokens, experts] are wanted")
+    T, E = logits.shape
+    if expert_ids.dim() != 2 or expert_ids.shape[0] != T or expert_ids.dtype != torch.int32 or expert_weights.shape != expert_ids.shape \
+            or expert_weights.dtype != torch.float32 or not expert_ids.is_contiguous() or not expert_weights.is_contiguous():
+        raise ValueError("expert_ids [tokens, k] int32 and expert_weights [tokens, k] float32 are wanted")
+    st = torch._C._cuda_getCurrentRawStream(logits.get_device()) if stream is None else stream.cuda_stream
+    s = lib().qmoe_route_topk(logits.data_ptr(), _dtype_code(logits), _rows2d(logits, T, E, "logits"), T, E, expert_ids.shape[1],
+                              1 if renormalize else 0, expert_ids.data_ptr(), expert_weights.data_ptr(), st)
+    return s if raw else _check(s, "qmoe_route_topk")
+
+
+def qmoe_tokens_workspace_bytes(tokens: int, k: int, hidden: int, inter: int) -> int:
+    return lib().qmoe_tokens_workspace_bytes(tokens, k, hidden, inter)
+
+
+def _expert_sizes(w, scales, zp, bias, N, K, bits, block_size, what):
+    """The number of experts of a projection [E, N, K]."""
+    torch = _torch()
+    E = w.shape[0]
+    nb = K // block_size if block_size > 0 else 0
+    if w.dtype != torch.uint8 or w.shape != (E, N, K * bits // 8) or not w.is_contiguous():
+        raise ValueError("%s_w: [experts, %d, %d] uint8, contiguous, is wanted" % (what, N, K * bits // 8))
+    for t, shape in ((scales, (E, N, nb)), (zp, (E, N, nb)), (bias, (E, N))):
+        if t is not None and (t.dtype != torch.float16 or t.shape != shape or not t.is_contiguous()):
+            raise ValueError("%s: scales and zero points [experts, %d, %d] and biases [experts, %d] in float16, contiguous, are wanted" % (what, N, nb, N))
+    return E
+
+
+def qmoe_tokens_fused(x, expert_ids, expert_weights, *, fc1_w, fc1_scales, fc1_zp, fc1_bias, fc2_w, fc2_scales, fc2_zp, fc2_bias, bits,
+                      block_size, y, swiglu_interleaved=0, status=None, workspace=None, stream=None, raw=False):
+    """The layer of qmoe_decode_fused over a few tokens, each with k experts of its own; every chosen expert's weights are read once.
+
+    x: [T, hidden] float16/bfloat16; expert_ids [T, k] int32 and expert_weights [T, k] float32 (T * k up to 1024); weights,
+    scales, zero points and biases as in qmoe_decode_fused; y: [T, hidden] float32/float16/bfloat16; status: a device int32
+    set to 1 by an id that is no expert, or None.
+    """
+    torch = _torch()
+    if x.dim() != 2 or y.shape != x.shape or not x.is_contiguous() or not y.is_contiguous():
+        raise ValueError("x and y: [tokens, hidden], contiguous, are wanted")
+    T, hidden = x.shape
+    if expert_ids.dim() != 2 or expert_ids.shape[0] != T or expert_ids.dtype != torch.int32 or expert_weights.shape != expert_ids.shape \
+            or expert_weights.dtype != torch.float32 or not expert_ids.is_contiguous() or not expert_weights.is_contiguous():
+        raise ValueError("expert_ids [tokens, k] int32 and expert_weights [tokens, k] float32 are wanted")
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status: an int32 is wanted")
+    k = expert_ids.shape[1]
+    inter = fc2_w.shape[-1] * 8 // bits
+    E = _expert_sizes(fc1_w, fc1_scales, fc1_zp, fc1_bias, 2 * inter, hidden, bits, block_size, "fc1")
+    if _expert_sizes(fc2_w, fc2_scales, fc2_zp, fc2_bias, hidden, inter, bits, block_size, "fc2") != E:
+        raise ValueError("fc1 and fc2: as many experts in both are wanted")
+    L = lib()
+    need = L.qmoe_tokens_workspace_bytes(T, k, hidden, inter) if workspace is None else 0
+    st, wp, wb, _ = _stream_and_workspace(need, workspace, x, stream)
+    s = L.qmoe_tokens_fused(x.data_ptr(), _dtype_code(x), expert_ids.data_ptr(), expert_weights.data_ptr(), T, k, E, fc1_w.data_ptr(),
+                            fc1_scales.data_ptr(), _addr(fc1_zp), _addr(fc1_bias), fc2_w.data_ptr(), fc2_scales.data_ptr(), _addr(fc2_zp),
+                            _addr(fc2_bias), hidden, inter, bits, block_size, 1 if swiglu_interleaved else 0, y.data_ptr(), _dtype_code(y), _addr(status), wp, wb, st)
+    return s if raw else _check(s, "qmoe_tokens_fused")
 
 
 def qg_read_device_fault() -> int:

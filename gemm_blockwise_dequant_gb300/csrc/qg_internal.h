@@ -272,6 +272,26 @@ struct TokenLogprobsGrad {
 };
 cudaError_t token_logprobs_grad(const TokenLogprobsGrad &q, cudaStream_t s);
 
+// A mixture-of-experts layer over a few tokens (validated requests; qg_moe_tokens.cu).
+cudaError_t route_topk(const void *logits, int dtype, int64_t ld, int T, int E, int k, int renormalize, int32_t *ids, float *weights, cudaStream_t s);
+struct MoeTokens {
+    const void *x;           // [T][hidden]
+    int x_dtype;
+    const int32_t *ids;      // [T][k]
+    const float *weights;    // [T][k]
+    int T, k, E;
+    const uint8_t *fc1_w;
+    const uint16_t *fc1_scales, *fc1_zp, *fc1_bias;
+    const uint8_t *fc2_w;
+    const uint16_t *fc2_scales, *fc2_zp, *fc2_bias;
+    int hidden, inter, bits, bs, interleaved;
+    void *y;
+    int y_dtype;
+    int *status;
+};
+size_t moe_tokens_workspace_bytes(int T, int k, int hidden, int inter);
+cudaError_t moe_tokens(const MoeTokens &q, void *ws, cudaStream_t s);
+
 // Utility kernels.
 cudaError_t launch_dequant(const GemmProblem &p, float *out, cudaStream_t s);
 cudaError_t launch_uniform_check(const uint16_t *t, size_t n, unsigned *ws, cudaStream_t s);

@@ -1,0 +1,9 @@
+// qg_moe_tokens_u4.cu -- the few-token expert products for 4-bit codes (qg_moe_tokens.cuh).
+#include "qg_moe_tokens.cuh"
+
+namespace qg {
+namespace moe {
+template cudaError_t launch_experts<4>(const Args &a, cudaStream_t s);
+template bool experts_fit<4>(int K, int bs, bool zp);
+}  // namespace moe
+}  // namespace qg

@@ -652,6 +652,40 @@ int qg_token_logprobs_grad(const void *X, int x_dtype, int64_t ldx, const int64_
                            void *dX, int64_t lddx, int rows, int vocab, qg_stream_t stream);
 
 /*
+ * qmoe_route_topk -- the experts of each token from its router logits (an addition of this library):
+ *   expert_ids[t] = the k largest of logits[t], the largest first, the lower index first among equals (NaN above all)
+ *   expert_weights[t][j] = exp(l_j - M) / sum exp(l_i - M), M the largest; the sum over the k chosen (renormalize = 1)
+ *   or over all experts (0).  An expert at -inf has weight 0, also where all of them are; a NaN or +inf among the
+ *   logits that are summed makes the token's weights NaN.
+ *   logits  [tokens] rows of num_experts values (1 .. 512), ld values apart, any of the three types;  k  1 .. 16
+ *   expert_ids [tokens][k] int32, expert_weights [tokens][k] fp32: as qmoe_tokens_fused and (a token) qmoe_decode_fused take them
+ *
+ * qmoe_tokens_fused -- the layer of qmoe_decode_fused over a few tokens at once, each with k experts of its own:
+ *   y[t] = round( sum_j expert_weights[t][j] * o_tj ),  o_tj as there, from x[t] and expert expert_ids[t][j]
+ * Every chosen expert's weights are read once for all its tokens (16 of them at a time; fewer where hidden or inter is
+ * above some 2,800).  Weights, scales, zero points, biases, block sizes and swiglu_interleaved as qmoe_decode_fused; bits 2, 4 or 8.
+ *   x            [tokens][hidden] fp16 or bf16 (fp32: QG_ERR_UNSUPPORTED)
+ *   expert_ids, expert_weights  [tokens][k] int32 and fp32 (device), k 1 .. 16, tokens * k at most 1024, num_experts at
+ *                most 512; an id outside [0, num_experts) adds nothing and sets *status_dev to 1 (it may be NULL and is
+ *                never cleared); one that a token has twice counts twice
+ *   y            [tokens][hidden] of y_dtype
+ *   workspace    at least qmoe_tokens_workspace_bytes(tokens, k, hidden, inter) bytes, 16-byte aligned
+ * Activations, and h between the products, enter the products as fp16 scaled by a power of two for each row (11 bits for
+ * what is above 2^-29 of the row's largest); codes, scales and zero points are exact; sums in fp32.  A row with an
+ * infinity or NaN gives outputs that are not finite, the other rows are not touched by it.
+ * Deterministic; the order of a sum depends on the shape and on how many experts were chosen.  A hidden or inter whose
+ * rows do not fit the kernel's shared memory (some 30,000 and more) is QG_ERR_UNSUPPORTED.  More tokens: qmoe_ragged_mm.
+ */
+int qmoe_route_topk(const void *logits, int dtype, int64_t ld, int tokens, int num_experts, int k, int renormalize,
+                    int32_t *expert_ids, float *expert_weights, qg_stream_t stream);
+size_t qmoe_tokens_workspace_bytes(int tokens, int k, int hidden, int inter);
+int qmoe_tokens_fused(const void *x, int x_dtype, const int32_t *expert_ids, const float *expert_weights, int tokens, int k,
+                      int num_experts, const uint8_t *fc1_w, const uint16_t *fc1_scales, const uint16_t *fc1_zp,
+                      const uint16_t *fc1_bias, const uint8_t *fc2_w, const uint16_t *fc2_scales, const uint16_t *fc2_zp,
+                      const uint16_t *fc2_bias, int hidden, int inter, int bits, int block_size, int swiglu_interleaved,
+                      void *y, int y_dtype, int *status_dev, void *workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/*
  * qg_read_device_fault -- every wait inside the library's kernels is
  * bounded; a wait that gives up records a bit in a device-side fault word
  * instead of hanging.  This call synchronises the current device, returns
