@@ -11,12 +11,13 @@
 //
 // Bound by memory.  The list is cut into chunks of 2048 values; a thread owns 8 neighbouring ones and a warp one
 // block of 256, so that a block's largest magnitude is a warp reduction.  With clipping a first launch reads the
-// gradients alone and leaves one sum of squares for each CTA; the second walks every CTA's run of chunks backwards,
-// where the L2 still holds the gradients that were read last.
+// gradients alone and leaves one sum of squares for each CTA; the second takes the chunks from the last one on, where
+// the L2 still holds the gradients that were read last.
 #include <cuda_fp8.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/qgemm.h"
 #include "qg_device.cuh"
@@ -25,55 +26,66 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kCtas = 4;                   // of an SM
+constexpr int kThreads = 256;              // of a group: a CTA is kGroups of them, one CTA on each SM
+constexpr int kGroups = 3;
 constexpr int kVals = 8;                   // of a thread
 constexpr int kChunk = kThreads * kVals;   // values
-constexpr float kCodeMax = 448.f, kCodeMin = 0.001953125f;  // e4m3: the largest value, the smallest above zero
+constexpr float kCodeMax = 448.f;          // the largest e4m3 value
 constexpr float kTinyBlock = 1e-30f;       // a block with no larger magnitude is stored as zeros (448 / it stays finite)
 
-// The tensor owning chunk c: the last one with first_chunk <= c (the block counts them).
-__device__ int find_tensor(const qg_adamw_tensor *list, int count, int64_t c) {
-    int n = 0;
-    for (int i = 0; i < count; i += kThreads)
-        n += __syncthreads_count(i + static_cast<int>(threadIdx.x) < count && list[i + threadIdx.x].first_chunk <= c);
-    return n - 1;
+__device__ __forceinline__ uint4 load128(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
 
-// Eight values at element e of an array (n: those that exist), zero where there are none.
-__device__ __forceinline__ void load8(const void *base, int dtype, int64_t e, int n, float (&x)[8]) {
-    if (dtype == 0) {
-        const float *p = static_cast<const float *>(base) + e;
-        if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-            const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = k < n ? p[k] : 0.f;
-        }
-        return;
+// Eight values at element e of an array as they lie there (n: those that exist, zero where there are none): one vector
+// of 16-bit values, two of fp32.  They become numbers apart from this, so that a thread's loads are all on their way
+// before it waits for the first.  WIDE: eight there, at whole vectors.
+struct Eight {
+    uint4 a, b;
+};
+template <bool WIDE>
+__device__ __forceinline__ Eight raw8(const void *base, int dtype, int64_t e, int n) {
+    Eight r;
+    const char *p = static_cast<const char *>(base) + e * (dtype == 0 ? 4 : 2);
+    if constexpr (WIDE) {
+        r.a = load128(p);
+        if (dtype == 0) r.b = load128(p + 16);
+        return r;
     }
-    const uint16_t *p = static_cast<const uint16_t *>(base) + e;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (dtype == 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) w[k] = reinterpret_cast<const uint32_t *>(p)[k];
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k < n) w[k >> 1] |= static_cast<uint32_t>(p[k]) << (16 * (k & 1));
+            if (k < n) w[k >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[k]) << (16 * (k & 1));
     }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]), r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    return r;
+}
+__device__ __forceinline__ void numbers(const Eight &r, int dtype, float (&x)[8]) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (dtype == 0) {  // the types apart: a choice of each value would convert it every way
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (dtype == 1) x[2 * i] = h2f(static_cast<uint16_t>(w[i] & 0xFFFFu)), x[2 * i + 1] = h2f(static_cast<uint16_t>(w[i] >> 16));
-        else x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(w[k]);
+    } else if (dtype == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = h2f(static_cast<uint16_t>(w[i] & 0xFFFFu)), x[2 * i + 1] = h2f(static_cast<uint16_t>(w[i] >> 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
 
+template <bool WIDE = false>
 __device__ __forceinline__ void store8(void *base, int dtype, int64_t e, int n, const float (&x)[8]) {
     if (dtype == 0) {
         float *p = static_cast<float *>(base) + e;
-        if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        if (WIDE || (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
             reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
             reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
         } else {
@@ -85,10 +97,20 @@ __device__ __forceinline__ void store8(void *base, int dtype, int64_t e, int n, 
     }
     uint16_t *p = static_cast<uint16_t *>(base) + e;
     uint32_t w[4];
+    if (dtype == 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = dtype == 1 ? f2h(x[2 * i]) | static_cast<uint32_t>(f2h(x[2 * i + 1])) << 16 : f2bf(x[2 * i]) | static_cast<uint32_t>(f2bf(x[2 * i + 1])) << 16;
-    if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    if (WIDE || (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
@@ -98,18 +120,24 @@ __device__ __forceinline__ void store8(void *base, int dtype, int64_t e, int n, 
 }
 
 // Eight e4m3 codes.
+template <bool WIDE>
 __device__ __forceinline__ uint2 load_codes(const void *base, int64_t e, int n) {
     const uint8_t *p = static_cast<const uint8_t *>(base) + e;
-    if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) return *reinterpret_cast<const uint2 *>(p);
+    if constexpr (WIDE) {
+        uint2 v;
+        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+        return v;
+    }
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (k < n) w[k >> 2] |= static_cast<uint32_t>(p[k]) << (8 * (k & 3));
     return make_uint2(w[0], w[1]);
 }
+template <bool WIDE>
 __device__ __forceinline__ void store_codes(void *base, int64_t e, int n, uint2 c) {
     uint8_t *p = static_cast<uint8_t *>(base) + e;
-    if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) {
+    if (WIDE || (n == 8 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0)) {
         *reinterpret_cast<uint2 *>(p) = c;
         return;
     }
@@ -118,69 +146,208 @@ __device__ __forceinline__ void store_codes(void *base, int64_t e, int n, uint2 
     for (int k = 0; k < 8; ++k)
         if (k < n) p[k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
 }
-__device__ __forceinline__ void decode(uint2 c, float scale, float (&x)[8]) {
+__device__ __forceinline__ void decode(uint2 c, float (&x)[8]) {
     const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-        x[2 * i] = h2f(h.x) * scale, x[2 * i + 1] = h2f(h.y) * scale;
+        x[2 * i] = h2f(h.x), x[2 * i + 1] = h2f(h.y);
     }
 }
+// The largest of a warp's values that are not negative (a NaN is one: its bits are above all).
+__device__ __forceinline__ float warp_top(float x) { return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(x))); }
+
+// To a unit in the last place; of 2^126 and more 0.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two products at a time (packed fp32).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Codes of x / scale for the warp's block of 256 values; scale is what goes with them.
 template <bool KEEP>
 __device__ __forceinline__ uint2 encode(const float (&x)[8], float &scale) {
     float top = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    // infinities and NaN: the codes of the others are zeros, and the state shows it (0 * inf is NaN)
-    const float inv = top >= kTinyBlock ? kCodeMax / top : 0.f;
-    scale = top >= kTinyBlock ? top / kCodeMax : 0.f;
+    top = warp_top(top);
+    // infinities: the codes of the others are zeros, and the state shows it (0 * inf is NaN); a NaN is a code of its own
+    const float inv = top >= kTinyBlock ? kCodeMax * 0.25f * reciprocal(top * 0.25f) : 0.f;
+    scale = top >= kTinyBlock ? top * (1.f / kCodeMax) : 0.f;
     uint32_t w[2] = {0, 0};
+    float2 y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
-        if constexpr (KEEP) {
-            a = a > 0.f ? fmaxf(a, kCodeMin) : a;
-            b = b > 0.f ? fmaxf(b, kCodeMin) : b;
+    for (int i = 0; i < 4; ++i) y[i] = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(inv));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(y[i].x, y[i].y), __NV_SATFINITE, __NV_E4M3)) << (16 * (i & 1));
+    if constexpr (KEEP) {  // what is above zero stays above
+        if (((w[0] - 0x01010101u) & ~w[0] & 0x80808080u) | ((w[1] - 0x01010101u) & ~w[1] & 0x80808080u)) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (x[k] * inv > 0.f && !(w[k >> 2] >> (8 * (k & 3)) & 0xFFu)) w[k >> 2] |= 1u << (8 * (k & 3));
         }
-        w[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) << (16 * (i & 1));
     }
     return make_uint2(w[0], w[1]);
 }
 
+// A root to a few units in the last place; below 2^-126 it is 0, which eps hides.
+__device__ __forceinline__ float root(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The list as a CTA sees it: in shared memory where it fits, else where it lies.  The chunks of all tensors, one after
+// another, are dealt out in turn, so that all of them work side by side in memory: each with a run of its own they
+// would open as many DRAM pages at a time as there are CTAs and arrays (55.7 million values with 8-bit states: 153 us, 93
+// side by side).  Every warp looks up each chunk's tensor.
+constexpr int kTable = 1024;  // entries in shared memory
+struct Where {
+    const qg_adamw_tensor *t;
+    int64_t e;  // this thread's first value
+    int kind;
+};
+enum Kind { ANY, WIDE_F32, WIDE_E4M3, WIDE_E4M3_F16, WIDE_E4M3_BF16 };  // WIDE: a whole chunk, every array at whole vectors
+
+__device__ __forceinline__ int kind_of(const qg_adamw_tensor &t) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad) | reinterpret_cast<uintptr_t>(t.master);
+    const uintptr_t states = reinterpret_cast<uintptr_t>(t.exp_avg) | reinterpret_cast<uintptr_t>(t.exp_avg_sq);
+    if ((all & 15u) != 0 || (states & (t.state == QG_STATE_E4M3 ? 7u : 15u)) != 0) return ANY;
+    if (t.state != QG_STATE_E4M3) return WIDE_F32;
+    if (t.master || t.param_dtype == 0 || t.param_dtype != t.grad_dtype) return WIDE_E4M3;
+    return t.param_dtype == 1 ? WIDE_E4M3_F16 : WIDE_E4M3_BF16;
+}
+
+struct List {
+    const qg_adamw_tensor *t;  // shared or global
+    const int *kinds;          // or null
+    int count;
+
+    // Copies the list to `room` (kTable entries and their kinds) where it fits; all threads call it.
+    __device__ __forceinline__ List(const qg_adamw_tensor *list, int n, char *room) : t(list), kinds(nullptr), count(n) {
+        if (n > kTable) return;
+        constexpr int W = sizeof(qg_adamw_tensor) / 8;
+        uint64_t *to = reinterpret_cast<uint64_t *>(room);
+        for (int i = threadIdx.x; i < n * W; i += kThreads * kGroups) to[i] = reinterpret_cast<const uint64_t *>(list)[i];
+        __syncthreads();
+        t = reinterpret_cast<const qg_adamw_tensor *>(room);
+        int *k = reinterpret_cast<int *>(room + n * sizeof(qg_adamw_tensor));
+        for (int i = threadIdx.x; i < n; i += kThreads * kGroups) k[i] = kind_of(t[i]);
+        __syncthreads();
+        kinds = k;
+    }
+    // The tensor owning chunk c: the last one with first_chunk <= c (a warp finds it, 32 steps at a time).
+    __device__ __forceinline__ int find(int64_t c) const {
+        const int lane = threadIdx.x & 31;
+        int lo = 0, n = count;
+        while (n > 1) {
+            const int step = (n + 31) / 32, i = lo + lane * step;
+            const unsigned who = __ballot_sync(~0u, lane * step < n && t[i].first_chunk <= c);  // ones first
+            const int last = __popc(who) - 1;
+            n = min(step, n - last * step);
+            lo += last * step;
+        }
+        return lo;
+    }
+    __device__ __forceinline__ Where place(int i, int64_t c) const {
+        Where w;
+        w.t = t + i;
+        const int64_t in = c - w.t->first_chunk;
+        w.e = in * kChunk + threadIdx.x % kThreads * kVals;
+        w.kind = (in + 1) * kChunk > w.t->numel ? ANY : kinds ? kinds[i] : kind_of(*w.t);
+        return w;
+    }
+};
+int list_bytes(int count) { return count > kTable ? 0 : (count * (static_cast<int>(sizeof(qg_adamw_tensor)) + 4) + 15) / 16 * 16; }
+
+// The sum of squares of eight values in fp32, or in fp64 where that leaves its range.
+__device__ __forceinline__ double squares(const float (&g)[8]) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k & 1] = fmaf(g[k], g[k], s[k & 1]);
+    const float sum = s[0] + s[1];
+    if (sum >= 1e-30f && sum <= 3e38f) return sum;
+    double wide = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) wide += static_cast<double>(g[k]) * g[k];
+    return wide;
+}
+
+// The sum of squares of whole chunks of one tensor, of eight at most (four of fp32): all loads of a thread together.
+template <int DT>
+__device__ __forceinline__ double squares_of_some(const void *grad, int64_t e, int chunks) {
+    constexpr int U = DT == 0 ? 2 : 1, N = 8 / U;
+    uint4 v[N][U];
+    const char *p = static_cast<const char *>(grad) + e * (DT == 0 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[i][u] = i < chunks ? load128(p + i * (kChunk * (DT == 0 ? 4 : 2)) + u * 16) : make_uint4(0, 0, 0, 0);
+    double total = 0.0;
+    float s = 0.f;
+    bool fits = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float g[8], q[2] = {0.f, 0.f};
+        numbers({v[i][0], v[i][U - 1]}, DT, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k & 1] = fmaf(g[k], g[k], q[k & 1]);
+        const float sum = q[0] + q[1];
+        fits = fits && ((sum >= 1e-30f && sum <= 3e37f) || i >= chunks);
+        s += sum;
+    }
+    if (fits) return s;
+#pragma unroll 1
+    for (int i = 0; i < chunks; ++i) {  // again, one by one
+        float g[8];
+        numbers(raw8<true>(grad, DT, e + static_cast<int64_t>(i) * kChunk, 8), DT, g);
+        total += squares(g);
+    }
+    return total;
+}
+
 // One sum of squares for each CTA.
-__global__ void __launch_bounds__(kThreads, kCtas) sumsq_kernel(const qg_adamw_tensor *__restrict__ list, int count, int64_t chunks,
+__global__ void __launch_bounds__(kThreads * kGroups, 1) sumsq_kernel(const qg_adamw_tensor *__restrict__ list, int count, int64_t chunks,
                                                                double *__restrict__ partial) {
-    __shared__ double red[kThreads / 32];
+    __shared__ double red[kThreads * kGroups / 32];
+    extern __shared__ __align__(16) char room[];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
     double total = 0.0;
-    if (c0 < c1) {
-        int at = find_tensor(list, count, c0);
-        int64_t next = at + 1 < count ? list[at + 1].first_chunk : chunks;
-        for (int64_t c = c0; c < c1; ++c) {
-            if (c >= next) {
-                while (at + 1 < count && list[at + 1].first_chunk <= c) ++at;
-                next = at + 1 < count ? list[at + 1].first_chunk : chunks;
-            }
-            const qg_adamw_tensor &t = list[at];
-            const int64_t e = (c - t.first_chunk) * kChunk + threadIdx.x * kVals;
-            const int64_t left = t.numel - e;
-            float g[8];
-            if (left > 0) load8(t.grad, t.grad_dtype, e, left < 8 ? static_cast<int>(left) : 8, g);
-            if (left <= 0) continue;
-            float s[2] = {0.f, 0.f};
-            bool any = false;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s[k & 1] = fmaf(g[k], g[k], s[k & 1]), any |= g[k] != 0.f;
-            const float sum = s[0] + s[1];
-            if (sum >= 1e-30f && sum <= 3e38f) {
-                total += sum;
-            } else if (any) {  // squares that leave fp32's range
-#pragma unroll
-                for (int k = 0; k < 8; ++k) total += static_cast<double>(g[k]) * g[k];
+    const int64_t groups = (chunks + 7) / 8;
+    {
+        const List l(list, count, room);
+        for (int64_t gr = blockIdx.x * kGroups + threadIdx.x / kThreads; gr < groups; gr += gridDim.x * kGroups) {
+            const int64_t end = std::min<int64_t>(chunks, gr * 8 + 8);
+            for (int64_t c = gr * 8; c < end;) {
+                const Where w = l.place(l.find(c), c);
+                const qg_adamw_tensor &t = *w.t;
+                const int64_t whole = t.first_chunk + t.numel / kChunk;  // up to here its chunks are
+                const void *grad = t.grad;
+                const int dt = t.grad_dtype;
+                if (c < whole && (reinterpret_cast<uintptr_t>(grad) & 15u) == 0) {
+                    const int some = static_cast<int>(std::min<int64_t>(std::min(whole, end) - c, dt == 0 ? 4 : 8));
+                    total += dt == 0 ? squares_of_some<0>(grad, w.e, some) : dt == 1 ? squares_of_some<1>(grad, w.e, some) : squares_of_some<2>(grad, w.e, some);
+                    c += some;
+                    continue;
+                }
+                const int64_t left = t.numel - w.e;
+                if (left > 0) {
+                    float g[8];
+                    numbers(raw8<false>(grad, dt, w.e, left < 8 ? static_cast<int>(left) : 8), dt, g);
+                    total += squares(g);
+                }
+                ++c;
             }
         }
     }
@@ -189,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sumsq_kernel(const qg_adamw_t
     __syncthreads();
     if (threadIdx.x == 0) {
         total = 0.0;
-        for (int w = 0; w < kThreads / 32; ++w) total += red[w];
+        for (int w = 0; w < kThreads * kGroups / 32; ++w) total += red[w];
         partial[blockIdx.x] = total;
     }
 }
@@ -198,7 +365,7 @@ struct StepArgs {
     const qg_adamw_tensor *list;
     int count;
     int64_t chunks;
-    float lr, beta1, beta2, keep1, keep2, ln1, ln2, eps;  // keep = 1 - beta, ln = log(beta)
+    float lr, beta1, beta2, root2, keep1, keep2, ln1, ln2, eps;  // root2 = sqrt(beta2), keep1 = 1 - beta1, keep2 = sqrt(1 - beta2), ln = log(beta)
     const float *lr_dev;
     float step;
     const int64_t *step_dev;
@@ -208,9 +375,167 @@ struct StepArgs {
     float *norm;
 };
 
-__global__ void __launch_bounds__(kThreads, kCtas) step_kernel(const __grid_constant__ StepArgs p) {
+// What a step multiplies with.
+struct Rates {
+    float g1, g2;             // of a gradient in m' and in the root of its part of v': (1 - b1) c, sqrt(1 - b2) c
+    float rate, widen, lr;    // lr / (1 - b1^step), 1 / sqrt(1 - b2^step)
+};
+
+// What a thread reads of a chunk.
+struct Raw {
+    Eight w, g, m, v;
+    uint2 cm, cv;
+    float sm, sv;
+};
+template <bool WIDE, bool EIGHT>
+__device__ __forceinline__ void fetch8(Raw &x, const qg_adamw_tensor &t, int64_t e, int n) {
+    x.g = raw8<WIDE>(t.grad, t.grad_dtype, e, n);
+    x.w = t.master ? raw8<WIDE>(t.master, 0, e, n) : raw8<WIDE>(t.param, t.param_dtype, e, n);
+    if constexpr (EIGHT) {
+        x.cm = load_codes<WIDE>(t.exp_avg, e, n), x.cv = load_codes<WIDE>(t.exp_avg_sq, e, n);
+        const int64_t block = e >> 8;
+        const bool there = WIDE || block << 8 < t.numel;
+        x.sm = there ? t.exp_avg_scale[block] : 0.f, x.sv = there ? t.exp_avg_sq_scale[block] : 0.f;
+    } else {
+        x.m = raw8<WIDE>(t.exp_avg, 0, e, n);
+        x.v = raw8<WIDE>(t.exp_avg_sq, 0, e, n);
+    }
+}
+
+// What a step multiplies with, twice each.
+struct Factors {
+    float2 b1, b2, g1, g2, rate, widen, eps, decay;
+};
+// The step of two values: w, m and v are replaced, u is the root of v'.  EIGHT: m comes as a code (b1 holds its scale too),
+// v as that of its root (b2: with sqrt(beta2)).
+template <bool EIGHT>
+__device__ __forceinline__ void step2(const Factors &f, float2 &w, float2 g, float2 &m, float2 &v, float2 &u) {
+    const float2 a = mul2(g, f.g2), aa = mul2(a, a);
+    m = ffma2(f.b1, m, mul2(g, f.g1));
+    if constexpr (EIGHT) {
+        const float2 old = mul2(v, f.b2);
+        v = ffma2(old, old, aa);
+    } else {
+        v = ffma2(f.b2, v, aa);
+    }
+    u = make_float2(root(v.x), root(v.y));
+    const float2 d = ffma2(u, f.widen, f.eps);
+    w = ffma2(mul2(m, make_float2(reciprocal(d.x), reciprocal(d.y))), f.rate, mul2(w, f.decay));
+}
+__device__ __forceinline__ Factors factors(const StepArgs &p, const Rates &r, float weight_decay) {
+    return {both(p.beta1), both(p.beta2), both(r.g1), both(r.g2), both(-r.rate), both(r.widen), both(p.eps), both(fmaf(-r.lr, weight_decay, 1.f))};
+}
+
+// The step of eight values, n of them there, and their stores.  WIDE: all there, at whole vectors.
+template <bool WIDE, bool EIGHT>
+__device__ __forceinline__ void step8(const Raw &x, const qg_adamw_tensor &t, const StepArgs &p, const Rates &r, int64_t e, int n) {
+    float w[8], g[8], m[8], v[8], u[8];
+    numbers(x.g, t.grad_dtype, g);
+    numbers(x.w, t.master ? 0 : t.param_dtype, w);
+    Factors f = factors(p, r, t.weight_decay);
+    if constexpr (EIGHT) {
+        f.b1 = both(p.beta1 * x.sm), f.b2 = both(p.root2 * x.sv);
+        decode(x.cm, m);
+        decode(x.cv, v);
+    } else {
+        numbers(x.m, 0, m);
+        numbers(x.v, 0, v);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        float2 w2 = make_float2(w[k], w[k + 1]), m2 = make_float2(m[k], m[k + 1]), v2 = make_float2(v[k], v[k + 1]), u2;
+        step2<EIGHT>(f, w2, make_float2(g[k], g[k + 1]), m2, v2, u2);
+        w[k] = w2.x, w[k + 1] = w2.y, m[k] = m2.x, m[k + 1] = m2.y, v[k] = v2.x, v[k + 1] = v2.y, u[k] = u2.x, u[k + 1] = u2.y;
+    }
+    store8<WIDE>(t.param, t.param_dtype, e, n, w);
+    if (t.master) store8<WIDE>(t.master, 0, e, n, w);
+    if constexpr (EIGHT) {
+        const int64_t block = e >> 8;
+        float sm, sv;
+        const uint2 cm = encode<false>(m, sm), cv = encode<true>(u, sv);
+        store_codes<WIDE>(t.exp_avg, e, n, cm);
+        store_codes<WIDE>(t.exp_avg_sq, e, n, cv);
+        if ((threadIdx.x & 31) == 0 && n > 0) {
+            t.exp_avg_scale[block] = sm;
+            t.exp_avg_sq_scale[block] = sv;
+        }
+    } else {
+        store8<WIDE>(t.exp_avg, 0, e, n, m);
+        store8<WIDE>(t.exp_avg_sq, 0, e, n, v);
+    }
+}
+
+// A whole chunk of a tensor with 8-bit states, and parameters and gradients of one 16-bit type, at whole vectors.  There is
+// as much to compute here as to move, so that the next chunks are on their way meanwhile.
+struct Half {
+    uint4 w, g;
+    uint2 m, v;
+    float sm, sv;
+};
+// The chunks to come wait in shared memory, each thread's values in places of its own (so nobody waits for anybody).
+constexpr int kAhead = 3;                                      // places
+constexpr int kSlot = kThreads * kGroups * (16 + 16 + 8 + 8 + 4 + 4);
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from, std::integral_constant<int, 16>) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from, std::integral_constant<int, N>) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
+}
+struct Places {  // of this thread in slot 0
+    uint32_t wg, mv, s;
+    __device__ __forceinline__ Places(uint32_t ring) {
+        const uint32_t all = kThreads * kGroups;
+        wg = ring + threadIdx.x * 16, mv = ring + all * 32 + threadIdx.x * 8, s = ring + all * 48 + threadIdx.x * 4;
+    }
+};
+__device__ __forceinline__ void request_half(const Places &p, uint32_t slot, const Where &at) {
+    constexpr uint32_t all = kThreads * kGroups;
+    const qg_adamw_tensor &t = *at.t;
+    copy_async(p.wg + slot, static_cast<const char *>(t.param) + at.e * 2, std::integral_constant<int, 16>{});
+    copy_async(p.wg + slot + all * 16, static_cast<const char *>(t.grad) + at.e * 2, std::integral_constant<int, 16>{});
+    copy_async(p.mv + slot, static_cast<const char *>(t.exp_avg) + at.e, std::integral_constant<int, 8>{});
+    copy_async(p.mv + slot + all * 8, static_cast<const char *>(t.exp_avg_sq) + at.e, std::integral_constant<int, 8>{});
+    copy_async(p.s + slot, t.exp_avg_scale + (at.e >> 8), std::integral_constant<int, 4>{});
+    copy_async(p.s + slot + all * 4, t.exp_avg_sq_scale + (at.e >> 8), std::integral_constant<int, 4>{});
+}
+__device__ __forceinline__ Half receive_half(const Places &p, uint32_t slot) {
+    constexpr uint32_t all = kThreads * kGroups;
+    Half x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.w.x), "=r"(x.w.y), "=r"(x.w.z), "=r"(x.w.w) : "r"(p.wg + slot) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.g.x), "=r"(x.g.y), "=r"(x.g.z), "=r"(x.g.w) : "r"(p.wg + slot + all * 16) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.m.x), "=r"(x.m.y) : "r"(p.mv + slot) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.v.x), "=r"(x.v.y) : "r"(p.mv + slot + all * 8) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x.sm) : "r"(p.s + slot) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x.sv) : "r"(p.s + slot + all * 4) : "memory");
+    return x;
+}
+template <int DT>
+__device__ __forceinline__ void step_half(const Half &x, const Where &at, const StepArgs &p, const Rates &r) {
+    const qg_adamw_tensor &t = *at.t;
+    Factors f = factors(p, r, t.weight_decay);
+    f.b1 = both(p.beta1 * x.sm), f.b2 = both(p.root2 * x.sv);
+    float m[8], u[8], w[8], g[8];
+    numbers({x.w, x.w}, DT, w);
+    numbers({x.g, x.g}, DT, g);
+    decode(x.m, m);
+    decode(x.v, u);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        float2 w2 = make_float2(w[k], w[k + 1]), m2 = make_float2(m[k], m[k + 1]), v2 = make_float2(u[k], u[k + 1]), u2;
+        step2<true>(f, w2, make_float2(g[k], g[k + 1]), m2, v2, u2);
+        w[k] = w2.x, w[k + 1] = w2.y, m[k] = m2.x, m[k + 1] = m2.y, u[k] = u2.x, u[k + 1] = u2.y;
+    }
+    store8<true>(t.param, DT, at.e, 8, w);
+    float s0, s1;
+    store_codes<true>(t.exp_avg, at.e, 8, encode<false>(m, s0));
+    store_codes<true>(t.exp_avg_sq, at.e, 8, encode<true>(u, s1));
+    if ((threadIdx.x & 31) == 0) t.exp_avg_scale[at.e >> 8] = s0, t.exp_avg_sq_scale[at.e >> 8] = s1;
+}
+
+__global__ void __launch_bounds__(kThreads * kGroups, 1) step_kernel(const __grid_constant__ StepArgs p) {
     __shared__ float factor;
-    const int64_t c0 = p.chunks * blockIdx.x / gridDim.x, c1 = p.chunks * (blockIdx.x + 1) / gridDim.x;
+    extern __shared__ __align__(16) char room[];
     pdl_launch_dependents();
     pdl_wait();
     float clip = 1.f;
@@ -230,67 +555,64 @@ __global__ void __launch_bounds__(kThreads, kCtas) step_kernel(const __grid_cons
         clip = factor;
         if (clip < 0.f) return;  // a norm that is infinite or NaN: no step
     }
-    if (c0 >= c1) return;
-    const float lr = p.lr_dev ? *p.lr_dev : p.lr, step = p.step_dev ? fmaxf(static_cast<float>(*p.step_dev), 1.f) : p.step;
-    const float rate = lr / -expm1f(step * p.ln1);                  // lr / (1 - b1^step)
-    const float widen = rsqrtf(-expm1f(step * p.ln2));              // 1 / sqrt(1 - b2^step)
-    int at = find_tensor(p.list, p.count, c1 - 1);
-    qg_adamw_tensor t = p.list[at];
-    for (int64_t c = c1 - 1; c >= c0; --c) {
-        if (c < t.first_chunk) {
-            do --at;
-            while (p.list[at].first_chunk > c || p.list[at].numel == 0);  // an empty tensor owns no chunk
-            t = p.list[at];
+    if (static_cast<int64_t>(blockIdx.x) * kGroups >= p.chunks) return;
+    Rates r;
+    r.g1 = p.keep1 * clip;
+    r.g2 = p.keep2 * clip;
+    r.lr = p.lr_dev ? *p.lr_dev : p.lr;
+    const float step = p.step_dev ? fmaxf(static_cast<float>(*p.step_dev), 1.f) : p.step;
+    r.rate = r.lr / -expm1f(step * p.ln1);
+    r.widen = rsqrtf(-expm1f(step * p.ln2));
+    const List l(p.list, p.count, room + kAhead * kSlot);
+    // from the last chunk on: the gradients that the norm's launch read last are still in the L2
+    const int64_t step_back = static_cast<int64_t>(gridDim.x) * kGroups;
+    int64_t c = p.chunks - 1 - (static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / kThreads);  // the next to be asked for
+    const Places mine(smem_u32(room));
+    const auto request = [&](uint32_t slot) {
+        Where w{};
+        if (c >= 0) {
+            w = l.place(l.find(c), c);
+            if (w.kind >= WIDE_E4M3_F16) request_half(mine, slot, w);
         }
-        const int64_t e = (c - t.first_chunk) * kChunk + threadIdx.x * kVals;
-        const int64_t left = t.numel - e;
-        const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
-        float w[8], g[8], m[8], v[8];
-        const bool eight = t.state == QG_STATE_E4M3;
-        const int64_t block = e >> 8;
-        load8(t.grad, t.grad_dtype, e, n, g);
-        if (t.master) load8(t.master, 0, e, n, w);
-        else load8(t.param, t.param_dtype, e, n, w);
-        if (eight) {
-            const bool there = (block << 8) < t.numel;
-            decode(load_codes(t.exp_avg, e, n), there ? t.exp_avg_scale[block] : 0.f, m);
-            decode(load_codes(t.exp_avg_sq, e, n), there ? t.exp_avg_sq_scale[block] : 0.f, v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= v[k];
+        c -= step_back;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return w;
+    };
+    Where at = request(0), then = request(kSlot);
+    uint32_t slot = 0;
+    while (at.t) {
+        const Where last = request(slot == 0 ? 2 * kSlot : slot - kSlot);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const qg_adamw_tensor &t = *at.t;
+        Raw x;
+        if (at.kind == WIDE_E4M3_F16) {
+            step_half<1>(receive_half(mine, slot), at, p, r);
+        } else if (at.kind == WIDE_E4M3_BF16) {
+            step_half<2>(receive_half(mine, slot), at, p, r);
+        } else if (at.kind == WIDE_F32) {
+            fetch8<true, false>(x, t, at.e, 8);
+            step8<true, false>(x, t, p, r, at.e, 8);
+        } else if (at.kind == WIDE_E4M3) {
+            fetch8<true, true>(x, t, at.e, 8);
+            step8<true, true>(x, t, p, r, at.e, 8);
         } else {
-            load8(t.exp_avg, 0, e, n, m);
-            load8(t.exp_avg_sq, 0, e, n, v);
-        }
-        const float decay = fmaf(-lr, t.weight_decay, 1.f);
-        float u[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float gk = g[k] * clip;
-            m[k] = fmaf(p.beta1, m[k], p.keep1 * gk);
-            v[k] = fmaf(p.beta2, v[k], p.keep2 * gk * gk);
-            u[k] = sqrtf(v[k]);
-            w[k] = fmaf(w[k], decay, -rate * m[k] / fmaf(u[k], widen, p.eps));
-        }
-        store8(t.param, t.param_dtype, e, n, w);
-        if (t.master) store8(t.master, 0, e, n, w);
-        if (eight) {
-            float sm, su;
-            const uint2 cm = encode<false>(m, sm), cu = encode<true>(u, su);
-            store_codes(t.exp_avg, e, n, cm);
-            store_codes(t.exp_avg_sq, e, n, cu);
-            if ((threadIdx.x & 31) == 0 && n > 0) {
-                t.exp_avg_scale[block] = sm;
-                t.exp_avg_sq_scale[block] = su;
+            const int64_t left = t.numel - at.e;
+            const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+            if (t.state == QG_STATE_E4M3) {
+                fetch8<false, true>(x, t, at.e, n);
+                step8<false, true>(x, t, p, r, at.e, n);
+            } else {
+                fetch8<false, false>(x, t, at.e, n);
+                step8<false, false>(x, t, p, r, at.e, n);
             }
-        } else {
-            store8(t.exp_avg, 0, e, n, m);
-            store8(t.exp_avg_sq, 0, e, n, v);
         }
+        at = then, then = last;
+        slot = slot == 2 * kSlot ? 0 : slot + kSlot;
     }
 }
 
 int parts_of(int64_t chunks) {
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, device_info().sm_count * kCtas)));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((chunks + kGroups - 1) / kGroups, device_info().sm_count)));
 }
 
 }  // namespace
@@ -302,8 +624,16 @@ size_t adamw_workspace_bytes(int64_t chunks) { return sizeof(double) * parts_of(
 cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s) {
     const qg_adamw_tensor *list = static_cast<const qg_adamw_tensor *>(q.list);
     const int parts = parts_of(q.chunks);
+    static std::atomic<unsigned long long> done{0};  // a bit for each device
+    const int slot = device_slot();
+    if (slot < 0 || !(done.load(std::memory_order_relaxed) >> slot & 1)) {
+        cudaError_t e = cudaFuncSetAttribute(step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAhead * kSlot + list_bytes(kTable));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(sumsq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, list_bytes(kTable));
+        if (e != cudaSuccess) return e;
+        if (slot >= 0) done.fetch_or(1ull << slot, std::memory_order_relaxed);
+    }
     if (q.clip) {
-        const cudaError_t e = launch_pdl(sumsq_kernel, dim3(parts), dim3(kThreads), 0, s, list, q.count, q.chunks, static_cast<double *>(ws));
+        const cudaError_t e = launch_pdl(sumsq_kernel, dim3(parts), dim3(kThreads * kGroups), list_bytes(q.count), s, list, q.count, q.chunks, static_cast<double *>(ws));
         if (e != cudaSuccess) return e;
     }
     if (q.chunks == 0 && !(q.clip && q.norm)) return cudaSuccess;
@@ -315,7 +645,8 @@ cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s) {
     a.beta1 = static_cast<float>(q.beta1);
     a.beta2 = static_cast<float>(q.beta2);
     a.keep1 = static_cast<float>(1.0 - q.beta1);
-    a.keep2 = static_cast<float>(1.0 - q.beta2);
+    a.keep2 = static_cast<float>(std::sqrt(1.0 - q.beta2));
+    a.root2 = static_cast<float>(std::sqrt(q.beta2));
     a.ln1 = static_cast<float>(std::log(q.beta1));  // -inf for 0: 1 - 0^step is 1
     a.ln2 = static_cast<float>(std::log(q.beta2));
     a.eps = static_cast<float>(q.eps);
@@ -327,7 +658,7 @@ cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s) {
     a.max_norm = q.max_norm;
     a.norm_eps = q.norm_eps;
     a.norm = q.norm;
-    const cudaError_t e = launch_pdl(step_kernel, dim3(parts), dim3(kThreads), 0, s, a);
+    const cudaError_t e = launch_pdl(step_kernel, dim3(parts), dim3(kThreads * kGroups), kAhead * kSlot + list_bytes(q.count), s, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
