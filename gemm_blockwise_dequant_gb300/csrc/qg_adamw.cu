@@ -9,15 +9,14 @@
 // magnitude / 448): u' needs half of v's range of exponents, which e4m3 has.  The step itself uses m' and u' before
 // that rounding.  A u' above zero is never stored as zero, which m' / u' of a later step could not bear.
 //
-// Bound by memory.  The list is cut into chunks of 2048 values; a thread owns 8 neighbouring ones and a warp one
-// block of 256, so that a block's largest magnitude is a warp reduction.  With clipping a first launch reads the
+// Bound by memory.  The list is cut into chunks of 4096 values; a thread owns 8 neighbouring ones and a warp one
+// block of 256 at a time, so that a block's largest magnitude is a warp reduction.  With clipping a first launch reads the
 // gradients alone and leaves one sum of squares for each CTA; the second takes the chunks from the last one on, where
 // the L2 still holds the gradients that were read last.
 #include <cuda_fp8.h>
 
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "../../include/qgemm.h"
 #include "qg_device.cuh"
@@ -29,7 +28,8 @@ namespace {
 constexpr int kThreads = 256;              // of a group: a CTA is kGroups of them, one CTA on each SM
 constexpr int kGroups = 3;
 constexpr int kVals = 8;                   // of a thread
-constexpr int kChunk = kThreads * kVals;   // values
+constexpr int kPart = kThreads * kVals;    // values that a group takes at a time
+constexpr int kChunk = 2 * kPart;          // looked up at a time
 constexpr float kCodeMax = 448.f;          // the largest e4m3 value
 constexpr float kTinyBlock = 1e-30f;       // a block with no larger magnitude is stored as zeros (448 / it stays finite)
 
@@ -207,17 +207,23 @@ __device__ __forceinline__ float root(float x) {
     return y;
 }
 
-// The list as a CTA sees it: in shared memory where it fits, else where it lies.  The chunks of all tensors, one after
-// another, are dealt out in turn, so that all of them work side by side in memory: each with a run of its own they
-// would open as many DRAM pages at a time as there are CTAs and arrays (55.7 million values with 8-bit states: 153 us, 93
-// side by side).  Every warp looks up each chunk's tensor.
-constexpr int kTable = 1024;  // entries in shared memory
-struct Where {
-    const qg_adamw_tensor *t;
-    int64_t e;  // this thread's first value
-    int kind;
+// The list as a CTA sees it, in shared memory (longer lists take more launches).  The chunks of all tensors, one after
+// another, are dealt out in turn, so that all SMs work side by side in memory: each with a run of its own they would open
+// as many DRAM pages at a time as there are runs and arrays (55.7 million values with 8-bit states: 153 us, 93 side by
+// side).  Every warp looks up each chunk's tensor.
+constexpr int kTable = 512;  // entries
+struct Entry {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *sm, *sv;
+    float *master;
+    int64_t numel;
+    int first;  // chunk
+    float decay;
+    short kind, state, param_dtype, grad_dtype;
 };
-enum Kind { ANY, WIDE_F32, WIDE_E4M3, WIDE_E4M3_F16, WIDE_E4M3_BF16 };  // WIDE: a whole chunk, every array at whole vectors
+enum Kind { ANY, WIDE_F32, WIDE_E4M3, WIDE_E4M3_F16, WIDE_E4M3_BF16 };  // WIDE: every array at whole vectors
 
 __device__ __forceinline__ int kind_of(const qg_adamw_tensor &t) {
     const uintptr_t all = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad) | reinterpret_cast<uintptr_t>(t.master);
@@ -229,46 +235,41 @@ __device__ __forceinline__ int kind_of(const qg_adamw_tensor &t) {
 }
 
 struct List {
-    const qg_adamw_tensor *t;  // shared or global
-    const int *kinds;          // or null
+    const Entry *t;
     int count;
 
-    // Copies the list to `room` (kTable entries and their kinds) where it fits; all threads call it.
-    __device__ __forceinline__ List(const qg_adamw_tensor *list, int n, char *room) : t(list), kinds(nullptr), count(n) {
-        if (n > kTable) return;
-        constexpr int W = sizeof(qg_adamw_tensor) / 8;
-        uint64_t *to = reinterpret_cast<uint64_t *>(room);
-        for (int i = threadIdx.x; i < n * W; i += kThreads * kGroups) to[i] = reinterpret_cast<const uint64_t *>(list)[i];
+    // All threads call it.
+    __device__ __forceinline__ List(const qg_adamw_tensor *list, int n, char *room) : t(reinterpret_cast<const Entry *>(room)), count(n) {
+        for (int i = threadIdx.x; i < n; i += kThreads * kGroups) {
+            const qg_adamw_tensor &q = list[i];
+            reinterpret_cast<Entry *>(room)[i] = {q.param, q.grad, q.exp_avg, q.exp_avg_sq, q.exp_avg_scale, q.exp_avg_sq_scale, q.master, q.numel,
+                                                  static_cast<int>(q.first_chunk), q.weight_decay, static_cast<short>(kind_of(q)), static_cast<short>(q.state),
+                                                  static_cast<short>(q.param_dtype), static_cast<short>(q.grad_dtype)};
+        }
         __syncthreads();
-        t = reinterpret_cast<const qg_adamw_tensor *>(room);
-        int *k = reinterpret_cast<int *>(room + n * sizeof(qg_adamw_tensor));
-        for (int i = threadIdx.x; i < n; i += kThreads * kGroups) k[i] = kind_of(t[i]);
-        __syncthreads();
-        kinds = k;
     }
-    // The tensor owning chunk c: the last one with first_chunk <= c (a warp finds it, 32 steps at a time).
-    __device__ __forceinline__ int find(int64_t c) const {
+    // The tensor owning chunk c: the last one with first <= c (a warp finds it, 32 steps at a time).
+    __device__ __forceinline__ int find(int c) const {
         const int lane = threadIdx.x & 31;
         int lo = 0, n = count;
         while (n > 1) {
             const int step = (n + 31) / 32, i = lo + lane * step;
-            const unsigned who = __ballot_sync(~0u, lane * step < n && t[i].first_chunk <= c);  // ones first
+            const unsigned who = __ballot_sync(~0u, lane * step < n && t[i].first <= c);  // ones first
             const int last = __popc(who) - 1;
             n = min(step, n - last * step);
             lo += last * step;
         }
         return lo;
     }
-    __device__ __forceinline__ Where place(int i, int64_t c) const {
-        Where w;
-        w.t = t + i;
-        const int64_t in = c - w.t->first_chunk;
-        w.e = in * kChunk + threadIdx.x % kThreads * kVals;
-        w.kind = (in + 1) * kChunk > w.t->numel ? ANY : kinds ? kinds[i] : kind_of(*w.t);
-        return w;
+    // The same where it is not behind entry i, and likely near.
+    __device__ __forceinline__ int find_before(int i, int c) const {
+        const int at = i - static_cast<int>(threadIdx.x & 31);
+        const unsigned who = __ballot_sync(~0u, at >= 0 && t[max(at, 0)].first <= c);
+        return who ? i - (__ffs(who) - 1) : find(c);
     }
 };
-int list_bytes(int count) { return count > kTable ? 0 : (count * (static_cast<int>(sizeof(qg_adamw_tensor)) + 4) + 15) / 16 * 16; }
+int list_bytes(int count) { return std::min(count, kTable) * static_cast<int>(sizeof(Entry)); }
+static_assert(sizeof(Entry) % 16 == 0, "read in 16-byte pieces");
 
 // The sum of squares of eight values in fp32, or in fp64 where that leaves its range.
 __device__ __forceinline__ double squares(const float (&g)[8]) {
@@ -283,16 +284,16 @@ __device__ __forceinline__ double squares(const float (&g)[8]) {
     return wide;
 }
 
-// The sum of squares of whole chunks of one tensor, of eight at most (four of fp32): all loads of a thread together.
+// The sum of squares of whole parts of one tensor, of eight at most (four of fp32): all loads of a thread together.
 template <int DT>
-__device__ __forceinline__ double squares_of_some(const void *grad, int64_t e, int chunks) {
+__device__ __forceinline__ double squares_of_some(const void *grad, int64_t e, int parts) {
     constexpr int U = DT == 0 ? 2 : 1, N = 8 / U;
     uint4 v[N][U];
     const char *p = static_cast<const char *>(grad) + e * (DT == 0 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[i][u] = i < chunks ? load128(p + i * (kChunk * (DT == 0 ? 4 : 2)) + u * 16) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < U; ++u) v[i][u] = i < parts ? load128(p + i * (kPart * (DT == 0 ? 4 : 2)) + u * 16) : make_uint4(0, 0, 0, 0);
     double total = 0.0;
     float s = 0.f;
     bool fits = true;
@@ -303,59 +304,61 @@ __device__ __forceinline__ double squares_of_some(const void *grad, int64_t e, i
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[k & 1] = fmaf(g[k], g[k], q[k & 1]);
         const float sum = q[0] + q[1];
-        fits = fits && ((sum >= 1e-30f && sum <= 3e37f) || i >= chunks);
+        fits = fits && ((sum >= 1e-30f && sum <= 3e37f) || i >= parts);
         s += sum;
     }
     if (fits) return s;
 #pragma unroll 1
-    for (int i = 0; i < chunks; ++i) {  // again, one by one
+    for (int i = 0; i < parts; ++i) {  // again, one by one
         float g[8];
-        numbers(raw8<true>(grad, DT, e + static_cast<int64_t>(i) * kChunk, 8), DT, g);
+        numbers(raw8<true>(grad, DT, e + static_cast<int64_t>(i) * kPart, 8), DT, g);
         total += squares(g);
     }
     return total;
 }
 
-// One sum of squares for each CTA.
-__global__ void __launch_bounds__(kThreads * kGroups, 1) sumsq_kernel(const qg_adamw_tensor *__restrict__ list, int count, int64_t chunks,
-                                                               double *__restrict__ partial) {
+// One sum of squares for each CTA; added to what is there (the entries before these).
+__global__ void __launch_bounds__(kThreads * kGroups, 1) sumsq_kernel(const qg_adamw_tensor *__restrict__ list, int count, int more, int64_t chunks,
+                                                                     double *__restrict__ partial, int add) {
     __shared__ double red[kThreads * kGroups / 32];
     extern __shared__ __align__(16) char room[];
     pdl_wait();
     pdl_launch_dependents();
     double total = 0.0;
-    const int64_t groups = (chunks + 7) / 8;
-    {
-        const List l(list, count, room);
-        for (int64_t gr = blockIdx.x * kGroups + threadIdx.x / kThreads; gr < groups; gr += gridDim.x * kGroups) {
-            const int64_t end = std::min<int64_t>(chunks, gr * 8 + 8);
-            for (int64_t c = gr * 8; c < end;) {
-                const Where w = l.place(l.find(c), c);
-                const qg_adamw_tensor &t = *w.t;
-                const int64_t whole = t.first_chunk + t.numel / kChunk;  // up to here its chunks are
-                const void *grad = t.grad;
-                const int dt = t.grad_dtype;
-                if (c < whole && (reinterpret_cast<uintptr_t>(grad) & 15u) == 0) {
-                    const int some = static_cast<int>(std::min<int64_t>(std::min(whole, end) - c, dt == 0 ? 4 : 8));
-                    total += dt == 0 ? squares_of_some<0>(grad, w.e, some) : dt == 1 ? squares_of_some<1>(grad, w.e, some) : squares_of_some<2>(grad, w.e, some);
-                    c += some;
+    const List l(list, count, room);
+    const int begin = l.t[0].first / 4, last = static_cast<int>(more ? list[count].first_chunk : chunks);  // of four chunks; chunks
+    for (int turn = begin + blockIdx.x * kGroups + threadIdx.x / kThreads; turn * 4 < last; turn += gridDim.x * kGroups) {
+        const int end = min(last, turn * 4 + 4);
+        for (int c = max(turn * 4, l.t[0].first); c < end;) {
+            const Entry &t = l.t[l.find(c)];
+            const void *grad = t.grad;
+            const int dt = t.grad_dtype, after = min(end, t.first + static_cast<int>((t.numel + kChunk - 1) / kChunk));
+            const bool wide = (reinterpret_cast<uintptr_t>(grad) & 15u) == 0;
+            const int64_t e0 = static_cast<int64_t>(c - t.first) * kChunk, e1 = std::min<int64_t>(t.numel, static_cast<int64_t>(after - t.first) * kChunk);
+            for (int64_t e = e0; e < e1;) {
+                const int64_t mine = e + threadIdx.x % kThreads * kVals;
+                const int some = wide ? static_cast<int>(std::min<int64_t>((e1 - e) / kPart, dt == 0 ? 4 : 8)) : 0;
+                if (some > 0) {
+                    total += dt == 0 ? squares_of_some<0>(grad, mine, some) : dt == 1 ? squares_of_some<1>(grad, mine, some) : squares_of_some<2>(grad, mine, some);
+                    e += static_cast<int64_t>(some) * kPart;
                     continue;
                 }
-                const int64_t left = t.numel - w.e;
+                const int64_t left = t.numel - mine;
                 if (left > 0) {
                     float g[8];
-                    numbers(raw8<false>(grad, dt, w.e, left < 8 ? static_cast<int>(left) : 8), dt, g);
+                    numbers(wide && left >= 8 ? raw8<true>(grad, dt, mine, 8) : raw8<false>(grad, dt, mine, left < 8 ? static_cast<int>(left) : 8), dt, g);
                     total += squares(g);
                 }
-                ++c;
+                e += kPart;
             }
+            c = after;
         }
     }
     for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = total;
     __syncthreads();
     if (threadIdx.x == 0) {
-        total = 0.0;
+        total = add ? partial[blockIdx.x] : 0.0;
         for (int w = 0; w < kThreads * kGroups / 32; ++w) total += red[w];
         partial[blockIdx.x] = total;
     }
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kThreads * kGroups, 1) sumsq_kernel(const qg_a
 
 struct StepArgs {
     const qg_adamw_tensor *list;
-    int count;
+    int count, more;  // entries of this launch, and whether others follow
     int64_t chunks;
     float lr, beta1, beta2, root2, keep1, keep2, ln1, ln2, eps;  // root2 = sqrt(beta2), keep1 = 1 - beta1, keep2 = sqrt(1 - beta2), ln = log(beta)
     const float *lr_dev;
@@ -388,17 +391,17 @@ struct Raw {
     float sm, sv;
 };
 template <bool WIDE, bool EIGHT>
-__device__ __forceinline__ void fetch8(Raw &x, const qg_adamw_tensor &t, int64_t e, int n) {
+__device__ __forceinline__ void fetch8(Raw &x, const Entry &t, int64_t e, int n) {
     x.g = raw8<WIDE>(t.grad, t.grad_dtype, e, n);
     x.w = t.master ? raw8<WIDE>(t.master, 0, e, n) : raw8<WIDE>(t.param, t.param_dtype, e, n);
     if constexpr (EIGHT) {
-        x.cm = load_codes<WIDE>(t.exp_avg, e, n), x.cv = load_codes<WIDE>(t.exp_avg_sq, e, n);
+        x.cm = load_codes<WIDE>(t.m, e, n), x.cv = load_codes<WIDE>(t.v, e, n);
         const int64_t block = e >> 8;
         const bool there = WIDE || block << 8 < t.numel;
-        x.sm = there ? t.exp_avg_scale[block] : 0.f, x.sv = there ? t.exp_avg_sq_scale[block] : 0.f;
+        x.sm = there ? t.sm[block] : 0.f, x.sv = there ? t.sv[block] : 0.f;
     } else {
-        x.m = raw8<WIDE>(t.exp_avg, 0, e, n);
-        x.v = raw8<WIDE>(t.exp_avg_sq, 0, e, n);
+        x.m = raw8<WIDE>(t.m, 0, e, n);
+        x.v = raw8<WIDE>(t.v, 0, e, n);
     }
 }
 
@@ -428,11 +431,11 @@ __device__ __forceinline__ Factors factors(const StepArgs &p, const Rates &r, fl
 
 // The step of eight values, n of them there, and their stores.  WIDE: all there, at whole vectors.
 template <bool WIDE, bool EIGHT>
-__device__ __forceinline__ void step8(const Raw &x, const qg_adamw_tensor &t, const StepArgs &p, const Rates &r, int64_t e, int n) {
+__device__ __forceinline__ void step8(const Raw &x, const Entry &t, const StepArgs &p, const Rates &r, int64_t e, int n) {
     float w[8], g[8], m[8], v[8], u[8];
     numbers(x.g, t.grad_dtype, g);
     numbers(x.w, t.master ? 0 : t.param_dtype, w);
-    Factors f = factors(p, r, t.weight_decay);
+    Factors f = factors(p, r, t.decay);
     if constexpr (EIGHT) {
         f.b1 = both(p.beta1 * x.sm), f.b2 = both(p.root2 * x.sv);
         decode(x.cm, m);
@@ -453,84 +456,88 @@ __device__ __forceinline__ void step8(const Raw &x, const qg_adamw_tensor &t, co
         const int64_t block = e >> 8;
         float sm, sv;
         const uint2 cm = encode<false>(m, sm), cv = encode<true>(u, sv);
-        store_codes<WIDE>(t.exp_avg, e, n, cm);
-        store_codes<WIDE>(t.exp_avg_sq, e, n, cv);
+        store_codes<WIDE>(t.m, e, n, cm);
+        store_codes<WIDE>(t.v, e, n, cv);
         if ((threadIdx.x & 31) == 0 && n > 0) {
-            t.exp_avg_scale[block] = sm;
-            t.exp_avg_sq_scale[block] = sv;
+            t.sm[block] = sm;
+            t.sv[block] = sv;
         }
     } else {
-        store8<WIDE>(t.exp_avg, 0, e, n, m);
-        store8<WIDE>(t.exp_avg_sq, 0, e, n, v);
+        store8<WIDE>(t.m, 0, e, n, m);
+        store8<WIDE>(t.v, 0, e, n, v);
     }
 }
 
 // A whole chunk of a tensor with 8-bit states, and parameters and gradients of one 16-bit type, at whole vectors.  There is
-// as much to compute here as to move, so that the next chunks are on their way meanwhile.
+// as much to compute here as to move, so that the next chunk is on its way meanwhile.
 struct Half {
     uint4 w, g;
     uint2 m, v;
     float sm, sv;
 };
-// The chunks to come wait in shared memory, each thread's values in places of its own (so nobody waits for anybody).
-constexpr int kAhead = 3;                                      // places
-constexpr int kSlot = kThreads * kGroups * (16 + 16 + 8 + 8 + 4 + 4);
-__device__ __forceinline__ void copy_async(uint32_t to, const void *from, std::integral_constant<int, 16>) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
+// The chunk to come waits in shared memory, each thread's values in places of its own (so nobody waits for anybody).
+constexpr int kAll = kThreads * kGroups;
+constexpr int kPlace = kAll * (16 + 16 + 8 + 8 + 4 + 4), kSlot = 2 * kPlace;
 template <int N>
-__device__ __forceinline__ void copy_async(uint32_t to, const void *from, std::integral_constant<int, N>) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
 }
-struct Places {  // of this thread in slot 0
+struct Places {  // of this thread in the first place
     uint32_t wg, mv, s;
-    __device__ __forceinline__ Places(uint32_t ring) {
-        const uint32_t all = kThreads * kGroups;
-        wg = ring + threadIdx.x * 16, mv = ring + all * 32 + threadIdx.x * 8, s = ring + all * 48 + threadIdx.x * 4;
-    }
+    __device__ __forceinline__ Places(uint32_t ring) : wg(ring + threadIdx.x * 16), mv(ring + kAll * 32 + threadIdx.x * 8), s(ring + kAll * 48 + threadIdx.x * 4) {}
 };
-__device__ __forceinline__ void request_half(const Places &p, uint32_t slot, const Where &at) {
-    constexpr uint32_t all = kThreads * kGroups;
-    const qg_adamw_tensor &t = *at.t;
-    copy_async(p.wg + slot, static_cast<const char *>(t.param) + at.e * 2, std::integral_constant<int, 16>{});
-    copy_async(p.wg + slot + all * 16, static_cast<const char *>(t.grad) + at.e * 2, std::integral_constant<int, 16>{});
-    copy_async(p.mv + slot, static_cast<const char *>(t.exp_avg) + at.e, std::integral_constant<int, 8>{});
-    copy_async(p.mv + slot + all * 8, static_cast<const char *>(t.exp_avg_sq) + at.e, std::integral_constant<int, 8>{});
-    copy_async(p.s + slot, t.exp_avg_scale + (at.e >> 8), std::integral_constant<int, 4>{});
-    copy_async(p.s + slot + all * 4, t.exp_avg_sq_scale + (at.e >> 8), std::integral_constant<int, 4>{});
+__device__ __forceinline__ void request_half(const Places &p, uint32_t place, const Entry &t, int64_t e) {
+    const char *w = static_cast<const char *>(t.param) + e * 2, *g = static_cast<const char *>(t.grad) + e * 2;
+    const char *m = static_cast<const char *>(t.m) + e, *v = static_cast<const char *>(t.v) + e;
+    const float *sm = t.sm + (e >> 8), *sv = t.sv + (e >> 8);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t to = place + i * kPlace;
+        copy_async<16>(p.wg + to, w + i * (kPart * 2));
+        copy_async<16>(p.wg + to + kAll * 16, g + i * (kPart * 2));
+        copy_async<8>(p.mv + to, m + i * kPart);
+        copy_async<8>(p.mv + to + kAll * 8, v + i * kPart);
+        copy_async<4>(p.s + to, sm + i * (kPart / 256));
+        copy_async<4>(p.s + to + kAll * 4, sv + i * (kPart / 256));
+    }
 }
-__device__ __forceinline__ Half receive_half(const Places &p, uint32_t slot) {
-    constexpr uint32_t all = kThreads * kGroups;
+__device__ __forceinline__ Half receive_half(const Places &p, uint32_t place) {
     Half x;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.w.x), "=r"(x.w.y), "=r"(x.w.z), "=r"(x.w.w) : "r"(p.wg + slot) : "memory");
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.g.x), "=r"(x.g.y), "=r"(x.g.z), "=r"(x.g.w) : "r"(p.wg + slot + all * 16) : "memory");
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.m.x), "=r"(x.m.y) : "r"(p.mv + slot) : "memory");
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.v.x), "=r"(x.v.y) : "r"(p.mv + slot + all * 8) : "memory");
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x.sm) : "r"(p.s + slot) : "memory");
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x.sv) : "r"(p.s + slot + all * 4) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.w.x), "=r"(x.w.y), "=r"(x.w.z), "=r"(x.w.w) : "r"(p.wg + place) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.g.x), "=r"(x.g.y), "=r"(x.g.z), "=r"(x.g.w) : "r"(p.wg + place + kAll * 16) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.m.x), "=r"(x.m.y) : "r"(p.mv + place) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.v.x), "=r"(x.v.y) : "r"(p.mv + place + kAll * 8) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x.sm) : "r"(p.s + place) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x.sv) : "r"(p.s + place + kAll * 4) : "memory");
     return x;
 }
 template <int DT>
-__device__ __forceinline__ void step_half(const Half &x, const Where &at, const StepArgs &p, const Rates &r) {
-    const qg_adamw_tensor &t = *at.t;
-    Factors f = factors(p, r, t.weight_decay);
-    f.b1 = both(p.beta1 * x.sm), f.b2 = both(p.root2 * x.sv);
-    float m[8], u[8], w[8], g[8];
-    numbers({x.w, x.w}, DT, w);
-    numbers({x.g, x.g}, DT, g);
-    decode(x.m, m);
-    decode(x.v, u);
+__device__ __forceinline__ void step_half(const Places &places, uint32_t place, const Entry &t, int64_t e, const StepArgs &p, const Rates &r) {
+    Factors f = factors(p, r, t.decay);
+    char *to = static_cast<char *>(t.param) + e * 2, *tm = static_cast<char *>(t.m) + e, *tv = static_cast<char *>(t.v) + e;
+    float *sm = t.sm + (e >> 8), *sv = t.sv + (e >> 8);
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-        float2 w2 = make_float2(w[k], w[k + 1]), m2 = make_float2(m[k], m[k + 1]), v2 = make_float2(u[k], u[k + 1]), u2;
-        step2<true>(f, w2, make_float2(g[k], g[k + 1]), m2, v2, u2);
-        w[k] = w2.x, w[k + 1] = w2.y, m[k] = m2.x, m[k + 1] = m2.y, u[k] = u2.x, u[k + 1] = u2.y;
+    for (int i = 0; i < 2; ++i) {
+        const Half x = receive_half(places, place + i * kPlace);
+        f.b1 = both(p.beta1 * x.sm), f.b2 = both(p.root2 * x.sv);
+        float m[8], u[8], w[8], g[8];
+        numbers({x.w, x.w}, DT, w);
+        numbers({x.g, x.g}, DT, g);
+        decode(x.m, m);
+        decode(x.v, u);
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            float2 w2 = make_float2(w[k], w[k + 1]), m2 = make_float2(m[k], m[k + 1]), v2 = make_float2(u[k], u[k + 1]), u2;
+            step2<true>(f, w2, make_float2(g[k], g[k + 1]), m2, v2, u2);
+            w[k] = w2.x, w[k + 1] = w2.y, m[k] = m2.x, m[k + 1] = m2.y, u[k] = u2.x, u[k + 1] = u2.y;
+        }
+        store8<true>(to + i * (kPart * 2), DT, 0, 8, w);
+        float s0, s1;
+        store_codes<true>(tm, i * kPart, 8, encode<false>(m, s0));
+        store_codes<true>(tv, i * kPart, 8, encode<true>(u, s1));
+        if ((threadIdx.x & 31) == 0) sm[i * (kPart / 256)] = s0, sv[i * (kPart / 256)] = s1;
     }
-    store8<true>(t.param, DT, at.e, 8, w);
-    float s0, s1;
-    store_codes<true>(t.exp_avg, at.e, 8, encode<false>(m, s0));
-    store_codes<true>(t.exp_avg_sq, at.e, 8, encode<true>(u, s1));
-    if ((threadIdx.x & 31) == 0) t.exp_avg_scale[at.e >> 8] = s0, t.exp_avg_sq_scale[at.e >> 8] = s1;
 }
 
 __global__ void __launch_bounds__(kThreads * kGroups, 1) step_kernel(const __grid_constant__ StepArgs p) {
@@ -555,7 +562,6 @@ __global__ void __launch_bounds__(kThreads * kGroups, 1) step_kernel(const __gri
         clip = factor;
         if (clip < 0.f) return;  // a norm that is infinite or NaN: no step
     }
-    if (static_cast<int64_t>(blockIdx.x) * kGroups >= p.chunks) return;
     Rates r;
     r.g1 = p.keep1 * clip;
     r.g2 = p.keep2 * clip;
@@ -563,51 +569,64 @@ __global__ void __launch_bounds__(kThreads * kGroups, 1) step_kernel(const __gri
     const float step = p.step_dev ? fmaxf(static_cast<float>(*p.step_dev), 1.f) : p.step;
     r.rate = r.lr / -expm1f(step * p.ln1);
     r.widen = rsqrtf(-expm1f(step * p.ln2));
-    const List l(p.list, p.count, room + kAhead * kSlot);
+    const List l(p.list, p.count, room + 2 * kSlot);
     // from the last chunk on: the gradients that the norm's launch read last are still in the L2
-    const int64_t step_back = static_cast<int64_t>(gridDim.x) * kGroups;
-    int64_t c = p.chunks - 1 - (static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / kThreads);  // the next to be asked for
+    const int first = l.t[0].first, back = static_cast<int>(gridDim.x) * kGroups;
+    int c = static_cast<int>(p.more ? p.list[p.count].first_chunk : p.chunks) - 1 - static_cast<int>(blockIdx.x * kGroups + threadIdx.x / kThreads);
+    int i = p.count - 1;
     const Places mine(smem_u32(room));
-    const auto request = [&](uint32_t slot) {
-        Where w{};
-        if (c >= 0) {
-            w = l.place(l.find(c), c);
-            if (w.kind >= WIDE_E4M3_F16) request_half(mine, slot, w);
+    struct Where {
+        int i;      // entry, or -1: no more
+        int64_t e;  // this thread's first value
+        bool half;
+    };
+    const auto request = [&](uint32_t place) {
+        Where w{-1, 0, false};
+        if (c >= first) {
+            i = l.find_before(i, c);
+            const Entry &t = l.t[i];
+            const int64_t begin = static_cast<int64_t>(c - t.first) * kChunk;
+            w = {i, begin + threadIdx.x % kThreads * kVals, t.kind >= WIDE_E4M3_F16 && begin + kChunk <= t.numel};
+            if (w.half) request_half(mine, place, t, w.e);
+            c -= back;
         }
-        c -= step_back;
         asm volatile("cp.async.commit_group;" ::: "memory");
         return w;
     };
-    Where at = request(0), then = request(kSlot);
-    uint32_t slot = 0;
-    while (at.t) {
-        const Where last = request(slot == 0 ? 2 * kSlot : slot - kSlot);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-        const qg_adamw_tensor &t = *at.t;
-        Raw x;
-        if (at.kind == WIDE_E4M3_F16) {
-            step_half<1>(receive_half(mine, slot), at, p, r);
-        } else if (at.kind == WIDE_E4M3_BF16) {
-            step_half<2>(receive_half(mine, slot), at, p, r);
-        } else if (at.kind == WIDE_F32) {
-            fetch8<true, false>(x, t, at.e, 8);
-            step8<true, false>(x, t, p, r, at.e, 8);
-        } else if (at.kind == WIDE_E4M3) {
-            fetch8<true, true>(x, t, at.e, 8);
-            step8<true, true>(x, t, p, r, at.e, 8);
+    uint32_t place = 0;
+    for (Where at = request(0); at.i >= 0; place ^= kSlot) {
+        const Where next = request(place ^ kSlot);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const Entry &t = l.t[at.i];
+        if (at.half) {
+            if (t.kind == WIDE_E4M3_F16) step_half<1>(mine, place, t, at.e, p, r);
+            else step_half<2>(mine, place, t, at.e, p, r);
         } else {
-            const int64_t left = t.numel - at.e;
-            const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
-            if (t.state == QG_STATE_E4M3) {
-                fetch8<false, true>(x, t, at.e, n);
-                step8<false, true>(x, t, p, r, at.e, n);
-            } else {
-                fetch8<false, false>(x, t, at.e, n);
-                step8<false, false>(x, t, p, r, at.e, n);
+#pragma unroll 1
+            for (int64_t e = at.e; e < at.e + kChunk; e += kPart) {
+                const int64_t left = t.numel - e;
+                const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+                if (!__any_sync(~0u, n > 0)) break;
+                Raw x;
+                const bool wide = t.kind != ANY && __all_sync(~0u, n == 8);
+                if (t.state == QG_STATE_E4M3) {
+                    if (wide) {
+                        fetch8<true, true>(x, t, e, 8);
+                        step8<true, true>(x, t, p, r, e, 8);
+                    } else {
+                        fetch8<false, true>(x, t, e, n);
+                        step8<false, true>(x, t, p, r, e, n);
+                    }
+                } else if (wide) {
+                    fetch8<true, false>(x, t, e, 8);
+                    step8<true, false>(x, t, p, r, e, 8);
+                } else {
+                    fetch8<false, false>(x, t, e, n);
+                    step8<false, false>(x, t, p, r, e, n);
+                }
             }
         }
-        at = then, then = last;
-        slot = slot == 2 * kSlot ? 0 : slot + kSlot;
+        at = next;
     }
 }
 
@@ -627,19 +646,22 @@ cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};  // a bit for each device
     const int slot = device_slot();
     if (slot < 0 || !(done.load(std::memory_order_relaxed) >> slot & 1)) {
-        cudaError_t e = cudaFuncSetAttribute(step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAhead * kSlot + list_bytes(kTable));
+        cudaError_t e = cudaFuncSetAttribute(step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kSlot + list_bytes(kTable));
         if (e == cudaSuccess) e = cudaFuncSetAttribute(sumsq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, list_bytes(kTable));
         if (e != cudaSuccess) return e;
         if (slot >= 0) done.fetch_or(1ull << slot, std::memory_order_relaxed);
     }
-    if (q.clip) {
-        const cudaError_t e = launch_pdl(sumsq_kernel, dim3(parts), dim3(kThreads * kGroups), list_bytes(q.count), s, list, q.count, q.chunks, static_cast<double *>(ws));
-        if (e != cudaSuccess) return e;
+    if (q.chunks == 0) {  // nothing but, perhaps, the norm of nothing
+        return q.clip && q.norm ? cudaMemsetAsync(q.norm, 0, sizeof(float), s) : cudaSuccess;
     }
-    if (q.chunks == 0 && !(q.clip && q.norm)) return cudaSuccess;
+    if (q.clip)
+        for (int at = 0; at < q.count; at += kTable) {
+            const int n = std::min(kTable, q.count - at);
+            const cudaError_t e = launch_pdl(sumsq_kernel, dim3(parts), dim3(kAll), list_bytes(n), s, list + at, n, at + n < q.count ? 1 : 0, q.chunks,
+                                             static_cast<double *>(ws), at > 0 ? 1 : 0);
+            if (e != cudaSuccess) return e;
+        }
     StepArgs a{};
-    a.list = list;
-    a.count = q.count;
     a.chunks = q.chunks;
     a.lr = static_cast<float>(q.lr);
     a.beta1 = static_cast<float>(q.beta1);
@@ -658,8 +680,14 @@ cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s) {
     a.max_norm = q.max_norm;
     a.norm_eps = q.norm_eps;
     a.norm = q.norm;
-    const cudaError_t e = launch_pdl(step_kernel, dim3(parts), dim3(kThreads * kGroups), kAhead * kSlot + list_bytes(q.count), s, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    for (int at = 0; at < q.count; at += kTable) {
+        a.list = list + at;
+        a.count = std::min(kTable, q.count - at);
+        a.more = at + a.count < q.count ? 1 : 0;
+        const cudaError_t e = launch_pdl(step_kernel, dim3(parts), dim3(kAll), 2 * kSlot + list_bytes(a.count), s, a);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaGetLastError();
 }
 
 }  // namespace qg

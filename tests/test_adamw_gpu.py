@@ -98,7 +98,7 @@ def check(c, want):
             assert bool((got_v[v > 0] > 0).all())
 
 
-SIZES = [1, 7, 8, 255, 256, 257, 2048, 2049, 0, 5000, 70001]
+SIZES = [1, 7, 8, 255, 256, 257, 2048, 2049, 0, 4096, 4097, 5000, 70001]
 
 
 @pytest.mark.parametrize("state", ["f32", "e4m3"])
