@@ -53,6 +53,21 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Packed fp32 pairs.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Words of logits as they lie in memory: largest() keeps a NaN, at_least() does not.
 template <int XT>
 struct Logits;  // f32, f16, bf16
 template <>
@@ -66,6 +81,10 @@ struct Logits<0> {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
     static __device__ __forceinline__ float one(const char *p) { return *reinterpret_cast<const float *>(p); }
+    static __device__ __forceinline__ uint32_t largest(uint32_t a, uint32_t b) { return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b))); }
+    static __device__ __forceinline__ uint32_t at_least(uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }
+    static __device__ __forceinline__ float value(uint32_t w) { return __uint_as_float(w); }
+    static __device__ __forceinline__ uint32_t word(float x) { return __float_as_uint(x); }
 };
 template <>
 struct Logits<1> {
@@ -89,6 +108,18 @@ struct Logits<1> {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     static __device__ __forceinline__ float one(const char *p) { return h2f(*reinterpret_cast<const uint16_t *>(p)); }
+    static __device__ __forceinline__ uint32_t largest(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t at_least(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ float value(uint32_t w) { return max_nan(h2f(static_cast<uint16_t>(w)), h2f(static_cast<uint16_t>(w >> 16))); }
+    static __device__ __forceinline__ uint32_t word(float x) { return f2h(fmaxf(x, -65504.f)) * 0x10001u; }
 };
 template <>
 struct Logits<2> {
@@ -109,6 +140,18 @@ struct Logits<2> {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     static __device__ __forceinline__ float one(const char *p) { return bf2f(*reinterpret_cast<const uint16_t *>(p)); }
+    static __device__ __forceinline__ uint32_t largest(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t at_least(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ float value(uint32_t w) { return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+    static __device__ __forceinline__ uint32_t word(float x) { return f2bf(x) * 0x10001u; }
 };
 
 __device__ __forceinline__ uint4 load_stream(const char *p) {
@@ -169,7 +212,7 @@ struct ScoreArgs {
     int64_t ldx;
     const int64_t *target;
     int T, V, top;
-    float inv_t, c;  // c = inv_t * log2(e)
+    float inv_t, c, back;  // c = inv_t * log2(e), back = 1 / c
     float *logprob, *entropy, *lse;
     int64_t *top_ids;
     float *top_logprobs;
@@ -260,27 +303,45 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) v[u] = ahead[u];
         if (q0 + kThreads * kVecs < v1) fetch(q0 + kThreads * kVecs);
-        float top = -INFINITY;
+        uint32_t best = L::NEG_INF;
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            float x[VE];
-            L::floats(v[u], x);
-#pragma unroll
-            for (int k = 0; k < VE; ++k) top = max_nan(top, x[k]);
-        }
+        for (int u = 0; u < kVecs; ++u) best = L::largest(L::largest(best, v[u].x), L::largest(v[u].y, L::largest(v[u].z, v[u].w)));
+        const float top = L::value(best);
         if (!(top < INFINITY)) bad = true;  // NaN, or an infinity whose differences are NaN
         if (top > -INFINITY) {
             move_reference(t, top, p.c);
+            if (fabsf(t.ref) <= 16384.f) {
+                // What is 2^-130 of the reference or less counts as about that, -inf too: its product with its logarithm is a
+                // number.  |ref| / 64 is more than the type's step there.
+                const uint32_t low = L::word(t.ref - fmaxf(130.f * p.back, fabsf(t.ref) * 0.015625f));
+                const float2 ref = make_float2(-t.ref, -t.ref), c = make_float2(p.c, p.c);
+                float2 s0 = make_float2(0.f, 0.f), a0 = s0;
 #pragma unroll
-            for (int u = 0; u < kVecs; ++u) {
-                float x[VE];
-                L::floats(v[u], x);
+                for (int u = 0; u < kVecs; ++u) {
+                    float x[VE];
+                    L::floats(make_uint4(L::at_least(v[u].x, low), L::at_least(v[u].y, low), L::at_least(v[u].z, low), L::at_least(v[u].w, low)), x);
 #pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    const float y = fmaxf((x[k] - t.ref) * p.c, -150.f);  // exp2 of it is 0, and so is its product with y
-                    const float e = ex2(y);
-                    t.s += e;
-                    t.a = fmaf(e, y, t.a);
+                    for (int k = 0; k < VE; k += 2) {
+                        const float2 y = mul2(add2(make_float2(x[k], x[k + 1]), ref), c);
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        s0 = add2(s0, e);
+                        a0 = ffma2(e, y, a0);
+                    }
+                }
+                t.s += s0.x + s0.y;
+                t.a += a0.x + a0.y;
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < kVecs; ++u) {
+                    const uint4 w = u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3];
+                    float x[VE];
+                    L::floats(w, x);
+#pragma unroll
+                    for (int k = 0; k < VE; ++k) {
+                        const float y = fmaxf((x[k] - t.ref) * p.c, -150.f), e = ex2(y);
+                        t.s += e;
+                        t.a = fmaf(e, y, t.a);
+                    }
                 }
             }
         }
@@ -345,9 +406,9 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
         }
     }
     if constexpr (TOP) {
-        kept = cut_list(sh, kept, p.top, bound);
+        if (kept > kThreads) kept = cut_list(sh, kept, p.top, bound);
         rank_keys(sh.list, kept, p.top, sh.best);
-        if (tid == 0) sh.found = kept;
+        if (tid == 0) sh.found = min(kept, p.top);
     }
     if (parts > 1) cluster.sync();
     else __syncthreads();
@@ -502,7 +563,7 @@ cudaError_t launch_score(const ScoreArgs &a, int want, cudaStream_t s) {
 
 cudaError_t token_logprobs(const TokenLogprobs &q, cudaStream_t s) {
     const double log2e = 1.4426950408889634;
-    const ScoreArgs a{q.X, q.ldx, q.target, q.T, q.V, q.top, q.inv_t, static_cast<float>(q.inv_t * log2e), q.logprob, q.entropy, q.lse, q.top_ids, q.top_logprobs, q.status};
+    const ScoreArgs a{q.X, q.ldx, q.target, q.T, q.V, q.top, q.inv_t, static_cast<float>(q.inv_t * log2e), static_cast<float>(1.0 / (q.inv_t * log2e)), q.logprob, q.entropy, q.lse, q.top_ids, q.top_logprobs, q.status};
     // CTAs of a row: until every SM has two, as long as each has a step of its own to do
     const int steps = static_cast<int>((static_cast<int64_t>(q.V) * (q.x_dtype == 0 ? 4 : 2) + kThreads * kVecs * 16 - 1) / (kThreads * kVecs * 16));
     int parts = 1;

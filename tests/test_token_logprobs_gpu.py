@@ -126,6 +126,18 @@ def test_masked_rows(x, T):
 
 
 @pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("offset", [-60000.0, -16384.0, -300.0, 16384.0, 30000.0, 60000.0])
+@pytest.mark.parametrize("inv_t", [0.01, 1.0, 50.0])
+def test_rows_far_from_zero(x, offset, inv_t):
+    """Logits with a common offset, some of them ruled out, at high and low temperatures."""
+    X, target = logits(3, 5003, "f32", seed=7)
+    X = (X + offset).to(DT[x])
+    X[:, ::3] = -math.inf
+    target = target // 3 * 3 + 1
+    check(X, target.clamp(max=5002), inv_t, 6, call(X, target.clamp(max=5002), inv_t, 6))
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
 def test_infinite_and_nan_logits(x):
     X, target = logits(6, 10007, x, seed=6)
     X[1, 9000] = math.nan
