@@ -243,6 +243,8 @@ def qmoe_decode_fused(x, expert_ids, expert_weights, *, num_experts, fc1_w, fc1_
                       workspace=None, stream=None, raw=False):
     """One-token fused QMoE decode (fc1 -> SwiGLU -> fc2, weighted over the k slots); y [hidden] float16."""
     hidden = x.shape[-1]
+    if bits not in (2, 4, 8):
+        raise ValueError("bits: 2, 4 or 8 is wanted")
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
     ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device, stream)
@@ -258,6 +260,8 @@ def qmoe_decode_fused_dp4a(x, expert_ids, expert_weights, *, num_experts, fc1_w,
                            status=None, workspace=None, stream=None, raw=False):
     """qmoe_decode_fused with int8 activations (per-block symmetric quantization, dp4a dot products)."""
     hidden = x.shape[-1]
+    if bits not in (2, 4, 8):
+        raise ValueError("bits: 2, 4 or 8 is wanted")
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
     ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device, stream)
@@ -274,6 +278,8 @@ def qmoe_decode_fused_noalloc(x, expert_ids, expert_weights, *, num_experts, fc1
     """qmoe_decode_fused without a workspace: the library's fixed device scratch is used
     (callers that cannot allocate; shapes beyond QG_QMOE_NOALLOC_SCRATCH_BYTES are refused)."""
     hidden = x.shape[-1]
+    if bits not in (2, 4, 8):
+        raise ValueError("bits: 2, 4 or 8 is wanted")
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
     s = lib().qmoe_decode_fused_noalloc(_ptr(x), _ptr(expert_ids), _ptr(expert_weights), k, num_experts,
@@ -441,6 +447,13 @@ def _rows2d(t, rows, cols, what):
     if t.shape != (rows, cols) or (step != 1 and cols > 1):
         raise ValueError("%s: a tensor of %d rows of %d contiguous values is wanted" % (what, rows, cols))
     return ld if rows > 1 else cols  # the stride of a single row says nothing
+
+
+def _on_gpu(*tensors):
+    """The library takes addresses: one of the host would go unnoticed."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("tensors of a GPU are wanted")
 
 
 def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter, status):
@@ -791,6 +804,7 @@ def qg_token_logprobs(X, targets, logprob, *, entropy=None, lse=None, top_ids=No
         k = top_ids.shape[1]
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
         raise ValueError("status: an int32 is wanted")
+    _on_gpu(X, targets, logprob, entropy, lse, top_ids, top_logprobs, status)
     st = torch._C._cuda_getCurrentRawStream(X.get_device()) if stream is None else stream.cuda_stream
     s = lib().qg_token_logprobs(X.data_ptr(), _dtype_code(X), ldx, tp, T, V, inv_temperature, _per_row(logprob, T, "logprob"),
                                 _per_row(entropy, T, "entropy"), _per_row(lse, T, "lse"), k, _addr(top_ids), _addr(top_logprobs), _addr(status), st)
@@ -804,6 +818,7 @@ def qg_token_logprobs_grad(X, targets, lse, d_logprob, dX, *, entropy=None, d_en
     lddx = _rows2d(dX, T, V, "dX")
     if dX.dtype != X.dtype:
         raise ValueError("dX: X's type is wanted")
+    _on_gpu(X, targets, lse, d_logprob, dX, entropy, d_entropy)
     st = _torch()._C._cuda_getCurrentRawStream(X.get_device()) if stream is None else stream.cuda_stream
     s = lib().qg_token_logprobs_grad(X.data_ptr(), _dtype_code(X), ldx, tp, _per_row(lse, T, "lse"), _per_row(entropy, T, "entropy"),
                                      _per_row(d_logprob, T, "d_logprob"), _per_row(d_entropy, T, "d_entropy"), inv_temperature, dX.data_ptr(), lddx, T, V, st)
@@ -824,6 +839,7 @@ def qmoe_route_topk(logits, expert_ids, expert_weights, *, renormalize=True, str
     if expert_ids.dim() != 2 or expert_ids.shape[0] != T or expert_ids.dtype != torch.int32 or expert_weights.shape != expert_ids.shape \
             or expert_weights.dtype != torch.float32 or not expert_ids.is_contiguous() or not expert_weights.is_contiguous():
         raise ValueError("expert_ids [tokens, k] int32 and expert_weights [tokens, k] float32 are wanted")
+    _on_gpu(logits, expert_ids, expert_weights)
     st = torch._C._cuda_getCurrentRawStream(logits.get_device()) if stream is None else stream.cuda_stream
     s = lib().qmoe_route_topk(logits.data_ptr(), _dtype_code(logits), _rows2d(logits, T, E, "logits"), T, E, expert_ids.shape[1],
                               1 if renormalize else 0, expert_ids.data_ptr(), expert_weights.data_ptr(), st)
@@ -865,10 +881,13 @@ def qmoe_tokens_fused(x, expert_ids, expert_weights, *, fc1_w, fc1_scales, fc1_z
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
         raise ValueError("status: an int32 is wanted")
     k = expert_ids.shape[1]
+    if bits not in (2, 4, 8):
+        raise ValueError("bits: 2, 4 or 8 is wanted")
     inter = fc2_w.shape[-1] * 8 // bits
     E = _expert_sizes(fc1_w, fc1_scales, fc1_zp, fc1_bias, 2 * inter, hidden, bits, block_size, "fc1")
     if _expert_sizes(fc2_w, fc2_scales, fc2_zp, fc2_bias, hidden, inter, bits, block_size, "fc2") != E:
         raise ValueError("fc1 and fc2: as many experts in both are wanted")
+    _on_gpu(x, expert_ids, expert_weights, fc1_w, fc1_scales, fc1_zp, fc1_bias, fc2_w, fc2_scales, fc2_zp, fc2_bias, y, status)
     L = lib()
     need = L.qmoe_tokens_workspace_bytes(T, k, hidden, inter) if workspace is None else 0
     st, wp, wb, _ = _stream_and_workspace(need, workspace, x, stream)

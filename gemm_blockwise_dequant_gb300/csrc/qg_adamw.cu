@@ -641,6 +641,8 @@ int64_t adamw_chunks(int64_t numel) { return (numel + kChunk - 1) / kChunk; }
 size_t adamw_workspace_bytes(int64_t chunks) { return sizeof(double) * parts_of(chunks); }
 
 cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s) {
+    // no values: nothing but, perhaps, the norm of nothing
+    if (q.chunks == 0) return q.clip && q.norm ? cudaMemsetAsync(q.norm, 0, sizeof(float), s) : cudaSuccess;
     const qg_adamw_tensor *list = static_cast<const qg_adamw_tensor *>(q.list);
     const int parts = parts_of(q.chunks);
     static std::atomic<unsigned long long> done{0};  // a bit for each device
@@ -650,9 +652,6 @@ cudaError_t adamw_step(const AdamwStep &q, void *ws, cudaStream_t s) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(sumsq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, list_bytes(kTable));
         if (e != cudaSuccess) return e;
         if (slot >= 0) done.fetch_or(1ull << slot, std::memory_order_relaxed);
-    }
-    if (q.chunks == 0) {  // nothing but, perhaps, the norm of nothing
-        return q.clip && q.norm ? cudaMemsetAsync(q.norm, 0, sizeof(float), s) : cudaSuccess;
     }
     if (q.clip)
         for (int at = 0; at < q.count; at += kTable) {
