@@ -147,13 +147,16 @@ struct Layout {
 struct Plan {
     int16_t *ids;       // [pairs], -1: none
     int *count;         // [experts]
-    uint32_t *group;    // [groups]: expert << 16 | first row's rank
+    uint32_t *group;    // [groups]: expert << 20 | groups of two columns before << 10 | first row's rank
     int *rows;          // [kMaxRows]: the pairs whose activations are here
     unsigned *top;      // [kMaxRows]: largest magnitude of a row, as bits
     float *back;        // [kMaxRows]: the power of two that undoes its scale
     int *base;          // [kMaxRows]: where a group's rows begin, by its place in the span
-    int *num;           // groups
+    int *num;           // groups, those of two columns, and where this CTA's and the next one's first tile is
 };
+__device__ __forceinline__ int expert_of(uint32_t group) { return static_cast<int>(group >> 20); }
+__device__ __forceinline__ int wide_before(uint32_t group) { return static_cast<int>(group >> 10 & 0x3FFu); }
+__device__ __forceinline__ int rank_of(uint32_t group) { return static_cast<int>(group & 0x3FFu); }
 
 // Groups the pairs by expert, at most `limit` rows to a group.
 __device__ __forceinline__ void make_plan(const Args &a, const Plan &p, int limit) {
@@ -171,24 +174,45 @@ __device__ __forceinline__ void make_plan(const Args &a, const Plan &p, int limi
     if (bad && a.status && blockIdx.x == 0) *a.status = 1;
     __syncthreads();
     if (tid < 32) {
-        int before = 0;
+        int before = 0;  // groups, and << 16 those of them of two columns
         for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + tid, n = e < a.E ? (p.count[e] + limit - 1) / limit : 0;
-            int sum = n;
+            const int e = e0 + tid, rows = e < a.E ? p.count[e] : 0, n = (rows + limit - 1) / limit;
+            const int full = rows / limit, wide = (limit > 8 ? full : 0) + (rows - full * limit > 8 ? 1 : 0);
+            const int own = n | wide << 16;
+            int sum = own;
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(~0u, sum, o);
                 if (tid >= o) sum += v;
             }
-            for (int j = 0; j < n; ++j) p.group[before + sum - n + j] = static_cast<uint32_t>(e) << 16 | static_cast<uint32_t>(j * limit);
+            const int at = before + sum - own;
+            for (int j = 0; j < n; ++j)  // the full ones first
+                p.group[(at & 0xFFFF) + j] = static_cast<uint32_t>(e) << 20 | static_cast<uint32_t>((at >> 16) + (limit > 8 ? j : 0)) << 10 | static_cast<uint32_t>(j * limit);
             before += __shfl_sync(~0u, sum, 31);
         }
-        if (tid == 0) *p.num = before;
+        if (tid == 0) p.num[0] = before & 0xFFFF, p.num[1] = before >> 16;
     }
     __syncthreads();
 }
 
 __device__ __forceinline__ int rows_of(const Plan &p, uint32_t group, int limit) {
-    return min(limit, p.count[group >> 16] - static_cast<int>(group & 0xFFFFu));
+    return min(limit, p.count[expert_of(group)] - rank_of(group));
+}
+
+// This CTA's tiles, num[2] .. num[3] - 1 of all groups' in a row: equal shares, where a tile of a group of two columns
+// (more than eight rows) counts for kWide / kNarrow of another: with shares of as many tiles each, the CTA with most rows was
+// done 26% after the others (64 tokens, 128 experts, top 8, 2880 x 2880: the layer took 541 us, and 446 us this way).
+constexpr int kNarrow = 3, kWide = 4;
+__device__ __forceinline__ void take_share(const Plan &p, int per) {
+    const int groups = p.num[0], all = kNarrow * groups + (kWide - kNarrow) * p.num[1];
+    for (int i = threadIdx.x; i < 2 * groups; i += kThreads) {
+        const int g = i >> 1, which = i & 1, block = blockIdx.x + which;
+        const auto cost_before = [&](int j) { return j == groups ? all : kNarrow * j + (kWide - kNarrow) * wide_before(p.group[j]); };
+        const int from = cost_before(g), tile = cost_before(g + 1) - from;
+        const int64_t begin = static_cast<int64_t>(all) * per * block / gridDim.x - static_cast<int64_t>(from) * per;
+        if (begin >= 0 && begin < static_cast<int64_t>(tile) * per) p.num[2 + which] = g * per + static_cast<int>(begin / tile);
+        else if (g == groups - 1 && begin >= 0) p.num[2 + which] = groups * per;
+    }
+    __syncthreads();
 }
 
 // The pairs of the groups g0 .. g1-1, in their order, one warp to a group.
@@ -200,7 +224,7 @@ __device__ __forceinline__ void find_rows(const Args &a, const Plan &p, int g0, 
         for (int i = g0; i < g; ++i) base += rows_of(p, p.group[i], limit);
         if (lane == 0) p.base[g - g0] = base;
         const uint32_t group = p.group[g];
-        const int e = static_cast<int>(group >> 16), first = static_cast<int>(group & 0xFFFFu);
+        const int e = expert_of(group), first = rank_of(group);
         int n = 0;
         for (int i0 = 0; i0 < a.P && n < first + limit; i0 += 32) {
             const bool is = i0 + lane < a.P && p.ids[i0 + lane] == e;
@@ -318,13 +342,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     char *xs = smem + L::kFixed;
     float *sums = reinterpret_cast<float *>(xs + a.room * x_stride);
 
-    pdl_wait();
-    pdl_launch_dependents();
+    // fc 2 begins when all of fc 1 has waited for what is before it, the ids among them: only h is still to wait for, and
+    // the plan and the first weights are fetched meanwhile.
+    if (a.fc == 1) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     const int most_rows = min(limit, a.room);
     make_plan(a, plan, most_rows);
-    const int per = a.N / 16, total = *plan.num * per;
-    const int first = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x), last = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
-    if (first >= last) return;
+    const int per = a.N / 16, total = plan.num[0] * per;
+    if (total) take_share(plan, per);
+    const int first = total ? plan.num[2] : 0, last = total ? plan.num[3] : 0;
+    if (first >= last) {
+        if (a.fc == 2) pdl_wait();
+        return;
+    }
     // Slices of K: the fewest rounds of G tiles, a round's cost being its units and what opening and joining a tile takes
     const int most = (total + gridDim.x - 1) / gridDim.x;
     int S = 1, cost = 1 << 30;
@@ -352,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     const int64_t zfar = ZP ? a.zp - a.scales : 0;
     const auto open = [&]() {
         while (ahead >= (ahead_g + 1) * per) ++ahead_g;
-        const int64_t row = static_cast<int64_t>(plan.group[ahead_g] >> 16) * a.N + first_row(ahead - ahead_g * per);
+        const int64_t row = static_cast<int64_t>(expert_of(plan.group[ahead_g])) * a.N + first_row(ahead - ahead_g * per);
         src = reinterpret_cast<const char *>(a.w) + (row + cr * step) * row_bytes + (lane % C::kCopies) * C::kCopy + u0 * (SB * BITS / 8);
         ssrc = a.scales + (row + (lane >> 1 & 7) * step + (lane >> 4) * across) * nb;
     };
@@ -394,6 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     for (int i = 0; i < D - 1; ++i)
         if (u0 < u1) issue();
         else cp_commit();
+
+    if (a.fc == 2) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
 
     int drain = 0, flip = 0;
     uint32_t magic;  // a value that the compiler does not know stays in its register
@@ -563,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             while (tile >= (g + 1) * per) ++g;
             const uint32_t group = plan.group[g];
             const int n = rows_of(plan, group, most_rows), base = plan.base[g - g0];
-            if (NTMAX == 1 || n <= 8) run_tile(std::integral_constant<int, 1>{}, static_cast<int>(group >> 16), tile - g * per, base, n);
-            else run_tile(std::integral_constant<int, NTMAX>{}, static_cast<int>(group >> 16), tile - g * per, base, n);
+            if (NTMAX == 1 || n <= 8) run_tile(std::integral_constant<int, 1>{}, expert_of(group), tile - g * per, base, n);
+            else run_tile(std::integral_constant<int, NTMAX>{}, expert_of(group), tile - g * per, base, n);
         }
         g0 = g1;
     }
