@@ -291,3 +291,15 @@ def test_narrower_clusters(limit):
         check(X, target, 1.0, 20, call(X, target, 1.0, 20))
     finally:
         qg.qg_test_cluster_limit(before)
+
+
+@pytest.mark.parametrize("limit", [1, 2, 4, 8])
+@pytest.mark.parametrize("T,k", [(1, 20), (3, 64), (30, 5), (70, 0)])
+def test_rows_shared_by_fewer_ctas(limit, T, k):
+    """As many CTAs to a row as the device gives them."""
+    X, target = logits(T, 60000, "bf16", seed=T)
+    before = qg.qg_test_cluster_limit(limit)
+    try:
+        check(X, target, 0.9, k, call(X, target, 0.9, k))
+    finally:
+        qg.qg_test_cluster_limit(before)
