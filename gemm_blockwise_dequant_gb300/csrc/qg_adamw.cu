@@ -181,7 +181,9 @@ __device__ __forceinline__ uint2 encode(const float (&x)[8], float &scale) {
     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
     top = warp_top(top);
     // infinities: the codes of the others are zeros, and the state shows it (0 * inf is NaN); a NaN is a code of its own
-    const float inv = top >= kTinyBlock ? kCodeMax * 0.25f * reciprocal(top * 0.25f) : 0.f;
+    // The quotient rounded as fp32 has it: one for 256 values, and every unit in its last place moves a value in a million to
+    // the next code.
+    const float inv = top >= kTinyBlock ? __fdiv_rn(kCodeMax, top) : 0.f;
     scale = top >= kTinyBlock ? top * (1.f / kCodeMax) : 0.f;
     uint32_t w[2] = {0, 0};
     float2 y[4];
