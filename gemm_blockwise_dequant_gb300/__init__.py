@@ -243,8 +243,6 @@ def qmoe_decode_fused(x, expert_ids, expert_weights, *, num_experts, fc1_w, fc1_
                       workspace=None, stream=None, raw=False):
     """One-token fused QMoE decode (fc1 -> SwiGLU -> fc2, weighted over the k slots); y [hidden] float16."""
     hidden = x.shape[-1]
-    if bits not in (2, 4, 8):
-        raise ValueError("bits: 2, 4 or 8 is wanted")
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
     ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device, stream)
@@ -260,8 +258,6 @@ def qmoe_decode_fused_dp4a(x, expert_ids, expert_weights, *, num_experts, fc1_w,
                            status=None, workspace=None, stream=None, raw=False):
     """qmoe_decode_fused with int8 activations (per-block symmetric quantization, dp4a dot products)."""
     hidden = x.shape[-1]
-    if bits not in (2, 4, 8):
-        raise ValueError("bits: 2, 4 or 8 is wanted")
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
     ws, wsb = _workspace(lambda: qmoe_decode_workspace_bytes(k, hidden, inter), workspace, x.device, stream)
@@ -278,8 +274,6 @@ def qmoe_decode_fused_noalloc(x, expert_ids, expert_weights, *, num_experts, fc1
     """qmoe_decode_fused without a workspace: the library's fixed device scratch is used
     (callers that cannot allocate; shapes beyond QG_QMOE_NOALLOC_SCRATCH_BYTES are refused)."""
     hidden = x.shape[-1]
-    if bits not in (2, 4, 8):
-        raise ValueError("bits: 2, 4 or 8 is wanted")
     inter = fc2_w.shape[-1] * 8 // bits
     k = expert_ids.numel()
     s = lib().qmoe_decode_fused_noalloc(_ptr(x), _ptr(expert_ids), _ptr(expert_weights), k, num_experts,
