@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads * kGroups, 1) step_kernel(const __gri
                 const float norm = static_cast<float>(sqrt(sum));
                 if (blockIdx.x == 0 && p.norm) *p.norm = norm;
                 const float c = p.max_norm / (norm + p.norm_eps);
-                factor = norm < INFINITY ? (c > 1.f ? 1.f : c) : -1.f;
+                factor = norm < INFINITY ? (c <= 1.f ? c : 1.f) : -1.f;  // 0 / 0: nothing to clip
             }
         }
         __syncthreads();

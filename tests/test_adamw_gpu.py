@@ -228,3 +228,18 @@ def test_on_another_stream_and_without_tensors():
     norm = torch.ones(1, device="cuda")
     qg.qg_adamw_step(qg.QGAdamWList([], []), lr=LR, step=1, max_norm=1.0, norm=norm)
     assert float(norm) == 0
+
+
+@pytest.mark.parametrize("state", ["f32", "e4m3"])
+@pytest.mark.parametrize("max_norm,norm_eps,zero", [(0.0, 0.0, True), (0.0, 1e-6, True), (1.0, 0.0, True), (0.0, 1e-6, False), (math.inf, 0.0, False)])
+def test_clipping_of_nothing_to_nothing_and_by_any_bound(state, max_norm, norm_eps, zero):
+    """Gradients of zero, and bounds of zero and infinity: the moments decay, and gradients enter by 0 or as they are."""
+    c = Case([3000, 17], "f32", "f32", state, seed=10)
+    if zero:
+        for g in c.g:
+            g.zero_()
+    want, _ = step64(c, 3, None if max_norm > 0 or zero else 0.0)
+    norm = torch.empty(1, device="cuda")
+    qg.qg_adamw_step(c.list, lr=LR, step=3, betas=BETAS, eps=EPS, max_norm=max_norm, norm_eps=norm_eps, norm=norm)
+    check(c, want)
+    assert (float(norm) == 0) == zero
