@@ -847,13 +847,17 @@ def qmoe_tokens_workspace_bytes(tokens: int, k: int, hidden: int, inter: int) ->
 def _expert_sizes(w, scales, zp, bias, N, K, bits, block_size, what):
     """The number of experts of a projection [E, N, K]."""
     torch = _torch()
+    half = torch.float16
     E = w.shape[0]
-    nb = K // block_size if block_size > 0 else 0
+    blocks = (E, N, K // block_size if block_size > 0 else 0)
     if w.dtype != torch.uint8 or w.shape != (E, N, K * bits // 8) or not w.is_contiguous():
         raise ValueError("%s_w: [experts, %d, %d] uint8, contiguous, is wanted" % (what, N, K * bits // 8))
-    for t, shape in ((scales, (E, N, nb)), (zp, (E, N, nb)), (bias, (E, N))):
-        if t is not None and (t.dtype != torch.float16 or t.shape != shape or not t.is_contiguous()):
-            raise ValueError("%s: scales and zero points [experts, %d, %d] and biases [experts, %d] in float16, contiguous, are wanted" % (what, N, nb, N))
+    if scales.dtype != half or scales.shape != blocks or not scales.is_contiguous() \
+            or zp is not None and (zp.dtype != half or zp.shape != blocks or not zp.is_contiguous()) \
+            or bias is not None and (bias.dtype != half or bias.shape != (E, N) or not bias.is_contiguous()):
+        raise ValueError("%s: scales and zero points [experts, %d, %d] and biases [experts, %d] in float16, contiguous, are wanted" % (what, N, blocks[2], N))
+    if not (w.is_cuda and scales.is_cuda and (zp is None or zp.is_cuda) and (bias is None or bias.is_cuda)):
+        raise ValueError("%s: tensors of a GPU are wanted" % what)
     return E
 
 
@@ -881,7 +885,7 @@ def qmoe_tokens_fused(x, expert_ids, expert_weights, *, fc1_w, fc1_scales, fc1_z
     E = _expert_sizes(fc1_w, fc1_scales, fc1_zp, fc1_bias, 2 * inter, hidden, bits, block_size, "fc1")
     if _expert_sizes(fc2_w, fc2_scales, fc2_zp, fc2_bias, hidden, inter, bits, block_size, "fc2") != E:
         raise ValueError("fc1 and fc2: as many experts in both are wanted")
-    _on_gpu(x, expert_ids, expert_weights, fc1_w, fc1_scales, fc1_zp, fc1_bias, fc2_w, fc2_scales, fc2_zp, fc2_bias, y, status)
+    _on_gpu(x, expert_ids, expert_weights, y, status)
     L = lib()
     need = L.qmoe_tokens_workspace_bytes(T, k, hidden, inter) if workspace is None else 0
     st, wp, wb, _ = _stream_and_workspace(need, workspace, x, stream)
