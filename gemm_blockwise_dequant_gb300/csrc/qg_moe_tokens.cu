@@ -115,6 +115,7 @@ cudaError_t moe_tokens(const MoeTokens &q, void *ws, cudaStream_t s) {
     a.bs = q.bs;
     a.most_rows = q.T;
     a.status = q.status;
+    a.terms = 1;
     a.fc = 1;
     a.src = q.x;
     a.src_dtype = q.x_dtype;
@@ -139,6 +140,8 @@ cudaError_t moe_tokens(const MoeTokens &q, void *ws, cudaStream_t s) {
     a.K = q.inter;
     a.out = o;
     a.status = nullptr;
+    // h is fp32: one fp16 of it is off by as much as the rounding of an fp16 y, which two are not; beside that of a bf16 y it is nothing
+    a.terms = q.y_dtype == QG_BF16 ? 1 : 2;
     e = experts(a, s);
     if (e != cudaSuccess) return e;
     e = launch_pdl(combine_kernel, dim3((q.hidden / 4 + 127) / 128, q.T), dim3(128), 0, s, static_cast<const float *>(o), q.ids, q.weights, q.T, q.k, q.E,

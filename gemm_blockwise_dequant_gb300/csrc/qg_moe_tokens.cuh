@@ -6,8 +6,9 @@
 //
 // Bound by memory: every chosen expert's weights are read once, and with few rows each there are few operations to a
 // byte.  The pairs (token, slot) are grouped by expert, up to 16 rows to a group; a group's activations are laid out
-// once in shared memory, as fp16 with a power of two for each row (so fp16, bf16 and fp32 rows alike keep 11 bits or
-// more).  The weights go through m16n8k16 MMAs as the wide operand, 16 weight rows by 8 tokens: codes less the midpoint
+// once in shared memory, as fp16 with a power of two for each row (so fp16 and bf16 rows keep what they have).  h, which is
+// fp32, takes two rows of fp16 for a pair, neighbouring columns of the MMAs, where y is not bf16: with one, an fp16 y was up to 1.5
+// times as far off as its own rounding has it; with two no further (2 tokens 77 us instead of 75).  The weights go through m16n8k16 MMAs as the wide operand, 16 weight rows by 8 tokens: codes less the midpoint
 // are whole numbers that fp16 holds exactly, one block's products are summed by the MMA and its scale is applied to
 // the fp32 sums, so that nothing is rounded on the way.  A zero point other than the midpoint enters through the sum
 // of the block's activations.
@@ -158,8 +159,8 @@ __device__ __forceinline__ int expert_of(uint32_t group) { return static_cast<in
 __device__ __forceinline__ int wide_before(uint32_t group) { return static_cast<int>(group >> 10 & 0x3FFu); }
 __device__ __forceinline__ int rank_of(uint32_t group) { return static_cast<int>(group & 0x3FFu); }
 
-// Groups the pairs by expert, at most `limit` rows to a group.
-__device__ __forceinline__ void make_plan(const Args &a, const Plan &p, int limit) {
+// Groups the pairs by expert, at most `limit` to a group; more than `narrow` take two columns.
+__device__ __forceinline__ void make_plan(const Args &a, const Plan &p, int limit, int narrow) {
     const int tid = threadIdx.x;
     for (int e = tid; e < a.E; e += kThreads) p.count[e] = 0;
     __syncthreads();
@@ -177,7 +178,7 @@ __device__ __forceinline__ void make_plan(const Args &a, const Plan &p, int limi
         int before = 0;  // groups, and << 16 those of them of two columns
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + tid, rows = e < a.E ? p.count[e] : 0, n = (rows + limit - 1) / limit;
-            const int full = rows / limit, wide = (limit > 8 ? full : 0) + (rows - full * limit > 8 ? 1 : 0);
+            const int full = rows / limit, wide = (limit > narrow ? full : 0) + (rows - full * limit > narrow ? 1 : 0);
             const int own = n | wide << 16;
             int sum = own;
             for (int o = 1; o < 32; o <<= 1) {
@@ -186,7 +187,7 @@ __device__ __forceinline__ void make_plan(const Args &a, const Plan &p, int limi
             }
             const int at = before + sum - own;
             for (int j = 0; j < n; ++j)  // the full ones first
-                p.group[(at & 0xFFFF) + j] = static_cast<uint32_t>(e) << 20 | static_cast<uint32_t>((at >> 16) + (limit > 8 ? j : 0)) << 10 | static_cast<uint32_t>(j * limit);
+                p.group[(at & 0xFFFF) + j] = static_cast<uint32_t>(e) << 20 | static_cast<uint32_t>((at >> 16) + (limit > narrow ? j : 0)) << 10 | static_cast<uint32_t>(j * limit);
             before += __shfl_sync(~0u, sum, 31);
         }
         if (tid == 0) p.num[0] = before & 0xFFFF, p.num[1] = before >> 16;
@@ -252,7 +253,9 @@ __device__ __forceinline__ void load_values(const void *src, int dtype, size_t a
     }
 }
 
-// n rows of activations as scaled fp16, eight at a time in the order of the codes' pairs.  A row is the work of as many
+// The second of two terms is what the first leaves, times kSecond (11 bits more).
+constexpr float kSecond = 2048.f;
+// The activations of n pairs as scaled fp16, eight at a time in the order of the codes' pairs: a row for each, or two.  A row is the work of as many
 // threads as there are for it; with up to kHeld vectors each they read it once.
 template <int BITS, int SB, bool ZP, int NT>
 __device__ __forceinline__ void stage_rows(const Args &a, const Plan &p, int n, char *xs, float *sums) {
@@ -290,21 +293,31 @@ __device__ __forceinline__ void stage_rows(const Args &a, const Plan &p, int n, 
         if (lane == 0) p.back[r] = exp2i(-max(up, -126)) / low;
         const auto put = [&](int q, const float (&x)[8]) {
             uint32_t w[4];
-            uint16_t h[8];
-            float sum = 0.f;
+            uint16_t h[8], l[8];
+            float sum = 0.f, sum2 = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                h[i] = f2h(x[i] * scale * low);
-                if constexpr (ZP) sum += h2f(h[i]);
+                const float y = x[i] * scale * low;
+                h[i] = f2h(y);
+                l[i] = a.terms == 2 ? f2h((y - h2f(h[i])) * kSecond) : 0;
+                if constexpr (ZP) sum += h2f(h[i]), sum2 += h2f(l[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = h[order<BITS>(2 * i)] | static_cast<uint32_t>(h[order<BITS>(2 * i + 1)]) << 16;
-            *reinterpret_cast<uint4 *>(xs + r * stride + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(xs + r * a.terms * stride + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (a.terms == 2) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = l[order<BITS>(2 * i)] | static_cast<uint32_t>(l[order<BITS>(2 * i + 1)]) << 16;
+                *reinterpret_cast<uint4 *>(xs + (2 * r + 1) * stride + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
             if constexpr (ZP) {
                 // SB / 8 neighbouring threads hold a block, and all of them are here: K / 8 is a multiple of SB / 8
                 const unsigned quad = ((1u << (SB / 8)) - 1u) << (threadIdx.x & 31 & ~(SB / 8 - 1));
-                for (int o = 1; o < SB / 8; o <<= 1) sum += __shfl_xor_sync(quad, sum, o);
-                if (q % (SB / 8) == 0) sums[r * (a.K / SB) + q / (SB / 8)] = sum;
+                for (int o = 1; o < SB / 8; o <<= 1) sum += __shfl_xor_sync(quad, sum, o), sum2 += __shfl_xor_sync(quad, sum2, o);
+                if (q % (SB / 8) == 0) {
+                    sums[r * a.terms * (a.K / SB) + q / (SB / 8)] = sum;
+                    if (a.terms == 2) sums[(2 * r + 1) * (a.K / SB) + q / (SB / 8)] = sum2;
+                }
             }
         };
 #pragma unroll
@@ -323,7 +336,7 @@ template <int BITS, int SB, bool ZP, int NTMAX>
 __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ Args a) {
     using C = Codes<BITS, SB>;
     using L = Layout<BITS, SB, ZP, NTMAX>;
-    constexpr int D = L::kStages, CU = C::kUnits, limit = 8 * NTMAX;
+    constexpr int D = L::kStages, CU = C::kUnits;
     extern __shared__ __align__(128) char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     char *ring = smem + warp * (D * L::kStage);
@@ -348,8 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         pdl_wait();
         pdl_launch_dependents();
     }
-    const int most_rows = min(limit, a.room);
-    make_plan(a, plan, most_rows);
+    const int two = a.terms - 1, room = a.room >> two;  // pairs whose rows fit
+    const int most_rows = min(8 * NTMAX >> two, room);
+    make_plan(a, plan, most_rows, 8 / a.terms);
     const int per = a.N / 16, total = plan.num[0] * per;
     if (total) take_share(plan, per);
     const int first = total ? plan.num[2] : 0, last = total ? plan.num[3] : 0;
@@ -560,19 +574,23 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 }
             }
             const float bias0 = a.bias ? h2f(a.bias[static_cast<int64_t>(expert) * a.N + n0]) : 0.f, bias1 = a.bias ? h2f(a.bias[static_cast<int64_t>(expert) * a.N + n1]) : 0.f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int r = j * 8 + 2 * t4 + c;
-                if (r >= rows) continue;
-                const float back = plan.back[base + r];
-                const float p = fmaf(c ? v.y : v.x, back, bias0), q = fmaf(c ? v.w : v.z, back, bias1);
-                const int64_t pair = plan.rows[base + r];
+            const auto store = [&](int r, float x0, float x1) {  // a pair's values of rows g8 and g8 + 8
+                const float back = plan.back[(base >> two) + r];
+                const float p = fmaf(x0, back, bias0), q = fmaf(x1, back, bias1);
+                const int64_t pair = plan.rows[(base >> two) + r];
                 if (a.fc == 1) {
                     a.out[pair * (a.N / 2) + tile * 8 + g8] = p / (1.f + __expf(-p)) * q;
                 } else {
                     a.out[pair * a.N + n0] = p;
                     a.out[pair * a.N + n1] = q;
                 }
+            };
+            const int col = j * 8 + 2 * t4;
+            if (two) {  // the terms of a pair are neighbouring columns
+                if (col < rows) store(col >> 1, fmaf(v.y, 1.f / kSecond, v.x), fmaf(v.w, 1.f / kSecond, v.z));
+            } else {
+                if (col < rows) store(col, v.x, v.z);
+                if (col + 1 < rows) store(col + 1, v.y, v.w);
             }
         }
         flip ^= 1;
@@ -586,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         int g1 = g0, rows = 0;
         while (g1 < g_end) {
             const int n = rows_of(plan, plan.group[g1], most_rows);
-            if (rows + n > a.room) break;
+            if (rows + n > room) break;
             rows += n;
             ++g1;
         }
@@ -599,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         for (; tile < end; tile += G) {
             while (tile >= (g + 1) * per) ++g;
             const uint32_t group = plan.group[g];
-            const int n = rows_of(plan, group, most_rows), base = plan.base[g - g0];
+            const int n = rows_of(plan, group, most_rows) << two, base = plan.base[g - g0] << two;
             if (NTMAX == 1 || n <= 8) run_tile(std::integral_constant<int, 1>{}, expert_of(group), tile - g * per, base, n);
             else run_tile(std::integral_constant<int, NTMAX>{}, expert_of(group), tile - g * per, base, n);
         }
@@ -613,10 +631,11 @@ cudaError_t launch_one(Args a, cudaStream_t s) {
     using L = Layout<BITS, SB, ZP, NT>;
     const auto kern = expert_kernel<BITS, SB, ZP, NT>;
     const int avail = device_info().max_smem_optin - L::kFixed;
-    int room = std::min(kMaxRows, a.P);
+    int room = std::min(kMaxRows, a.P * a.terms);
     while (room > 0 && L::x_bytes(a.K, room) > avail) --room;
     if (room == 0) return cudaErrorNotSupported;
-    if (NT == 2 && room < kMaxRows && room < a.P) return launch_one<BITS, SB, ZP, 1>(a, s);
+    if (room < a.terms) a.terms = 1;  // rows so long that one fits
+    if (NT == 2 && room < kMaxRows && room < a.P * a.terms) return launch_one<BITS, SB, ZP, 1>(a, s);
     a.room = room;
     static std::atomic<unsigned long long> done{0};  // a bit for each device
     const int slot = device_slot();
@@ -638,7 +657,7 @@ bool experts_fit(int K, int bs, bool zp) {
 // Two columns of MMAs where more than eight tokens may meet at one expert.
 template <int BITS>
 cudaError_t launch_experts(const Args &a, cudaStream_t s) {
-    const bool two = a.most_rows > 8;
+    const bool two = a.most_rows * a.terms > 8;
     if (a.bs == 32) {
         if (a.zp) return two ? launch_one<BITS, 32, true, 2>(a, s) : launch_one<BITS, 32, true, 1>(a, s);
         return two ? launch_one<BITS, 32, false, 2>(a, s) : launch_one<BITS, 32, false, 1>(a, s);

@@ -21,6 +21,7 @@ struct Args {
     float *out;             // fc 1: [P][N / 2]; fc 2: [P][N]
     int *status;            // or null
     int most_rows;          // that can meet at one expert, were every token's choices different
+    int terms;              // fp16 values that an activation enters as: 1 or 2, each with a row (and an MMA column) of its own
     int room;               // rows of activations that fit (filled in at the launch)
 };
 template <int BITS>

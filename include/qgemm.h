@@ -663,17 +663,17 @@ int qg_token_logprobs_grad(const void *X, int x_dtype, int64_t ldx, const int64_
  *
  * qmoe_tokens_fused -- the layer of qmoe_decode_fused over a few tokens at once, each with k experts of its own:
  *   y[t] = round( sum_j expert_weights[t][j] * o_tj ),  o_tj as there, from x[t] and expert expert_ids[t][j]
- * Every chosen expert's weights are read once for all its tokens (16 of them at a time; fewer where hidden or inter is
- * above some 2,800).  Weights, scales, zero points, biases, block sizes and swiglu_interleaved as qmoe_decode_fused; bits 2, 4 or 8.
+ * Every chosen expert's weights are read once for all its tokens (16 of them at a time, 8 in the second product of an
+ * fp16 or fp32 y; fewer where hidden or inter is above some 2,800).  Weights, scales, zero points, biases, block sizes and swiglu_interleaved as qmoe_decode_fused; bits 2, 4 or 8.
  *   x            [tokens][hidden] fp16 or bf16 (fp32: QG_ERR_UNSUPPORTED)
  *   expert_ids, expert_weights  [tokens][k] int32 and fp32 (device), k 1 .. 16, tokens * k at most 1024, num_experts at
  *                most 512; an id outside [0, num_experts) adds nothing and sets *status_dev to 1 (it may be NULL and is
  *                never cleared); one that a token has twice counts twice
  *   y            [tokens][hidden] of y_dtype
  *   workspace    at least qmoe_tokens_workspace_bytes(tokens, k, hidden, inter) bytes, 16-byte aligned
- * Activations, and h between the products, enter the products as fp16 scaled by a power of two for each row (11 bits for
- * what is above 2^-29 of the row's largest); codes, scales and zero points are exact; sums in fp32.  A row with an
- * infinity or NaN gives outputs that are not finite, the other rows are not touched by it.
+ * Activations enter the products as fp16 scaled by a power of two for each row (11 bits for what is above 2^-29 of the
+ * row's largest), h between the products as two such values (22 bits) or, where y is bf16 or inter above some 20,000, as one; codes, scales and zero
+ * points are exact; sums in fp32.  A row with an infinity or NaN gives outputs that are not finite, the other rows are not touched by it.
  * Deterministic; the order of a sum depends on the shape and on how many experts were chosen.  A hidden or inter whose
  * rows do not fit the kernel's shared memory (some 30,000 and more) is QG_ERR_UNSUPPORTED.  More tokens: qmoe_ragged_mm.
  */

@@ -33,14 +33,14 @@ def weight64(w, name, e, bits, bs):
     return ((q - z) * scales[..., None]).flatten(1)
 
 
-def layer64(x, ids, weights, w, bits, bs, interleaved=0):
+def layer64(x, ids, weights, w, bits, bs, interleaved=0, half=2.0 ** -11):
     """(y, what y may be off before its rounding)."""
     E, H = w["fc1_w"].shape[0], x.shape[1]
     y = torch.zeros(x.shape[0], H, dtype=torch.float64, device="cuda")
     off = torch.zeros_like(y)
     # fp32 sums of a block by the MMAs and of the blocks: 2^-18 of the magnitudes; fp16 of a row: 2^-11 of h (x is exact but
-    # where it is 2^-29 of its row's largest)
-    sums, half = 2.0 ** -18, 2.0 ** -11
+    # where it is 2^-29 of its row's largest); half: of h where it is one fp16
+    sums = 2.0 ** -18
     for e in range(E):
         t, j = (ids == e).nonzero(as_tuple=True)
         if t.numel() == 0:
@@ -253,3 +253,31 @@ def test_route_of_masked_infinite_and_nan_logits():
         assert int(ids[3, 0]) == 6 and weights[3, 0].isnan()
         assert ids[4].tolist() == [0, 1, 2, 3, 4] and torch.allclose(weights[4], torch.full((5,), 0.2 if renormalize else 0.025, device="cuda"))
         assert (ids[5] % 2 == 1).all()
+
+
+@pytest.mark.parametrize("zp", [False, True])
+@pytest.mark.parametrize("bits,bs", [(2, 32), (2, 64), (4, 32), (4, 128), (8, 32), (8, 64)])
+@pytest.mark.parametrize("T,E,k", [(1, 3, 2), (5, 4, 3), (9, 3, 3), (40, 5, 2)])
+def test_the_inner_activations_keep_their_bits(T, E, k, bits, bs, zp):
+    """An fp32 y is as far off as two fp16 terms of h and the sums are, an fp16 y hardly further than its rounding."""
+    H, I = 384, 640
+    w = layer(E, H, I, bits, bs, zp, True, seed=T)
+    X = torch.randn(T, H, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").half()
+    ids, weights = choose(T, E, k, seed=T)
+    y, off = layer64(X, ids, weights, w, bits, bs, half=2.0 ** -21)
+    got = run(X, ids, weights, w, bits, bs, y=torch.empty(T, H, device="cuda"))
+    assert ((got.double() - y).abs() <= off + 2.0 ** -23 * y.abs()).all()
+    # sums that are off by no more than 2^-18 of their terms' magnitudes; those are some ten times the sum
+    assert (got.double() - y).norm() <= 2.0 ** -14 * y.norm()
+    rounded, best = run(X, ids, weights, w, bits, bs), y.half()
+    assert (rounded.double() - y).norm() <= 1.05 * (best.double() - y).norm()
+
+
+def test_long_rows_in_two_terms():
+    """Rows of which a pair's two just fit, or one alone does."""
+    for I in (17920, 26624, 30720):
+        w = layer(3, 128, I, 4, 64)
+        X = torch.randn(5, 128, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").half()
+        ids, weights = choose(5, 3, 2)
+        out = torch.empty(5, 128, device="cuda")
+        check(run(X, ids, weights, w, 4, 64, y=out), X, ids, weights, w, 4, 64)
