@@ -8,18 +8,18 @@
 // byte.  The pairs (token, slot) are grouped by expert, up to 16 rows to a group; a group's activations are laid out
 // once in shared memory, as fp16 with a power of two for each row (so fp16 and bf16 rows keep what they have).  h, which is
 // fp32, takes two rows of fp16 for a pair, neighbouring columns of the MMAs, where y is not bf16: with one, an fp16 y was up to 1.5
-// times as far off as its own rounding has it; with two no further (2 tokens 77 us instead of 75).  The weights go through m16n8k16 MMAs as the wide operand, 16 weight rows by 8 tokens: codes less the midpoint
-// are whole numbers that fp16 holds exactly, one block's products are summed by the MMA and its scale is applied to
-// the fp32 sums, so that nothing is rounded on the way.  A zero point other than the midpoint enters through the sum
-// of the block's activations.
+// times as far off as its own rounding has it; with two no further (2 tokens 77 us instead of 75).  The weights go through
+// m16n8k16 MMAs as the wide operand, 16 weight rows by 8 tokens: codes less the midpoint are whole numbers that fp16 holds
+// exactly, one block's products are summed by the MMA and its scale is applied to the fp32 sums, so that nothing is rounded
+// on the way.  A zero point other than the midpoint enters through the sum of the block's activations.
 //
 // Each warp streams its weights through a ring of its own (cp.async, no barrier between warps); S warps share a tile
 // of 16 rows, each with a slice of K, and G = 16 / S tiles are worked on at a time.  S is chosen from the number of
 // tiles, so that few of them still fill the warps.  A tile of fc1 is 8 gate rows and their 8 up rows: both values of an
 // output meet in one lane.
 //
-// Measured (128 experts, top 8, 2880 x 2880, 4 bits in blocks of 32; the whole layer): 64 tokens 448 us, 1.87 GB of weights at 4.2 TB/s, of
-// which the copies alone, in pieces of 128 bytes, take 396; 2 tokens 77 us.
+// Measured (128 experts, top 8, 2880 x 2880, 4 bits in blocks of 32; the whole layer): 64 tokens 448 us, 1.87 GB of weights at
+// 4.2 TB/s, of which the copies alone, in pieces of 128 bytes, take 396; 2 tokens 77 us.
 #pragma once
 
 #include <algorithm>
@@ -169,7 +169,7 @@ __device__ __forceinline__ void make_plan(const Args &a, const Plan &p, int limi
     __syncthreads();
     bool bad = false;
     for (int i = tid; i < a.P; i += kThreads) {
-        const int e = a.ids[i];
+        const int e = __ldcg(a.ids + i);  // from the L2: fc 2 comes here before its own wait
         const bool ok = e >= 0 && e < a.E;
         p.ids[i] = static_cast<int16_t>(ok ? e : -1);
         if (ok) atomicAdd(&p.count[e], 1);
