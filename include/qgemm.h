@@ -580,6 +580,11 @@ int qg_clip_grad_norm(const qg_grad_tensor *tensors_dev, int count, int64_t chun
  *                   exp_avg_sq_scale, [ceil(numel / QG_STATE_BLOCK)].  A step stores round(x / scale), scale = the
  *                   block's largest magnitude / 448 (a block below 1e-30 is stored as zeros with scale 0), u above
  *                   zero never as zero; p' uses m' and v' before that rounding.  All zeros is the state to begin with.
+ * The moments are evaluated as they stand above, each product, sum and root rounded to fp32 by itself, and so are codes and
+ * scales: round(x * (448 * (1 / amax))) and amax * (1 / 448).  An fp32 program of the same operations therefore keeps the same
+ * 8-bit states.  One that orders them otherwise parts from these: a unit in the last place moves one value in a million to the
+ * next code, which is up to 7% of it, and where that value comes to be the largest of its block, a scale is off by as much.
+ * So does a norm whose last bit is another.  A g'^2 past fp32's range is infinity.
  * A block of a QG_STATE_E4M3 state that an infinity or NaN enters holds NaN from then on; values outside the block keep theirs.
  *
  *   tensors     the list in DEVICE memory, laid out by qg_adamw_list_init from a host array (it holds addresses).
