@@ -121,7 +121,7 @@ struct Logits<1> {
         return d;
     }
     static __device__ __forceinline__ float value(uint32_t w) { return max_nan(h2f(static_cast<uint16_t>(w)), h2f(static_cast<uint16_t>(w >> 16))); }
-    static __device__ __forceinline__ uint32_t word(float x) { return f2h(fmaxf(x, -65504.f)) * 0x10001u; }
+    static __device__ __forceinline__ uint32_t word(float x) { return f2h(x) * 0x10001u; }
 };
 template <>
 struct Logits<2> {
@@ -225,7 +225,8 @@ struct ScoreArgs {
     int64_t ldx;
     const int64_t *target;
     int T, V, top;
-    float inv_t, c, back;  // c = inv_t * log2(e), back = 1 / c
+    float inv_t, c;      // c = inv_t * log2(e)
+    float reach, least;  // 130 / c; the least reference that a value of the type lies so far below (infinity: none)
     float *logprob, *entropy, *lse;
     int64_t *top_ids;
     float *top_logprobs;
@@ -330,10 +331,11 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
         if (!(top < INFINITY)) bad = true;  // NaN, or an infinity whose differences are NaN
         if (top > -INFINITY) {
             move_reference(t, top, p.c);
-            if (fabsf(t.ref) <= 16384.f) {
+            if (fabsf(t.ref) <= 16384.f && t.ref >= p.least) {
                 // What is 2^-130 of the reference or less counts as about that, -inf too: its product with its logarithm is a
-                // number.  |ref| / 64 is more than the type's step there.
-                const uint32_t low = L::word(t.ref - fmaxf(130.f * p.back, fabsf(t.ref) * 0.015625f));
+                // number.  |ref| / 64 is more than the type's step there.  Where the type has no such value (fp16 at temperatures
+                // above some 700), -inf would count as its lowest one: those logits are taken one by one below.
+                const uint32_t low = L::word(t.ref - fmaxf(p.reach, fabsf(t.ref) * 0.015625f));
                 const float2 ref = make_float2(-t.ref, -t.ref), c = make_float2(p.c, p.c);
                 float2 s0 = make_float2(0.f, 0.f), a0 = s0;
 #pragma unroll
@@ -584,8 +586,10 @@ cudaError_t launch_score(const ScoreArgs &a, int want, cudaStream_t s) {
 }  // namespace
 
 cudaError_t token_logprobs(const TokenLogprobs &q, cudaStream_t s) {
-    const double log2e = 1.4426950408889634;
-    const ScoreArgs a{q.X, q.ldx, q.target, q.T, q.V, q.top, q.inv_t, static_cast<float>(q.inv_t * log2e), static_cast<float>(1.0 / (q.inv_t * log2e)), q.logprob, q.entropy, q.lse, q.top_ids, q.top_logprobs, q.status};
+    const double c = q.inv_t * 1.4426950408889634;
+    const bool fits = c >= 1e-36 && c <= (q.x_dtype == 1 ? 1e9 : 1e36);  // 130 / c and c * 256 are finite, and 130 / c is above the type's least step
+    const float reach = fits ? static_cast<float>(130.0 / c) : 0.f, least = fits ? reach - (q.x_dtype == 1 ? 65504.f : 3e38f) : INFINITY;
+    const ScoreArgs a{q.X, q.ldx, q.target, q.T, q.V, q.top, q.inv_t, static_cast<float>(c), reach, least, q.logprob, q.entropy, q.lse, q.top_ids, q.top_logprobs, q.status};
     // CTAs of a row: as many as are on the SMs at a time, two on each, as long as each has a step of its own to do (64 rows of
     // 100352 bf16 with 5 alternatives: 4 CTAs each 14 us, 8 take two turns, 24; one row of 100352 fp32: 16 CTAs are 0.3 us
     // slower than 8, their join costs more)

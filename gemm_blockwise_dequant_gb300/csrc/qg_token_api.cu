@@ -13,6 +13,7 @@ bool valid_dtype(int d) { return d == QG_F32 || d == QG_F16 || d == QG_BF16; }
 size_t esize(int d) { return d == QG_F32 ? 4 : 2; }
 
 constexpr int kMaxRows = 1 << 20, kMaxVocab = 1 << 28, kMaxTop = 64;
+constexpr float kMaxInvTemperature = 2.3e38f;  // times log2(e) it is finite
 // Every CTA of the expert products groups all pairs by expert before it begins: more of them are a ragged GEMM's work.
 constexpr int kMaxSlots = 16, kMaxPairs = 1024, kMaxExperts = 512;
 
@@ -41,7 +42,7 @@ int qg_token_logprobs(const void *X, int x_dtype, int64_t ldx, const int64_t *ta
     const int st = check_logits(X, x_dtype, ldx, targets, rows, vocab, inv_temperature);
     if (st != QG_OK) return st;
     if (top_k < 0 || top_k > vocab) return QG_ERR_INVALID_ARG;
-    if (top_k > kMaxTop) return QG_ERR_UNSUPPORTED;
+    if (top_k > kMaxTop || inv_temperature > kMaxInvTemperature) return QG_ERR_UNSUPPORTED;
     if (!aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(top_ids, 8) || !aligned(top_logprobs, 4) || !aligned(status_dev, 4))
         return QG_ERR_INVALID_ARG;
     if (rows == 0) return QG_OK;

@@ -633,7 +633,7 @@ int qg_adamw_step(const qg_adamw_tensor *tensors_dev, int count, int64_t chunks,
  *   X            [rows] rows of vocab values, ldx values apart; x_dtype; any alignment of its type
  *   targets      [rows] int64 (device), or NULL (none).  Negative: no token is given, logprob 0.  At or past vocab:
  *                the same, and *status_dev is set to 1 (it may be NULL and is never cleared).
- *   inv_temperature  finite, above 0
+ *   inv_temperature  finite, above 0 (in qg_token_logprobs at most 2.3e38: QG_ERR_UNSUPPORTED)
  *   logprob, entropy, lse  [rows] fp32, each may be NULL
  *   top_k        0 .. 64 and at most vocab (0: top_ids and top_logprobs may be NULL)
  *   top_ids      [rows][top_k] int64;  top_logprobs  [rows][top_k] fp32
