@@ -270,13 +270,20 @@ struct List {
 int list_bytes(int count) { return std::min(count, kTable) * static_cast<int>(sizeof(Entry)); }
 static_assert(sizeof(Entry) % 16 == 0, "read in 16-byte pieces");
 
+// Nothing but zeros: eight squares whose sum is 0 may also have left fp32's range.
+__device__ __forceinline__ bool all_zero(const float (&g)[8]) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) any |= __float_as_uint(g[k]);
+    return any << 1 == 0;
+}
 // The sum of squares of eight values in fp32, or in fp64 where that leaves its range.
 __device__ __forceinline__ double squares(const float (&g)[8]) {
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 8; ++k) s[k & 1] = fmaf(g[k], g[k], s[k & 1]);
     const float sum = s[0] + s[1];
-    if (sum >= 1e-30f && sum <= 3e38f) return sum;
+    if ((sum >= 1e-30f && sum <= 3e38f) || all_zero(g)) return sum;
     double wide = 0.0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) wide += static_cast<double>(g[k]) * g[k];
@@ -303,7 +310,8 @@ __device__ __forceinline__ double squares_of_some(const void *grad, int64_t e, i
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[k & 1] = fmaf(g[k], g[k], q[k & 1]);
         const float sum = q[0] + q[1];
-        fits = fits && ((sum >= 1e-30f && sum <= 3e37f) || i >= parts);
+        // zeros (of tensors that no token reached) are as quick as other gradients: they took 2.8 times as long one by one
+        fits = fits && ((sum >= 1e-30f && sum <= 3e37f) || all_zero(g));
         s += sum;
     }
     if (fits) return s;
