@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     float *sums = reinterpret_cast<float *>(xs + a.room * x_stride);
 
     // fc 2 begins when all of fc 1 has waited for what is before it, the ids among them: only h is still to wait for, and
-    // the plan and the first weights are fetched meanwhile.
+    // the plan and the first codes are fetched meanwhile, past the first-level cache: that may hold what the same addresses had before a kernel
+    // ahead of this layer wrote there, and only the wait says that it does not.
     if (a.fc == 1) {
         pdl_wait();
         pdl_launch_dependents();
@@ -407,12 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     };
     if (ahead < last && u0 < u1) open();
     uint32_t fill = 0;  // bytes
-    const auto issue = [&]() {
+    // A stage of the ring: its codes, its scales and zero points, or both.
+    const auto issue = [&](auto codes_tag, auto params_tag) {
+        constexpr bool CODES = decltype(codes_tag)::value, PARAMS = decltype(params_tag)::value;
         if (ahead < last) {
             const int left = u1 - ahead_u;  // units
             const bool there = (lane % C::kCopies) * (C::kCopy * 8 / BITS) < left * SB;
 #pragma unroll
-            for (int i = 0; i < C::kPerLane; ++i) {
+            for (int i = 0; i < (CODES ? C::kPerLane : 0); ++i) {
                 // kCopies 4: rows cr, cr + 8; 8: cr, cr + 4, cr + 8, cr + 12
                 const char *from = src + (C::kCopies == 4 ? (i ? far8 : 0) : (i & 1 ? far4 : 0) + (i & 2 ? far8 : 0));
                 cp_async_if<C::kCopy>(there, code_to + fill + i * (32 / C::kCopies) * C::kStride, from);
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             const int behind = (static_cast<int>(s0 >> 1 & 1) + b1 - b0) >> 1;
             const char *word = reinterpret_cast<const char *>(s0 & ~static_cast<uintptr_t>(3)) + (lane & 1) * 4;
 #pragma unroll
-            for (int i = 0; i < (C::kParWords + 1) / 2; ++i) {
+            for (int i = 0; i < (PARAMS ? (C::kParWords + 1) / 2 : 0); ++i) {
                 cp_async_if<4>((lane & 1) + 2 * i <= behind, par_to + fill + 8 * i, word + 8 * i);
                 if constexpr (ZP) cp_async_if<4>((lane & 1) + 2 * i <= behind, par_to + fill + L::kParams + 8 * i, word + 2 * zfar + 8 * i);
             }
@@ -437,16 +440,32 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 if (ahead < last) open();
             }
         }
-        cp_commit();
+        if constexpr (PARAMS) cp_commit();
     };
-#pragma unroll 1
-    for (int i = 0; i < D - 1; ++i)
-        if (u0 < u1) issue();
-        else cp_commit();
-
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
     if (a.fc == 2) {
+        constexpr bool EARLY = C::kCopy == 16;  // smaller copies go through the first-level cache
+        const int ahead0 = ahead, ahead_g0 = ahead_g;
+        const char *const src0 = src;
+        const uint16_t *const ssrc0 = ssrc;
+        if constexpr (EARLY) {
+#pragma unroll 1
+            for (int i = 0; i < D - 1 && u0 < u1; ++i) issue(yes, no);
+            ahead = ahead0, ahead_g = ahead_g0, ahead_u = u0, src = src0, ssrc = ssrc0, fill = 0;
+        }
         pdl_wait();
         pdl_launch_dependents();
+        // the codes of all these stages are waited for with the scales of the first
+#pragma unroll 1
+        for (int i = 0; i < D - 1; ++i)
+            if (u0 < u1) issue(std::bool_constant<!EARLY>{}, yes);
+            else cp_commit();
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < D - 1; ++i)
+            if (u0 < u1) issue(yes, yes);
+            else cp_commit();
     }
 
     int drain = 0, flip = 0;
@@ -532,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         for (int u = u0; u < u1; u += CU) {
             cp_wait<D - 2>();
             __syncwarp();  // also: everyone has read the stage before, which the next copy goes to
-            issue();
+            issue(yes, yes);
             const char *row0 = codes + drain;
             const uint16_t *sc = reinterpret_cast<const uint16_t *>(ring + drain + 16 * C::kStride) + g8 * (L::kParRow / 2);
             const int b0 = u >> shift;
