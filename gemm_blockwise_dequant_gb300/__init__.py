@@ -444,10 +444,19 @@ def _rows2d(t, rows, cols, what):
 
 
 def _on_gpu(*tensors):
-    """The library takes addresses: one of the host would go unnoticed."""
+    """The library takes addresses and works on the current device: one of the host, or of another device, would go unnoticed until a kernel follows it."""
+    here = -1
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("tensors of a GPU are wanted")
+        if t is not None:
+            at = t.get_device()
+            if at < 0:
+                raise ValueError("tensors of a GPU are wanted")
+            if at != here:
+                if here >= 0:
+                    raise ValueError("tensors of one GPU are wanted")
+                here = at
+    if here >= 0 and here != _torch()._C._cuda_getDevice():
+        raise ValueError("tensors of the current device are wanted")
 
 
 def _adapter_sizes(A, B, scaling, seg_offsets, seg_adapter, status):
@@ -747,6 +756,7 @@ def qg_adamw_step(tensors, *, lr, step, betas=(0.9, 0.999), eps=1e-8, max_norm=N
     norm_dev = None if norm is None else _device_scalar(norm, torch.float32, "norm")
     if max_norm is not None and not max_norm >= 0:
         raise ValueError("max_norm: a number that is not negative, or None, is wanted")
+    _on_gpu(tensors.table, None if lr_dev is None else lr, None if step_dev is None else step, norm, workspace)
     st, wp, wb, _ = _stream_and_workspace(0, tensors.workspace if workspace is None else workspace, tensors.table, stream)
     if stream is not None:
         tensors.table.record_stream(stream)
@@ -856,8 +866,6 @@ def _expert_sizes(w, scales, zp, bias, N, K, bits, block_size, what):
             or zp is not None and (zp.dtype != half or zp.shape != blocks or not zp.is_contiguous()) \
             or bias is not None and (bias.dtype != half or bias.shape != (E, N) or not bias.is_contiguous()):
         raise ValueError("%s: scales and zero points [experts, %d, %d] and biases [experts, %d] in float16, contiguous, are wanted" % (what, N, blocks[2], N))
-    if not (w.is_cuda and scales.is_cuda and (zp is None or zp.is_cuda) and (bias is None or bias.is_cuda)):
-        raise ValueError("%s: tensors of a GPU are wanted" % what)
     return E
 
 
@@ -885,7 +893,7 @@ def qmoe_tokens_fused(x, expert_ids, expert_weights, *, fc1_w, fc1_scales, fc1_z
     E = _expert_sizes(fc1_w, fc1_scales, fc1_zp, fc1_bias, 2 * inter, hidden, bits, block_size, "fc1")
     if _expert_sizes(fc2_w, fc2_scales, fc2_zp, fc2_bias, hidden, inter, bits, block_size, "fc2") != E:
         raise ValueError("fc1 and fc2: as many experts in both are wanted")
-    _on_gpu(x, expert_ids, expert_weights, y, status)
+    _on_gpu(x, expert_ids, expert_weights, y, status, fc1_w, fc1_scales, fc1_zp, fc1_bias, fc2_w, fc2_scales, fc2_zp, fc2_bias, workspace)
     L = lib()
     need = L.qmoe_tokens_workspace_bytes(T, k, hidden, inter) if workspace is None else 0
     st, wp, wb, _ = _stream_and_workspace(need, workspace, x, stream)
