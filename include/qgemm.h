@@ -648,6 +648,8 @@ int qg_adamw_step(const qg_adamw_tensor *tensors_dev, int count, int64_t chunks,
  *   d_logprob    [rows] fp32;  d_entropy  [rows] fp32 or NULL (zeros)
  *   dX           [rows] rows of vocab values, lddx apart, x_dtype; may be X itself (with lddx = ldx)
  * A row whose two gradients are 0, or whose lse is -inf, gets zeros, whatever its logits.
+ * p_v is exp(z_v - lse[t]) of the lse that is given, which is fp32: the p of a row are off by one factor of up to exp(2^-24 |lse[t]|), 3% where lse is
+ * 800,000 and nothing where it is some hundreds. Rows that far from zero want their largest logit taken off first. A z past fp32's range has no gradient.
  * rows == 0 is a no-op in both; vocab 1 .. 2^28.
  */
 int qg_token_logprobs(const void *X, int x_dtype, int64_t ldx, const int64_t *targets, int rows, int vocab,
