@@ -413,12 +413,13 @@ __device__ __forceinline__ void fetch8(Raw &x, const Entry &t, int64_t e, int n)
 }
 
 // Two roots, rounded as fp32 has them but for a few in a million: a Newton step, s + (x - s s) / (2 sqrt(x)), from the approximate s = x / sqrt(x).
-// The product at the end is below every finite root and stands in where the step gives NaN: 0 below 2^-126 (which eps hides), infinity, NaN.
-// (56.5 million values with 8-bit states, clipped: 147 us; with the IEEE root, which is a dozen instructions and a branch, 205.)
+// The product at the end is below every root and stands in where the step gives NaN: of 0, infinity and NaN.
+// (56.5 million values with 8-bit states, clipped: 149 us, 147 were subnormal x to count as 0; with the IEEE root, which is a dozen instructions and
+// a branch, 205.)
 __device__ __forceinline__ float2 roots(float2 x) {
     float2 y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
     const float2 s = mul2(x, y), low = mul2(x, both(0x1p-65f));
     const float2 u = ffma2(ffma2(make_float2(-s.x, -s.y), s, x), mul2(y, both(0.5f)), s);
     return make_float2(fmaxf(u.x, low.x), fmaxf(u.y, low.y));

@@ -597,8 +597,8 @@ int qg_clip_grad_norm(const qg_grad_tensor *tensors_dev, int count, int64_t chun
  *               infinite or NaN leaves every tensor as it was.
  *   norm_dev    fp32, device: the norm before clipping, or NULL
  *   workspace   at least qg_adamw_step_workspace_bytes(chunks) bytes, 16-byte aligned (with clipping; else NULL will do)
- * Sums of the norm as in qg_clip_grad_norm.  A v' below 2^-126 counts as 0 in the step's quotient, which eps is meant to be far
- * above.  Deterministic.
+ * Sums of the norm as in qg_clip_grad_norm.  eps is meant to be far above the root of a v' that fp32 has few bits of (2^-126 and less).
+ * Deterministic.
  *
  * qg_adamw_list_init -- checks a host array and fills in first_chunk; *chunks receives the number of chunks.  Pointers
  * have their type's alignment (any address for codes); numel may be 0, with NULL pointers.  Host only.
