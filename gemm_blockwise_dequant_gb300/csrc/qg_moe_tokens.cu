@@ -141,7 +141,8 @@ cudaError_t moe_tokens(const MoeTokens &q, void *ws, cudaStream_t s) {
     a.K = q.inter;
     a.out = o;
     a.status = nullptr;
-    // h is fp32: one fp16 of it is off by as much as the rounding of an fp16 y, which two are not; beside that of a bf16 y it is nothing
+    // h is fp32: one fp16 of it is off by as much as the rounding of an fp16 y, which two are not; beside that of a bf16 y it is
+    // little (1.666e-3 instead of 1.656e-3 from fp64; two terms take 64 tokens from 460 to 478 us)
     a.terms = q.y_dtype == QG_BF16 ? 1 : 2;
     e = experts(a, s);
     if (e != cudaSuccess) return e;

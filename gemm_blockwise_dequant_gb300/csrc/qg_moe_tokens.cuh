@@ -18,8 +18,8 @@
 // tiles, so that few of them still fill the warps.  A tile of fc1 is 8 gate rows and their 8 up rows: both values of an
 // output meet in one lane.
 //
-// Measured (128 experts, top 8, 2880 x 2880, 4 bits in blocks of 32; the whole layer): 64 tokens 448 us, 1.87 GB of weights at
-// 4.2 TB/s, of which the copies alone, in pieces of 128 bytes, take 396; 2 tokens 77 us.
+// Measured (128 experts, top 8, 2880 x 2880, 4 bits in blocks of 32; the whole layer): 64 tokens 448 us, 1.76 GB of weights at
+// 3.9 TB/s, of which the copies alone, in pieces of 128 bytes through two stages, take 396; 2 tokens 76 us.
 #pragma once
 
 #include <algorithm>
@@ -204,7 +204,7 @@ __device__ __forceinline__ int rows_of(const Plan &p, uint32_t group, int limit)
 
 // This CTA's tiles, num[2] .. num[3] - 1 of all groups' in a row: equal shares, where a tile of a group of two columns
 // (more than eight rows) counts for kWide / kNarrow of another: with shares of as many tiles each, the CTA with most rows was
-// done 26% after the others (64 tokens, 128 experts, top 8, 2880 x 2880: the layer took 541 us, and 446 us this way).
+// done 26% after the others (64 tokens, 128 experts, top 8, 2880 x 2880, the one layer it was measured on: 541 us, and 446 us this way).
 constexpr int kNarrow = 3, kWide = 4;
 __device__ __forceinline__ void take_share(const Plan &p, int per) {
     const int groups = p.num[0], all = kNarrow * groups + (kWide - kNarrow) * p.num[1];
