@@ -24,3 +24,14 @@ def test_small_gradients(state, eps):
     assert ((p.double() - want).abs() <= 2.0 ** -20 * want.abs()).all()
     if state == "f32":
         assert torch.equal(t.exp_avg_sq[0], v)
+
+
+def test_a_second_moment_below_zero_has_no_root():
+    """Of a state that something spoiled: it shows in its own parameter and nowhere else."""
+    g, m, v = torch.zeros(5000, device="cuda"), torch.full((5000,), 1e-3, device="cuda"), torch.full((5000,), 1e-6, device="cuda")
+    v[7], v[4999], v[2000] = -1e-6, -1e-30, -0.0
+    p = torch.ones(5000, device="cuda")
+    t = qg.QGAdamWList([p], [g], exp_avg=[m], exp_avg_sq=[v])
+    qg.qg_adamw_step(t, lr=LR, step=1, betas=BETAS)
+    assert p.isnan().nonzero().flatten().tolist() == [7, 4999]
+    assert float(p[2000]) < -1  # m' over eps
